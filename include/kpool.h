@@ -308,6 +308,108 @@ kpool_status kpool_select_rows_ex(const void* q, const float* w, const int32_t* 
                                   const kpool_options* options);
 
 /*
+ * Attention around the selection. Three operators share one formula over
+ * different sets of visible keys. For a query row with visible keys J, query
+ * head h and its key head h / (q_heads / kv_heads):
+ *     s[j] = scale * q[h] . k[j]
+ *     out[h] = sum_J exp(s[j]) v[j] / sum_J exp(s[j]),   lse[h] = log sum_J exp(s[j])
+ * A row that sees no key, or whose every visible score is -INFINITY, gets
+ * out = 0 and lse = -INFINITY. What a key that a row does not see holds
+ * (infinities and NaN included) does not reach that row. Scores, weights' sums
+ * and outputs are kept in fp32; with bf16 inputs the weights are rounded to bf16
+ * for the product with v, and out is rounded once.
+ *
+ * Heads: q_heads is a multiple of kv_heads, the quotient at most 128.
+ * head_dim <= 256 and a multiple of 16 bytes. scale is finite and > 0.
+ *
+ * Workspace (256-byte aligned, kpool_attention_workspace_bytes bytes) for every
+ * one of them; what the device finds wrong with cu_seqlens, prefix or row_seq
+ * is recorded there as KPOOL_ERR_INVALID_ARG (kpool_last_device_error): a
+ * sequence or row with an out-of-range prefix or sequence id gets out = 0 and
+ * lse = -INFINITY; with malformed cumulative lengths the outputs' values are
+ * unspecified, and nothing outside the given arrays is read or written.
+ * The calls allocate and synchronise nothing and can be captured into a graph.
+ */
+
+/* A [tokens, heads, head_dim] tensor on the device: element (t, h, c) is at
+ * data + t * token_stride + h * head_stride + c (strides in elements, positive).
+ * data and both strides are multiples of 16 bytes, so a cache may keep its heads
+ * apart ([heads, tokens, head_dim]) or lie beside another tensor in one row. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kpool_heads;
+
+typedef struct {
+  int32_t q_heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;    /* a kpool_dtype: q, k, v and out */
+  float scale;
+  int32_t reserved; /* must be zero */
+} kpool_attention_shape;
+
+/* Workspace size for q_rows query rows of num_seqs sequences; 0 for shapes the calls reject. */
+size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_attention_shape* shape);
+
+/*
+ * Causal attention of a packed batch: sequence b's query rows
+ * [cu_q[b], cu_q[b+1]) are the last ones of its key tokens [cu_k[b], cu_k[b+1]):
+ * row i of nq sees the keys j <= i + (nk - nq). Equal lengths are a whole prompt; more
+ * keys than rows a later chunk of one (or, with one row, a decode step); with
+ * fewer keys than rows the first rows see nothing.
+ *   q, out      [q_rows, q_heads, head_dim];  k, v  [k_tokens, kv_heads, head_dim]
+ *   cu_q, cu_k  [num_seqs + 1] int32 (device), from 0 to q_rows / k_tokens
+ *   out_lse     [q_rows, q_heads] fp32 or NULL
+ *   options     NULL, or a score_kernel (KPOOL_SCORE_TC: bf16, head_dim 64 or 128) with
+ *               every other field zero
+ */
+kpool_status kpool_attention_prompt(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
+                                    const int32_t* cu_q, const int32_t* cu_k, int32_t num_seqs, int64_t q_rows,
+                                    int64_t k_tokens, const kpool_attention_shape* shape, const kpool_heads* out,
+                                    float* out_lse, void* workspace, size_t workspace_bytes, void* stream,
+                                    const kpool_options* options);
+
+/*
+ * Attention of drafted tokens over a cache. Sequence b owns the cache tokens
+ * [cu_k[b], cu_k[b+1]), holds prefix[b] committed keys and, right after them, the
+ * keys of its n = cu_q[b+1] - cu_q[b] drafted nodes (prefix[b] + n must fit). Node i
+ * (query row cu_q[b] + i) sees every committed key and the nodes its mask names:
+ *   mask   [q_rows, mask_words] int32 (device): bit j % 32 of word j / 32 of a
+ *          row is set when that row sees node j of its sequence (its ancestors and
+ *          itself); bits at n and beyond are ignored, nodes past 32 * mask_words
+ *          are seen by no row.
+ *          NULL (mask_words = 0): a chain, node i sees the nodes j <= i; with one
+ *          node per sequence that is an ordinary decode step.
+ * The cache beyond prefix[b] + n is not read into any result. Other arguments as above.
+ */
+kpool_status kpool_attention_tree(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
+                                  const int32_t* cu_q, const int32_t* cu_k, const int32_t* prefix,
+                                  const int32_t* mask, int32_t mask_words, int32_t num_seqs, int64_t q_rows,
+                                  int64_t k_tokens, const kpool_attention_shape* shape, const kpool_heads* out,
+                                  float* out_lse, void* workspace, size_t workspace_bytes, void* stream,
+                                  const kpool_options* options);
+
+/*
+ * Attention over selected tokens: row r sees the keys token_ids[r, 0..width) of its
+ * sequence, as kpool_select / kpool_select_rows leave them (width = index_topk +
+ * kpool, sequence-local ids, -1 where empty). An id outside [0, L_b) is not seen; an id
+ * that appears twice counts twice. The order of the ids does not matter but for
+ * rounding.
+ *   token_ids  [q_rows, width] int32 (device)
+ *   row_seq    [q_rows] int32 (device): the row's sequence, as for kpool_select_rows; or
+ *              NULL when the query rows are the key tokens' own (q_rows = k_tokens,
+ *              as for kpool_select): row r is then of the sequence that holds token r.
+ */
+kpool_status kpool_attention_selected(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
+                                      const int32_t* token_ids, int32_t width, const int32_t* row_seq,
+                                      const int32_t* cu_k, int32_t num_seqs, int64_t q_rows, int64_t k_tokens,
+                                      const kpool_attention_shape* shape, const kpool_heads* out, float* out_lse,
+                                      void* workspace, size_t workspace_bytes, void* stream,
+                                      const kpool_options* options);
+
+/*
  * Synchronises `stream`, then reads the device error word the last call on this
  * workspace recorded: KPOOL_OK, KPOOL_ERR_INVALID_ARG (malformed cu_seqlens),
  * KPOOL_ERR_DEVICE_TIMEOUT (a bounded wait ran out), KPOOL_ERR_INTERNAL (a

@@ -70,6 +70,9 @@ __global__ void wait_selftest_kernel(WorkspaceHeader* hdr, int64_t spin_limit) {
 
 }  // namespace
 
+bool note_cuda_error(cudaError_t e) { return cuda_ok(e); }
+cudaError_t device_sm_count(int* out) { return sm_count(out); }
+
 cudaError_t launch_wait_selftest(char* ws, int64_t spin_limit, cudaStream_t stream) {
   wait_selftest_kernel<<<1, 32, 0, stream>>>(reinterpret_cast<WorkspaceHeader*>(ws), spin_limit);
   return cudaGetLastError();

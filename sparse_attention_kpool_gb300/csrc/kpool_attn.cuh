@@ -1,0 +1,155 @@
+// kpool_attn.cuh -- shared pieces of the attention entry points: the call's
+// parameters, which keys a row sees, the row tiles of a packed batch, and the
+// launch wrappers of the kernel families.
+//
+// All three operators are one formula over different sets of visible keys:
+//   s[j] = scale * q . k[j],  out = sum_J exp(s[j]) v[j] / sum_J exp(s[j]),
+//   lse = log sum_J exp(s[j]);  no visible key: out = 0, lse = -inf.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kpool_internal.cuh"
+
+namespace kpool {
+
+enum AttnMode { kAttnPrompt = 0, kAttnTree = 1, kAttnSelected = 2 };
+
+struct AttnParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;                                // [R, Hq] or null
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;  // token / head strides, elements
+  const int32_t* cu_q;                       // [S + 1] query rows (prompt, tree)
+  const int32_t* cu_k;                       // [S + 1] key tokens
+  const int32_t* prefix;                     // [S] committed keys (tree)
+  const int32_t* mask;                       // [R, mask_words] or null (tree)
+  const int32_t* ids;                        // [R, width] (selected)
+  const int32_t* row_seq;                    // [R] or null (selected)
+  int32_t mask_words, width;
+  int32_t S, R;
+  int64_t T;
+  int32_t Hq, Hkv, G, D;
+  float scale;
+  AttnMode mode;
+};
+
+// Query rows, keys and committed prefix of one sequence, clipped so that nothing
+// read through them leaves the call's arrays whatever the arrays hold. `ok` is
+// false when the sequence's entries are malformed: its rows then get zeros.
+struct AttnSeq {
+  int32_t q0, nq;     // first query row and their number
+  int32_t k0, nk;     // first key token and the keys that exist for some row
+  int32_t prefix;     // row i sees keys < prefix (+ i + 1 when causal); may be negative (prompt)
+  bool ok;
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
+  AttnSeq s;
+  s.q0 = __ldg(p.cu_q + b);
+  const int64_t q1 = __ldg(p.cu_q + b + 1);
+  s.k0 = __ldg(p.cu_k + b);
+  const int64_t k1 = __ldg(p.cu_k + b + 1);
+  s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= p.R && s.k0 >= 0 && k1 >= s.k0 && k1 <= p.T;
+  if (!s.ok) {
+    // rows inside the call's range still get their zeros
+    s.q0 = max(0, min(s.q0, p.R));
+    s.nq = int32_t(max(int64_t(0), min(q1, int64_t(p.R)) - s.q0));
+    s.k0 = s.nk = s.prefix = 0;
+    return s;
+  }
+  s.nq = int32_t(q1 - s.q0);
+  const int64_t extent = k1 - s.k0;
+  if (p.mode == kAttnTree) {
+    const int64_t pre = __ldg(p.prefix + b);
+    if (pre < 0 || pre + s.nq > extent) {
+      s.ok = false;
+      s.nk = s.prefix = 0;
+      return s;
+    }
+    s.prefix = int32_t(pre);
+    s.nk = s.prefix + s.nq;
+  } else {
+    s.prefix = int32_t(extent - s.nq);
+    s.nk = int32_t(extent);
+  }
+  return s;
+}
+
+// Does row i of the sequence (global query row q0 + i) see key j? (prompt, tree; j < nk)
+__device__ __forceinline__ bool attn_sees(const AttnParams& p, const AttnSeq& s, int i, int j) {
+  const int slot = j - s.prefix;
+  if (p.mask == nullptr) return slot <= i;
+  if (slot < 0) return true;
+  if (slot >= 32 * p.mask_words || slot >= s.nq) return false;
+  return (uint32_t(__ldg(p.mask + int64_t(s.q0 + i) * p.mask_words + (slot >> 5))) >> (slot & 31)) & 1u;
+}
+
+// Keys [0, end) hold every key that some row before i1 sees.
+__device__ __forceinline__ int attn_keys_end(const AttnParams& p, const AttnSeq& s, int i1) {
+  if (!s.ok || s.nk == 0) return 0;
+  if (p.mask != nullptr) return s.nk;
+  return int(max(int64_t(0), min(int64_t(s.nk), int64_t(s.prefix) + i1)));
+}
+
+// A packed batch is cut into tiles of `tt` query rows that do not cross sequences.
+// Sequence b's tiles are numbered from cu_q[b] / tt + b: a sequence of n rows has
+// ceil(n / tt) of them, at most floor(cu[b+1]/tt) - floor(cu[b]/tt) + 1, so the ranges
+// do not overlap, R / tt + S numbers cover all, and a binary search finds a number's
+// sequence without any scan or planning kernel; numbers without a tile are skipped.
+inline int64_t attn_tiles(int64_t R, int64_t S, int64_t tt) { return R / tt + S; }
+
+__device__ __forceinline__ int attn_seq_of_tile(const AttnParams& p, int tile, int tt) {
+  int lo = 0, hi = p.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(p.cu_q + mid) / tt + mid <= tile) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Every thread of one CTA of the grid: checks the device arrays of the whole call and
+// writes the header's error word (0 when all is well), so no kernel has to clear it.
+__device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader* hdr) {
+  int bad = 0;
+  for (int b = threadIdx.x; b <= p.S; b += blockDim.x) {
+    const int k = __ldg(p.cu_k + b);
+    if (b == 0 ? k != 0 : k < __ldg(p.cu_k + b - 1)) bad = 1;
+    if (b == p.S && k != p.T) bad = 1;
+    if (p.mode == kAttnSelected) continue;
+    const int q = __ldg(p.cu_q + b);
+    if (b == 0 ? q != 0 : q < __ldg(p.cu_q + b - 1)) bad = 1;
+    if (b == p.S && q != p.R) bad = 1;
+    if (p.mode == kAttnTree && b < p.S) {
+      const int64_t pre = __ldg(p.prefix + b);
+      const int64_t rows = int64_t(__ldg(p.cu_q + b + 1)) - q, extent = int64_t(__ldg(p.cu_k + b + 1)) - k;
+      if (pre < 0 || pre + rows > extent) bad = 1;
+    }
+  }
+  if (p.mode == kAttnSelected && p.row_seq != nullptr)
+    for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+      const int b = __ldg(p.row_seq + r);
+      if (b < 0 || b >= p.S) bad = 1;
+    }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) hdr->error = bad ? KPOOL_ERR_INVALID_ARG : KPOOL_OK;
+}
+
+// Key tokens of selected row r: first token and number (0 when the row has no valid sequence).
+__device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, int* k0, int* nk) {
+  int b = p.row_seq ? __ldg(p.row_seq + r) : seq_of_row(p.cu_k, p.S, r);
+  *k0 = *nk = 0;
+  if (b < 0 || b >= p.S) return;
+  const int lo = __ldg(p.cu_k + b), hi = __ldg(p.cu_k + b + 1);
+  if (lo < 0 || hi < lo || hi > p.T) return;
+  *k0 = lo;
+  *nk = hi - lo;
+}
+
+// CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
+cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
+
+}  // namespace kpool

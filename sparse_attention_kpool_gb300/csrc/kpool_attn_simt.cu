@@ -1,0 +1,225 @@
+// kpool_attn_simt.cu -- the attention operators on the CUDA cores: fp32 inputs at fp32
+// precision, and the head sizes the tensor-core kernels do not take.
+//
+// One CTA of 4 warps holds 16 (query row, head) pairs that share a key head and walks the
+// keys in blocks of 32 with the running maximum and sum of a softmax (one pass over K and
+// V, nothing written but the result). A lane scores one key for its warp's four rows, so a
+// 16-byte read of K from shared memory feeds 16 multiply-adds; for the second product a
+// lane owns 4 (or 8) channels and reads V the same way. K rows are padded by 16 bytes, which
+// spreads the lanes' 16-byte reads over all banks.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "kpool_attn.cuh"
+
+namespace kpool {
+namespace {
+
+constexpr int kVRows = 16;        // (row, head) pairs per CTA
+constexpr int kPerWarp = 4;
+constexpr int kThreadsSimt = 128;
+constexpr int kKeys = 32;         // keys per block: one per lane
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t*>(&a);
+  u.y = *reinterpret_cast<uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParams p, int gt, int tt,
+                                                                 WorkspaceHeader* hdr) {
+  extern __shared__ __align__(16) float smem[];
+  const int D = p.D, ldk = D + 4;
+  float* s_q = smem;                    // [kVRows][D]
+  float* s_k = s_q + kVRows * D;        // [kKeys][D + 4]
+  float* s_v = s_k + kKeys * ldk;       // [kKeys][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && blockIdx.y == 0) attn_check(p, hdr);
+
+  // the CTA's rows: tokens [i0, i1) of a sequence x heads [g0, g0 + gt) of key head hk
+  const int gb_n = (p.G + gt - 1) / gt;
+  const int hk = blockIdx.y / gb_n, g0 = (blockIdx.y % gb_n) * gt;
+  AttnSeq sq{};
+  int i0, i1, end;
+  const bool selected = p.mode == kAttnSelected;
+  const int32_t* ids = nullptr;
+  if (selected) {
+    const int r = blockIdx.x;
+    attn_selected_seq(p, r, &sq.k0, &sq.nk);
+    sq.q0 = 0;
+    i0 = r;
+    i1 = r + 1;
+    ids = p.ids + int64_t(r) * p.width;
+    end = sq.nk > 0 ? p.width : 0;
+  } else {
+    const int b = attn_seq_of_tile(p, blockIdx.x, tt);
+    sq = attn_seq(p, b);
+    i0 = (int(blockIdx.x) - (__ldg(p.cu_q + b) / tt + b)) * tt;
+    if (i0 < 0 || i0 >= sq.nq) return;
+    i1 = min(i0 + tt, sq.nq);
+    end = attn_keys_end(p, sq, i1);
+  }
+
+  const E* q = static_cast<const E*>(p.q);
+  const E* kk = static_cast<const E*>(p.k) + int64_t(hk) * p.k_hs;
+  const E* vv = static_cast<const E*>(p.v) + int64_t(hk) * p.v_hs;
+  const int chunks = D / 4;
+  for (int x = threadIdx.x; x < kVRows * chunks; x += kThreadsSimt) {
+    const int r = x / chunks, c = x % chunks, i = i0 + r / gt, g = g0 + r % gt;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r / gt < tt && i < i1 && g < p.G)
+      f = load4(q + int64_t(sq.q0 + i) * p.q_ts + int64_t(hk * p.G + g) * p.q_hs + 4 * c);
+    store4(s_q + r * D + 4 * c, f);
+  }
+
+  const float c2 = p.scale * kLog2e;
+  float m[kPerWarp], l[kPerWarp];
+  float4 o[kPerWarp][2];
+  int tok[kPerWarp];  // the warp's rows: token index, or -1 where the slot holds no row
+#pragma unroll
+  for (int r = 0; r < kPerWarp; ++r) {
+    const int vr = warp * kPerWarp + r;
+    const int i = i0 + vr / gt;
+    tok[r] = (vr / gt < tt && i < i1 && g0 + vr % gt < p.G) ? i : -1;
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+    o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+
+  for (int j0 = 0; j0 < end; j0 += kKeys) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < kKeys * chunks; x += kThreadsSimt) {
+      const int jj = x / chunks, c = x % chunks;
+      int64_t t = -1;
+      if (j0 + jj < end) {
+        const int id = selected ? __ldg(ids + j0 + jj) : j0 + jj;
+        if (id >= 0 && id < sq.nk) t = int64_t(sq.k0) + id;
+      }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if (t >= 0) {
+        a = load4(kk + t * p.k_ts + 4 * c);
+        b = load4(vv + t * p.v_ts + 4 * c);
+      }
+      store4(s_k + jj * ldk + 4 * c, a);
+      store4(s_v + jj * D + 4 * c, b);
+    }
+    __syncthreads();
+
+    float s[kPerWarp] = {0.f, 0.f, 0.f, 0.f};
+    const float* kr = s_k + lane * ldk;
+    const float* qr = s_q + warp * kPerWarp * D;
+    for (int c = 0; c < D; c += 4) {
+      const float4 a = load4(kr + c);
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r) {
+        const float4 b = load4(qr + r * D + c);
+        s[r] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[r]))));
+      }
+    }
+    const int j = j0 + lane;
+    bool in = j < end;
+    if (selected && in) {
+      const int id = __ldg(ids + j);
+      in = id >= 0 && id < sq.nk;
+    }
+    unsigned seen[kPerWarp];
+    float pr[kPerWarp];
+#pragma unroll
+    for (int r = 0; r < kPerWarp; ++r) {
+      const bool see = tok[r] >= 0 && in && (selected || attn_sees(p, sq, tok[r], j));
+      seen[r] = __ballot_sync(0xffffffffu, see);
+      const float x = see ? s[r] * c2 : -INFINITY;
+      float mx = x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mx = fmaxf(mx, m[r]);
+      const float base = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every weight below is exp2(-inf) = 0
+      const float f = exp2f(m[r] - base);
+      pr[r] = exp2f(x - base);
+      float sum = pr[r];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[r] = fmaf(l[r], f, sum);
+      m[r] = mx;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        o[r][h].x *= f;
+        o[r][h].y *= f;
+        o[r][h].z *= f;
+        o[r][h].w *= f;
+      }
+    }
+    const int n = min(kKeys, end - j0);
+    for (int jj = 0; jj < n; ++jj) {
+      float w[kPerWarp];
+#pragma unroll
+      for (int r = 0; r < kPerWarp; ++r) w[r] = __shfl_sync(0xffffffffu, pr[r], jj);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = h * 128 + lane * 4;
+        if (c >= D) break;
+        const float4 b = load4(s_v + jj * D + c);
+#pragma unroll
+        for (int r = 0; r < kPerWarp; ++r)
+          if ((seen[r] >> jj) & 1u) {  // a key the row does not see adds nothing, whatever its value holds
+            o[r][h].x = fmaf(w[r], b.x, o[r][h].x);
+            o[r][h].y = fmaf(w[r], b.y, o[r][h].y);
+            o[r][h].z = fmaf(w[r], b.z, o[r][h].z);
+            o[r][h].w = fmaf(w[r], b.w, o[r][h].w);
+          }
+      }
+    }
+  }
+
+  E* out = static_cast<E*>(p.out);
+#pragma unroll
+  for (int r = 0; r < kPerWarp; ++r) {
+    if (tok[r] < 0) continue;
+    const int64_t row = sq.q0 + tok[r];
+    const int head = hk * p.G + g0 + (warp * kPerWarp + r) % gt;
+    const bool none = m[r] == -INFINITY && l[r] == 0.f;  // (a NaN score leaves l NaN: not empty)
+    const float inv = none ? 0.f : 1.f / l[r];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h * 128 + lane * 4;
+      if (c >= D) break;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!none) f = make_float4(o[r][h].x * inv, o[r][h].y * inv, o[r][h].z * inv, o[r][h].w * inv);
+      store4(out + row * p.o_ts + int64_t(head) * p.o_hs + c, f);
+    }
+    if (lane == 0 && p.lse) p.lse[row * p.Hq + head] = none ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
+  // heads of a group share the CTA's key blocks; what is left of the 16 slots takes more tokens
+  const int gt = p.G < kVRows ? p.G : kVRows;
+  const int tt = p.mode == kAttnSelected ? 1 : kVRows / gt;
+  const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles(p.R, p.S, tt);
+  const size_t smem = sizeof(float) * (size_t(kVRows) * p.D + size_t(kKeys) * (p.D + 4) + size_t(kKeys) * p.D);
+  const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
+  WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
+  auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreadsSimt, smem, stream>>>(p, gt, tt, hdr);
+    return cudaGetLastError();
+  };
+  return dtype == KPOOL_BF16 ? go(attn_simt_kernel<__nv_bfloat16>) : go(attn_simt_kernel<float>);
+}
+
+}  // namespace kpool

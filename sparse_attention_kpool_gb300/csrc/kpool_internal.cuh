@@ -189,6 +189,12 @@ kpool_status select_check_args(const void* q, const void* kin, const float* w, c
 // unavailable or rejects the arguments (base not 16-byte aligned, too many rows).
 bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
 
+// Remembers a failing CUDA call of this thread for kpool_last_cuda_error; true on success.
+bool note_cuda_error(cudaError_t e);
+
+// SM count of the current device (looked up once per device).
+cudaError_t device_sm_count(int* out);
+
 // Bounded-wait self test.
 cudaError_t launch_wait_selftest(char* ws, int64_t spin_limit, cudaStream_t stream);
 

@@ -41,6 +41,7 @@ EXPORTED = (
     "kpool_select_static_scratch", "kpool_rows_workspace_bytes", "kpool_select_rows", "kpool_select_rows_ex",
     "kpool_pool_keys_gated", "kpool_select_pooled", "kpool_static_scratch_last_device_error",
     "kpool_balanced_row_split", "kpool_index_scores", "kpool_index_scores_pooled",
+    "kpool_attention_workspace_bytes", "kpool_attention_prompt", "kpool_attention_tree", "kpool_attention_selected",
 )
 KPOOL_STATIC_SCRATCH_BYTES = 48 << 20
 
@@ -59,6 +60,15 @@ class kpool_options(ctypes.Structure):
     _fields_ = [("score_kernel", ctypes.c_int32), ("max_ctas", ctypes.c_int32),
                 ("stage_events", ctypes.POINTER(ctypes.c_void_p)), ("row_begin", ctypes.c_int32),
                 ("row_end", ctypes.c_int32), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class kpool_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class kpool_attention_shape(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -121,6 +131,17 @@ def load() -> ctypes.CDLL:
         lib.kpool_index_scores.restype = i32
         lib.kpool_index_scores_pooled.argtypes = isc
         lib.kpool_index_scores_pooled.restype = i32
+        HP, SP, OP = (ctypes.POINTER(kpool_heads), ctypes.POINTER(kpool_attention_shape),
+                      ctypes.POINTER(kpool_options))
+        lib.kpool_attention_workspace_bytes.argtypes = [i64, i32, SP]
+        lib.kpool_attention_workspace_bytes.restype = sz
+        tail = [i32, i64, i64, SP, HP, P, P, sz, P, OP]
+        lib.kpool_attention_prompt.argtypes = [HP, HP, HP, P, P] + tail
+        lib.kpool_attention_prompt.restype = i32
+        lib.kpool_attention_tree.argtypes = [HP, HP, HP, P, P, P, P, i32] + tail
+        lib.kpool_attention_tree.restype = i32
+        lib.kpool_attention_selected.argtypes = [HP, HP, HP, P, i32, P, P] + tail
+        lib.kpool_attention_selected.restype = i32
         _lib = lib
         return lib
 
@@ -451,6 +472,113 @@ def kpool_index_scores(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, cu_seq
     if st != KPOOL_OK:
         raise KpoolError(st, "kpool_index_scores")
     return out
+
+
+def _attention_shape(hq, hkv, d, dtype, scale):
+    code = {torch.bfloat16: KPOOL_BF16, torch.float32: KPOOL_F32}.get(dtype)
+    if code is None:
+        raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
+    return kpool_attention_shape(hq, hkv, d, code, scale, 0)
+
+
+def new_attention_workspace(q_rows: int, num_seqs: int, q_heads: int, kv_heads: int, head_dim: int, dtype,
+                            device=None) -> torch.Tensor:
+    """Workspace of the kpool_attention_* calls with up to these sizes (dtype: the torch dtype of q)."""
+    n = int(load().kpool_attention_workspace_bytes(q_rows, num_seqs, ctypes.byref(
+        _attention_shape(q_heads, kv_heads, head_dim, dtype, 1.0))))
+    if n == 0:
+        raise KpoolError(KPOOL_ERR_INVALID_ARG, "kpool_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def _heads(t: torch.Tensor, what: str) -> kpool_heads:
+    n, h, d = t.shape
+    ts, hs, ds = t.stride()
+    if not t.is_cuda or (ds != 1 and d > 1):
+        raise ValueError(f"{what} must be a CUDA tensor whose last dimension is contiguous")
+    # the stride of a dimension of one element carries no meaning in torch
+    return kpool_heads(t.data_ptr(), ts if n > 1 else d, hs if h > 1 else d)
+
+
+def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse, workspace, stream, score_kernel):
+    """Marshals one kpool_attention_* call: `arrays` are its arguments between v and num_seqs."""
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or q.shape[2] != k.shape[2]:
+        raise ValueError("q is [rows, q_heads, head_dim]; k and v are [tokens, kv_heads, head_dim] alike")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("k and v must match q's dtype")
+    R, hq, d = q.shape
+    if out is None:
+        out = torch.empty((R, hq, d), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise TypeError("out must have q's shape and dtype")
+    if out_lse is None:
+        if return_lse:
+            out_lse = torch.empty((R, hq), dtype=torch.float32, device=q.device)
+    elif out_lse.dtype != torch.float32 or out_lse.shape != (R, hq):
+        raise TypeError("out_lse must be float32 [rows, q_heads]")
+    shape = _attention_shape(hq, k.shape[1], d, q.dtype, scale)
+    if workspace is None:
+        workspace = new_attention_workspace(R, num_seqs, hq, k.shape[1], d, q.dtype, q.device)
+    args = []
+    for a in arrays:
+        if torch.is_tensor(a):
+            if a.dtype != torch.int32:
+                raise TypeError("cumulative lengths, prefix, mask, token ids and row_seq are int32")
+            _check_cuda(a)
+            args.append(a.data_ptr())
+        else:
+            args.append(a)
+    _check_cuda(out_lse, workspace)
+    st = getattr(load(), name)(_heads(q, "q"), _heads(k, "k"), _heads(v, "v"), *args, num_seqs, R, k.shape[0], shape,
+                               _heads(out, "out"), None if out_lse is None else out_lse.data_ptr(),
+                               workspace.data_ptr(), workspace.numel(), _stream(stream),
+                               None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
+    if st != KPOOL_OK:
+        raise KpoolError(st, name)
+    return out, out_lse
+
+
+def kpool_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                           cu_k: torch.Tensor, scale: float, out=None, return_lse: bool = False, out_lse=None,
+                           workspace=None, stream=None, score_kernel: int = KPOOL_SCORE_AUTO):
+    """Causal attention of a packed batch with grouped heads: q [R,Hq,D], k and v [T,Hkv,D] (bf16 or
+    fp32; any token and head strides), cu_q and cu_k [S+1] int32 -> (out [R,Hq,D], lse [R,Hq] fp32 or
+    None). Sequence b's query rows are the last ones of its keys: row i of nq sees keys j <= i + nk - nq."""
+    if cu_q.numel() != cu_k.numel():
+        raise ValueError("cu_q and cu_k must have the same length")
+    return _attention("kpool_attention_prompt", q, k, v, (cu_q, cu_k), cu_k.numel() - 1, scale, out, return_lse,
+                      out_lse, workspace, stream, score_kernel)
+
+
+def kpool_attention_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                         prefix: torch.Tensor, scale: float, mask=None, out=None, return_lse: bool = False,
+                         out_lse=None, workspace=None, stream=None, score_kernel: int = KPOOL_SCORE_AUTO):
+    """Attention of drafted nodes (or single decode tokens) over a cache: sequence b owns the cache
+    tokens [cu_k[b], cu_k[b+1]), has prefix[b] committed keys and then the keys of its nodes, the query
+    rows [cu_q[b], cu_q[b+1]). mask [R, words] int32 names the nodes each row sees by bits; None is a
+    chain (node i sees nodes j <= i). Returns (out, lse) as kpool_attention_prompt does."""
+    S = cu_k.numel() - 1
+    if cu_q.numel() != S + 1 or prefix.numel() != S:
+        raise ValueError("cu_q needs cu_k's length, prefix one element per sequence")
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] != q.shape[0] or mask.shape[1] < 1):
+        raise ValueError("mask is [rows, words] with at least one word")
+    return _attention("kpool_attention_tree", q, k, v,
+                      (cu_q, cu_k, prefix, mask, 0 if mask is None else mask.shape[1]), S, scale, out, return_lse,
+                      out_lse, workspace, stream, score_kernel)
+
+
+def kpool_attention_selected(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, token_ids: torch.Tensor,
+                             cu_k: torch.Tensor, scale: float, row_seq=None, out=None, return_lse: bool = False,
+                             out_lse=None, workspace=None, stream=None, score_kernel: int = KPOOL_SCORE_AUTO):
+    """Attention of each row over its selected tokens: token_ids [R, width] int32 as kpool_select or
+    kpool_select_rows return them (sequence-local, -1 where empty), row_seq [R] int32 the rows' sequences
+    (None: query row r belongs to key token r). Returns (out, lse) as kpool_attention_prompt does."""
+    if token_ids.dim() != 2 or token_ids.shape[0] != q.shape[0]:
+        raise ValueError("token_ids is [rows, width]")
+    if row_seq is not None and row_seq.numel() != q.shape[0]:
+        raise ValueError("row_seq needs one element per row")
+    return _attention("kpool_attention_selected", q, k, v, (token_ids, token_ids.shape[1], row_seq, cu_k),
+                      cu_k.numel() - 1, scale, out, return_lse, out_lse, workspace, stream, score_kernel)
 
 
 def kpool_balanced_row_split(cu_seqlens, kpool: int, parts: int, row_weight: int = 0) -> list:
