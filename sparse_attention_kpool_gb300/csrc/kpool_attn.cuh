@@ -149,6 +149,24 @@ __device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, in
   *nk = hi - lo;
 }
 
+// Runs of the persistent tensor-core form: CTAs, sequences it takes, row tiles per SM from
+// which one CTA per row tile is used instead, and the rows of one partial result.
+constexpr int kAttnMaxRuns = 152;
+constexpr int kAttnMaxRunSeqs = 8192;
+constexpr int kAttnDirectItems = 6;
+inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
+  const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned
+  return int(rows < tile_rows ? rows : tile_rows);
+}
+// Partial results of the persistent form: two per run, [rows][D] fp32 and (m, l) per row.
+inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
+  return size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
+}
+
+// Tensor-core kernel of prompt and tree attention: bf16, head_dim 64 or 128, at least one key token.
+bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
+cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
+
 // CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
 

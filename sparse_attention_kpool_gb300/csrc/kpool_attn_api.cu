@@ -47,7 +47,9 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
     return KPOOL_ERR_INVALID_ARG;
   const int32_t group = shape->q_heads / shape->kv_heads;
   if (shape->head_dim > 256 || group > 128 || shape->q_heads > 4096) return KPOOL_ERR_UNSUPPORTED;
-  if (opt.score_kernel == KPOOL_SCORE_TC) return KPOOL_ERR_UNSUPPORTED;
+  const kpool_dtype dtype = kpool_dtype(shape->dtype);
+  const bool tc_ok = p.mode != kAttnSelected && attn_tc_supported(dtype, shape->head_dim);
+  if (opt.score_kernel == KPOOL_SCORE_TC && !tc_ok) return KPOOL_ERR_UNSUPPORTED;
   if (q_rows == 0) return KPOOL_OK;
   if (!heads_ok(q, *shape) || !heads_ok(out, *shape)) return KPOOL_ERR_INVALID_ARG;
   // with no key token there is nothing to point at
@@ -80,9 +82,10 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
   p.G = group;
   p.D = shape->head_dim;
   p.scale = shape->scale;
-  const kpool_dtype dtype = kpool_dtype(shape->dtype);
-  const cudaError_t e = launch_attn_simt(p, dtype, static_cast<char*>(workspace),
-                                         static_cast<cudaStream_t>(stream_ptr));
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  const bool tc = tc_ok && k_tokens > 0 && opt.score_kernel != KPOOL_SCORE_SIMT;
+  const cudaError_t e = tc ? launch_attn_tc(p, ws, stream) : launch_attn_simt(p, dtype, ws, stream);
   return note_cuda_error(e) ? KPOOL_OK : KPOOL_ERR_CUDA;
 }
 
@@ -95,7 +98,10 @@ extern "C" {
 
 size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_attention_shape* shape) {
   if (!shape_ok(shape) || !sizes_ok(q_rows, 0, num_seqs)) return 0;
-  return sizeof(WorkspaceHeader);
+  size_t bytes = sizeof(WorkspaceHeader);
+  if (attn_tc_supported(kpool_dtype(shape->dtype), shape->head_dim))
+    bytes += attn_partial_bytes(q_rows, shape->q_heads / shape->kv_heads, shape->head_dim);
+  return bytes;
 }
 
 kpool_status kpool_attention_prompt(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,

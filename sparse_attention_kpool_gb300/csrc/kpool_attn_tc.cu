@@ -1,0 +1,943 @@
+// kpool_attn_tc.cu -- prompt and tree attention on the 5th-generation tensor cores (bf16,
+// head_dim 64 or 128): one pass over K and V with the running maximum and sum of a softmax.
+//
+// Rows. The G query heads that share a key head and TT = 128 / G tokens fill the 128 rows of
+// an MMA (row = token * G + head of the group), so a K/V tile read once serves all of them,
+// decode steps of one token included. A CTA holds two such row tiles ("two", 2 * TT tokens that
+// share every K/V tile) or, where sequences have fewer rows, one tile whose K/V tiles alternate
+// between the two softmax groups ("one": each group keeps its own accumulator and statistics,
+// added up at the end).
+//
+// Roles (12 warps): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread per row; warp 8
+// loads by TMA; warp 9 issues the MMAs and owns TMEM; warps 10-11 clean V tiles (below). Per
+// 128-key tile of a group: S = Q K^T (128 x 128, fp32 in TMEM); its thread reads the row, takes
+// the maximum, writes P = 2^(c s - c m) as bf16 over S in TMEM and adds its fp32 sum; O += P V
+// with P read from TMEM. The tensor core works on one group while the other does its softmax.
+// K and V share one ring of tiles in the order in which the MMAs consume them.
+//
+// Running maximum. O is rescaled only when a row's maximum has grown by more than 8 in the
+// exponent: weights then reach at most 2^8, which costs neither bf16 nor fp32 any precision,
+// and the rescale (a pass over O in TMEM) becomes rare. P is rounded to bf16 (half a step is
+// 2^-8 of a weight) because the second product takes bf16; the row sum adds the weights before
+// that rounding, in fp32.
+//
+// Masked places. A key that a row does not see gets s = -inf, so what K holds there does not
+// matter. A weight of zero does not silence V, though (0 * NaN): in the tiles that some row
+// does not see entirely, warps 10-11 first overwrite V rows past the last visible key with
+// zeros, replace every other infinity or NaN by zero and raise a flag; rows that do see such
+// a value add it in the epilogue.
+//
+// Work. A pass over (sequence, key head, row tile, K/V tile). Many row tiles: one CTA each,
+// the deepest first. Few: a persistent CTA per SM takes an equal run of all K/V tiles of the
+// call (found by every CTA itself from the lengths on the device), unfinished rows go to the
+// workspace as (m, l, O) and a second kernel joins them in order, so results repeat bit for bit.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "kpool_attn.cuh"
+#include "kpool_ptx.cuh"
+
+namespace kpool {
+namespace {
+
+constexpr int kThreadsTc = 384;
+constexpr int kTileKeys = 128;
+constexpr int kTileRows = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
+constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are microseconds
+constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
+
+template <int D, bool TWO>
+struct Cfg {
+  static constexpr int kTileBytes = kTileKeys * D * 2;   // one K or V tile, one Q tile
+  static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kQTiles = TWO ? 2 : 1;
+  static constexpr int kStages = D == 64 ? 8 : (TWO ? 5 : 6);
+  static constexpr int kOffRing = kQTiles * kTileBytes;
+  static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
+  // full[stages] empty[stages] clean[stages] dirty[stages] q_full q_empty s_full[2] p_ready[2] o_final o_free done
+  // seg_full[ring] seg_empty[ring]
+  static constexpr int kNumBars = 4 * kStages + 9 + 2 * kSegRing;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr int kOffSeg = kOffMisc + 64;
+  static constexpr int kOffStat = kOffSeg + 64 * kSegRing;         // [2][128] float2 (m, l), one-tile form only
+  static constexpr int kSmem = kOffStat + (TWO ? 0 : 2 * kTileRows * 8);
+  static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
+};
+
+struct Misc {
+  int64_t base;       // persistent form: first position of sequence b
+  int64_t lo, hi;     // positions of this CTA
+  int64_t total;
+  int32_t b;
+  uint32_t tmem;
+  volatile int32_t abort;
+  volatile int32_t bad_seg[kSegRing];  // 1 + the last segment of this slot with an infinity or NaN in a cleaned V tile
+};
+static_assert(sizeof(Misc) <= 64, "Misc fits its space");
+
+// ------------------------------------------------------------------ work segments
+
+struct Seg {
+  AttnSeq sq;
+  int hk, tok0;
+  int kt0, n;      // first K/V tile of this CTA and their number (0: no row sees a key; -1: the work is done)
+  int n0;          // tiles that the first row tile needs (two)
+  int end;         // keys that some row sees
+  int all;         // keys that every row sees
+  int8_t whole;    // no other CTA has tiles of these rows
+  int8_t slot;     // partial slot of the CTA (0: the run's first segment, 1: a later one)
+};
+static_assert(sizeof(Seg) <= 64, "Seg fits its space");
+
+__device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, int t, int ttb) {
+  const int end = attn_keys_end(p, s, min((t + 1) * ttb, s.nq));
+  return max(1, (end + kTileKeys - 1) / kTileKeys);
+}
+
+__device__ __forceinline__ int64_t seq_cost(const AttnParams& p, const AttnSeq& s, int ttb) {
+  int64_t c = 0;
+  for (int t = 0; t * ttb < s.nq; ++t) c += tile_cost(p, s, t, ttb);
+  return c * p.Hkv;
+}
+
+// The segments of a CTA. Positions number the K/V tiles of the call: by sequence, key
+// head, row tile, then key tile; a row tile without any key counts as one.
+struct SegIter {
+  int64_t pos, hi, lo, base, cost;
+  int b;
+  AttnSeq sq;
+
+  __device__ __forceinline__ void start(const AttnParams& p, const Misc* m, int ttb) {
+    lo = pos = m->lo;
+    hi = m->hi;
+    base = m->base;
+    b = m->b;
+    if (pos < hi) {
+      sq = attn_seq(p, b);
+      cost = seq_cost(p, sq, ttb);
+    }
+  }
+  __device__ __forceinline__ bool next(const AttnParams& p, int ttb, Seg* s) {
+    if (pos >= hi) return false;
+    while (pos >= base + cost) {
+      base += cost;
+      ++b;
+      sq = attn_seq(p, b);
+      cost = seq_cost(p, sq, ttb);
+    }
+    const int64_t per_head = cost / p.Hkv;
+    s->sq = sq;
+    s->hk = int((pos - base) / per_head);
+    int64_t off = (pos - base) - s->hk * per_head;
+    int t = 0, c = tile_cost(p, sq, 0, ttb);
+    while (off >= c) {
+      off -= c;
+      c = tile_cost(p, sq, ++t, ttb);
+    }
+    s->tok0 = t * ttb;
+    s->kt0 = int(off);
+    s->n = int(min(int64_t(c) - off, hi - pos));
+    s->whole = s->n == c;
+    s->slot = pos == lo ? 0 : 1;
+    pos += s->n;
+    return true;
+  }
+};
+
+// One CTA per row tile: head by head (a head's K and V stay in L2), the deepest row tiles of each first.
+__device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int tiles, Seg* s) {
+  s->hk = blockIdx.x / tiles;
+  const int tile = tiles - 1 - int(blockIdx.x % tiles);
+  const int b = attn_seq_of_tile(p, tile, ttb);
+  s->sq = attn_seq(p, b);
+  s->tok0 = (tile - (__ldg(p.cu_q + b) / ttb + b)) * ttb;
+  if (s->tok0 < 0 || s->tok0 >= s->sq.nq) return false;
+  s->kt0 = 0;
+  s->n = tile_cost(p, s->sq, s->tok0 / ttb, ttb);
+  s->whole = 1;
+  s->slot = 0;
+  return true;
+}
+
+// The rest of a segment's fields; tt: tokens of a row tile, ttb: of all row tiles of the CTA.
+__device__ __forceinline__ void finish_seg(const AttnParams& p, int tt, int ttb, Seg* s) {
+  s->end = attn_keys_end(p, s->sq, min(s->tok0 + ttb, s->sq.nq));
+  if (s->end == 0) s->n = 0;
+  const int end0 = attn_keys_end(p, s->sq, min(s->tok0 + tt, s->sq.nq));
+  s->n0 = max(0, min(s->n, (end0 + kTileKeys - 1) / kTileKeys - s->kt0));
+  s->all = p.mask ? s->sq.prefix : s->sq.prefix + s->tok0 + 1;
+}
+
+// Every thread of the CTA: this CTA's run of positions [total * i / n, total * (i + 1) / n)
+// and the sequence it starts in. `scratch` holds S 64-bit words of shared memory.
+__device__ __forceinline__ int64_t find_run(const AttnParams& p, int ttb, int64_t* scratch, int64_t i, int64_t n,
+                                            Misc* m) {
+  for (int b = threadIdx.x; b < p.S; b += blockDim.x) scratch[b] = seq_cost(p, attn_seq(p, b), ttb);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t sum = 0;
+    for (int b = lane; b < p.S; b += 32) sum += scratch[b];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const int64_t lo = sum * i / n, hi = sum * (i + 1) / n;
+    int64_t run = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.S && !found; b0 += 32) {
+      const int64_t own = b0 + lane < p.S ? scratch[b0 + lane] : 0;
+      int64_t inc = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      const bool mine = lo < run + inc && lo >= run + inc - own;
+      if (mine) {
+        m->b = b0 + lane;
+        m->base = run + inc - own;
+      }
+      found = __any_sync(0xffffffffu, mine);
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      m->lo = lo;
+      m->hi = found ? hi : lo;
+      m->total = sum;
+    }
+  }
+  __syncthreads();
+  return m->total;
+}
+
+// ------------------------------------------------------------------------- waits
+
+// Bounded wait; also gives up when another role did.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (int i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (m->abort) return false;
+    if ((i & 63) == 0 && ptx::globaltimer_ns() - t0 > kMaxWaitNs) {
+      m->abort = 1;
+      return false;
+    }
+  }
+}
+
+// Barrier of the 8 softmax warps that also tells all of them whether one has given up.
+__device__ __forceinline__ bool group_bar_or(bool flag) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.or.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(flag ? 1u : 0u)
+      : "memory");
+  return out != 0;
+}
+
+// Visibility of 32 keys from key j on to row i of the sequence, as bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnSeq& s, int i, int j) {
+  if (p.mask == nullptr) return low_bits(s.prefix + i + 1 - j);
+  const int slot = j - s.prefix;  // first of the 32 keys as a node; negative: committed keys come first
+  if (slot <= -32) return 0xffffffffu;
+  const int32_t* row = p.mask + int64_t(s.q0 + i) * p.mask_words;
+  auto word = [&](int w) { return w < p.mask_words ? uint32_t(__ldg(row + w)) : 0u; };
+  uint32_t bits;
+  if (slot < 0) {
+    bits = (word(0) & low_bits(s.nq)) << -slot | low_bits(-slot);
+  } else {
+    const int w = slot >> 5, sh = slot & 31;
+    bits = __funnelshift_r(word(w), word(w + 1), sh) & low_bits(s.nq - slot);
+  }
+  return bits;
+}
+
+// K/V tile kt holds keys that some row of the segment does not see.
+__device__ __forceinline__ bool tile_masked(const Seg* s, int kt) { return (kt + 1) * kTileKeys > s->all; }
+
+__device__ __forceinline__ bool bad_bf16(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
+
+// -------------------------------------------------------------------- the kernel
+
+template <int D, bool TWO>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
+                   int direct, float* part, int slot_rows, WorkspaceHeader* hdr) {
+  using C = Cfg<D, TWO>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::kStages;
+  uint64_t* clean = bars + 2 * C::kStages;
+  uint64_t* dirty = bars + 3 * C::kStages;
+  uint64_t* q_full = bars + 4 * C::kStages;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;   // [2]
+  uint64_t* p_ready = q_full + 4;  // [2]
+  uint64_t* o_final = q_full + 6;
+  uint64_t* o_free = q_full + 7;
+  uint64_t* done = q_full + 8;
+  uint64_t* seg_full = q_full + 9;              // [kSegRing]
+  uint64_t* seg_empty = seg_full + kSegRing;    // [kSegRing]: 8 softmax and 2 cleaning warps and the MMA issuer
+  Seg* ring = reinterpret_cast<Seg*>(smem + C::kOffSeg);
+  Misc* misc = reinterpret_cast<Misc*>(smem + C::kOffMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tt = kTileRows / p.G, ttb = C::kQTiles * tt;  // tokens of a row tile, of the CTA's row tiles
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
+  if (blockIdx.x == 0) attn_check(p, hdr);
+  if (!direct) {
+    find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, misc);
+    ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(full + i, 1);
+      ptx::mbar_init(empty + i, 1);
+      ptx::mbar_init(clean + i, 2);
+      ptx::mbar_init(dirty + i, 1);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(s_full + g, 1);
+      ptx::mbar_init(p_ready + g, 4);
+    }
+    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(o_free, 8);
+    ptx::mbar_init(done, 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      ptx::mbar_init(seg_full + i, 1);
+      ptx::mbar_init(seg_empty + i, 11);
+    }
+    ptx::fence_mbar_init();
+    misc->abort = 0;
+    for (int i = 0; i < kSegRing; ++i) misc->bad_seg[i] = 0;
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&misc->tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+
+  // the segment with number i, once the producer has written it (null: give up)
+  auto segment = [&](int i) -> const Seg* {
+    return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? ring + i % kSegRing : nullptr;
+  };
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      if (lane == 0) {  // -------------------------------------------------- TMA producer
+        SegIter it;
+        if (!direct) it.start(p, misc, ttb);
+        uint32_t fills = 0, q_loads = 0;
+        bool ok = true;
+        Seg sg;
+        auto load_kv = [&](const CUtensorMap* tm, int kt) {
+          const int st = fills % C::kStages;
+          if (fills >= C::kStages && !wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)) return false;
+          uint8_t* dst = smem + C::kOffRing + st * C::kTileBytes;
+          ptx::mbar_arrive_expect_tx(full + st, C::kTileBytes);
+          ++fills;
+#pragma unroll
+          for (int h = 0; h < C::kBlocks; ++h)
+            ptx::tma_load_3d(dst + h * C::kHalf, tm, full + st, 64 * h, sg.hk, sg.sq.k0 + kt * kTileKeys);
+          if (tm == &tm_v && tile_masked(&sg, kt)) ptx::mbar_arrive(dirty + st);
+          return true;
+        };
+        for (int i = 0;; ++i) {
+          const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
+          if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
+          ring[i % kSegRing] = sg;
+          ptx::mbar_arrive(seg_full + i % kSegRing);
+          if (!more) break;
+          if (sg.n == 0) continue;
+          if (q_loads > 0 && !wait_bar(q_empty, (q_loads - 1) & 1, misc)) break;
+          ptx::mbar_arrive_expect_tx(q_full, C::kQTiles * C::kBlocks * uint32_t(tt * p.G) * 128);
+          ++q_loads;
+          for (int g = 0; g < C::kQTiles; ++g)
+#pragma unroll
+            for (int h = 0; h < C::kBlocks; ++h)
+              ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
+                               sg.sq.q0 + sg.tok0 + g * tt);
+          // the order in which the MMAs use them: K runs one tile (two: one per group) ahead of V
+          constexpr int kAhead = TWO ? 1 : 2;
+          for (int j = 0; ok && j < sg.n + kAhead; ++j) {
+            if (j < sg.n) ok = load_kv(&tm_k, sg.kt0 + j);
+            if (ok && j >= kAhead) ok = load_kv(&tm_v, sg.kt0 + j - kAhead);
+          }
+          if (!ok) break;
+        }
+        // every copy armed above lands before the CTA exits
+        for (uint32_t s2 = 0; s2 < uint32_t(C::kStages) && s2 < fills; ++s2) {
+          const uint32_t uses = (fills - 1 - s2) / C::kStages;
+          ptx::mbar_wait_bounded(full + s2, uses & 1, int64_t(1) << 40, kMaxWaitNs);
+        }
+        if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {  // ---------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kTileRows, kTileKeys);
+        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32_bn(kTileRows, D);
+        const uint32_t q_addr = ptx::smem_addr(smem), r_addr = ptx::smem_addr(smem + C::kOffRing);
+        uint32_t use = 0, q_uses = 0, p_uses[2] = {0, 0}, segs = 0;
+        uint32_t clean_par = 0;  // bit per ring slot
+        bool ok = true;
+        const Seg* sg;
+        auto qk = [&](int g, uint32_t slot) {
+          const uint32_t a = q_addr + (TWO ? g : 0) * C::kTileBytes, b = r_addr + slot * C::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            ptx::tc_mma_f16(tmem + g * kTileKeys,
+                            ptx::smem_desc_kmajor_sw128(a + (kk >> 2) * C::kHalf + (kk & 3) * 32),
+                            ptx::smem_desc_kmajor_sw128(b + (kk >> 2) * C::kHalf + (kk & 3) * 32), idesc_s,
+                            kk > 0 ? 1u : 0u);
+          ptx::tc_commit(s_full + g);
+        };
+        auto pv = [&](int g, uint32_t slot, bool first) {
+          const uint32_t b = r_addr + slot * C::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < kTileKeys / 16; ++kk)
+            ptx::tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * kTileKeys + kk * 8,
+                               ptx::smem_desc_mnmajor_sw128(b + kk * 2048, C::kHalf), idesc_o,
+                               (kk > 0 || !first) ? 1u : 0u);
+        };
+        // ring slot of the next tile, once it has landed
+        auto take = [&](uint32_t* slot) {
+          *slot = use % C::kStages;
+          const bool r = wait_bar(full + *slot, (use / C::kStages) & 1, misc);
+          ++use;
+          ptx::tc_fence_after();
+          return r;
+        };
+        auto take_v = [&](uint32_t* slot, int kt) {
+          if (!take(slot)) return false;
+          if (tile_masked(sg, kt)) {
+            if (!wait_bar(clean + *slot, (clean_par >> *slot) & 1, misc)) return false;
+            clean_par ^= 1u << *slot;
+            ptx::tc_fence_after();
+          }
+          return true;
+        };
+        auto take_p = [&](int g) {
+          const bool r = wait_bar(p_ready + g, p_uses[g] & 1, misc);
+          ++p_uses[g];
+          ptx::tc_fence_after();
+          return r;
+        };
+        for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
+          const int n = sg->n;
+          if (n > 0) {
+            if (!wait_bar(q_full, q_uses & 1, misc)) {
+              ok = false;
+              break;
+            }
+            ++q_uses;
+            uint32_t ks, vs;
+            if (TWO) {
+              // group 0's rows come first: they may need fewer tiles
+              const int n0 = sg->n0;
+              ok = take(&ks);
+              if (!ok) break;
+              if (n0 > 0) qk(0, ks);
+              qk(1, ks);
+              ptx::tc_commit(empty + ks);
+              if (n == 1) ptx::tc_commit(q_empty);
+              if (segs > 0 && !wait_bar(o_free, (segs - 1) & 1, misc)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              for (int j = 0; j < n; ++j) {
+                if (j + 1 < n && !(ok = take(&ks))) break;
+                if (!(ok = take_v(&vs, sg->kt0 + j))) break;
+                if (j < n0) {
+                  if (!(ok = take_p(0))) break;
+                  pv(0, vs, j == 0);
+                  if (j + 1 < n0) qk(0, ks);
+                }
+                if (!(ok = take_p(1))) break;
+                pv(1, vs, j == 0);
+                ptx::tc_commit(empty + vs);
+                if (j + 1 < n) {
+                  qk(1, ks);
+                  ptx::tc_commit(empty + ks);
+                  if (j + 2 == n) ptx::tc_commit(q_empty);
+                }
+              }
+            } else {
+              for (int j = 0; ok && j < min(n, 2); ++j) {
+                ok = take(&ks);
+                if (!ok) break;
+                qk(j, ks);
+                ptx::tc_commit(empty + ks);
+              }
+              if (!ok) break;
+              if (n <= 2) ptx::tc_commit(q_empty);
+              if (segs > 0 && !wait_bar(o_free, (segs - 1) & 1, misc)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              for (int j = 0; j < n; ++j) {
+                const int g = j & 1;
+                if (j + 2 < n && !(ok = take(&ks))) break;
+                if (!(ok = take_v(&vs, sg->kt0 + j))) break;
+                if (!(ok = take_p(g))) break;
+                pv(g, vs, j < 2);
+                ptx::tc_commit(empty + vs);
+                if (j + 2 < n) {
+                  qk(g, ks);
+                  ptx::tc_commit(empty + ks);
+                  if (j + 3 == n) ptx::tc_commit(q_empty);
+                }
+              }
+            }
+            if (!ok) break;
+            ptx::tc_commit(o_final);
+            ++segs;
+          }
+          ptx::mbar_arrive(seg_empty + i % kSegRing);
+        }
+        ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
+        ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
+      }
+    } else {  // ------------------------------------------------------- V cleaning warps
+      uint32_t use = 0, dirty_par = 0;
+      bool ok = true;
+      const int part_id = warp - 10;
+      const Seg* sg;
+      for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
+        constexpr int kAhead = TWO ? 1 : 2;
+        const int n = sg->n;
+        for (int j = max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
+          // before tile j's V come the V tiles [0, j) and the K tiles [0, j + kAhead]
+          const uint32_t u = use + uint32_t(min(n, j + kAhead + 1) + j);
+          const uint32_t slot = u % C::kStages;
+          // The producer says when it has begun to fill the slot with this tile: the slot's
+          // full barrier is then in this tile's phase, not one of the same parity before.
+          ok = __all_sync(0xffffffffu, wait_bar(dirty + slot, (dirty_par >> slot) & 1, misc) &&
+                                           wait_bar(full + slot, (u / C::kStages) & 1, misc));
+          dirty_par ^= 1u << slot;
+          if (!ok) break;
+          uint8_t* v = smem + C::kOffRing + slot * C::kTileBytes;
+          const int live = sg->end - (sg->kt0 + j) * kTileKeys;  // rows of the tile that some row sees
+          bool bad = false;
+          // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
+          for (int x = part_id * 32 + lane; x < C::kTileBytes / 16; x += 64) {
+            uint4* w = reinterpret_cast<uint4*>(v) + x;
+            const int key = (x & (C::kHalf / 16 - 1)) >> 3;
+            if (key >= live) {
+              *w = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 q = *w;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&q);
+            bool hit = false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (bad_bf16(e[y])) {
+                e[y] &= 0xFFFF0000u;
+                hit = true;
+              }
+              if (bad_bf16(e[y] >> 16)) {
+                e[y] &= 0x0000FFFFu;
+                hit = true;
+              }
+            }
+            if (hit) *w = q;
+            bad |= hit;
+          }
+          if (bad) misc->bad_seg[i % kSegRing] = i + 1;
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(clean + slot);
+        }
+        use += 2 * n;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
+      }
+    }
+  } else {  // -------------------------------------------------------------- softmax groups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int g = warp >> 2;                 // group
+    const int row = threadIdx.x & 127;       // row of the tile
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + g * kTileKeys;
+    const uint32_t o_col = tmem + lane_base + 256 + g * D;
+    const int tok_in = row / p.G, head_in = row - tok_in * p.G;
+    const float c2 = p.scale * kLog2e;
+    uint32_t s_uses = 0, finals = 0;
+    bool ok = true;
+    for (int is = 0;; ++is) {
+      const Seg* sg = segment(is);
+      ok = __all_sync(0xffffffffu, sg != nullptr);
+      if (TWO ? !ok : group_bar_or(!ok)) break;
+      if (sg->n < 0) break;
+      const int i = sg->tok0 + (TWO ? g * tt : 0) + tok_in;   // token of the sequence
+      const bool valid = tok_in < tt && i < sg->sq.nq;
+      const int n_all = sg->n, n = TWO && g == 0 ? sg->n0 : n_all;
+      const int first = TWO ? 0 : g, step = TWO ? 1 : 2;
+      float m = -INFINITY;
+      uint64_t l2[2] = {0, 0};
+      for (int j = first; j < n; j += step) {
+        const int kt = sg->kt0 + j;
+        ok = __all_sync(0xffffffffu, wait_bar(s_full + g, s_uses & 1, misc));
+        if (!ok) break;
+        ++s_uses;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tc_ld_32x32b_x32(s_col + 32 * c, s[c]);
+        ptx::tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tc_reg_fence(s[c]);
+        if (tile_masked(sg, kt)) {
+          const int im = min(i, sg->sq.nq - 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = seen_bits(p, sg->sq, im, kt * kTileKeys + 32 * c);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;  // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int x = 1; x < 31; x += 2)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = mt > m && (mt - m) * c2 > kLazy;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mt : m;
+          const float f = grow ? ptx::exp2_approx((m - mn) * c2) : 1.0f;
+          m = mn;
+          if (j != first) {  // S of this tile was issued after the last P V of the group: O is at rest
+            const uint64_t ff = ptx::pack_f32x2(f, f);
+            l2[0] = ptx::fma_f32x2(l2[0], ff, 0);
+            l2[1] = ptx::fma_f32x2(l2[1], ff, 0);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              ptx::tc_ld_32x32b_x32(o_col + 32 * c, o);
+              ptx::tc_wait_ld();
+              ptx::tc_reg_fence(o);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              ptx::tc_st_32x32b_x32(o_col + 32 * c, o);
+            }
+          }
+        }
+        const float nb = m == -INFINITY ? 0.0f : -m * c2;
+        const uint64_t c22 = ptx::pack_f32x2(c2, c2), nb2 = ptx::pack_f32x2(nb, nb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const uint64_t e = ptx::fma_f32x2(
+                ptx::pack_f32x2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), c22, nb2);
+            float a, b;
+            ptx::unpack_f32x2(e, a, b);
+            a = ptx::exp2_approx(a);
+            b = ptx::exp2_approx(b);
+            l2[x & 1] = ptx::add_f32x2(l2[x & 1], ptx::pack_f32x2(a, b));
+            pk[x] = ptx::pack_bf16(a, b);
+          }
+          ptx::tc_st_32x32b_x16(s_col + 16 * c, pk);
+        }
+        ptx::tc_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_ready + g);
+      }
+      if (TWO && !ok) break;
+      float l;
+      {
+        float a, b, c, d;
+        ptx::unpack_f32x2(l2[0], a, b);
+        ptx::unpack_f32x2(l2[1], c, d);
+        l = (a + b) + (c + d);
+      }
+      // ------------------------------------------------------------------------ epilogue
+      float w0 = 1.0f, w1 = 0.0f;                       // factors of the groups' accumulators
+      bool has0 = TWO ? n > 0 : n_all > 0, has1 = !TWO && n_all > 1;
+      if (!TWO) {  // add up the two groups' statistics
+        float2* st = reinterpret_cast<float2*>(smem + C::kOffStat);
+        st[g * kTileRows + row] = make_float2(m, l);
+        if (group_bar_or(!ok)) break;
+        const float2 a = st[row], b = st[kTileRows + row];
+        m = fmaxf(a.x, b.x);
+        const float mb = m == -INFINITY ? 0.0f : m;
+        w0 = ptx::exp2_approx((a.x - mb) * c2);
+        w1 = ptx::exp2_approx((b.x - mb) * c2);
+        if (m == -INFINITY) w0 = w1 = 1.0f;  // nothing, or a NaN that l carries on
+        l = a.y * w0 + b.y * w1;
+      }
+      if (n_all > 0) ok = __all_sync(0xffffffffu, wait_bar(o_final, finals & 1, misc));
+      if (TWO ? !ok : group_bar_or(!ok)) break;  // (one: the statistics have been read, too)
+      ptx::tc_fence_after();
+      const bool none = m == -INFINITY && l == 0.0f;
+      const bool fix = n_all > 0 && misc->bad_seg[is % kSegRing] == is + 1;
+      const int64_t grow_row = int64_t(sg->sq.q0) + i;
+      const int head = sg->hk * p.G + head_in;
+      const float inv = none ? 0.0f : 1.0f / l;
+      const int prow = TWO ? g * kTileRows + row : row;
+      float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slot_rows) * (D + 2);
+      // columns of this thread: all (two), or the group's half (one)
+      constexpr int kCols = TWO ? D : D / 2;
+      const int col0 = TWO ? 0 : g * kCols;
+      const uint32_t oa = tmem + lane_base + 256 + (TWO ? g * D : 0) + col0, ob = tmem + lane_base + 256 + D + col0;
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0;
+        if (has0) {
+          ptx::tc_ld_32x32b_x32(oa + 32 * c, o);
+          ptx::tc_wait_ld();
+          ptx::tc_reg_fence(o);
+        }
+        if (!TWO) {
+          uint32_t o1[32];
+          if (has1) {
+            ptx::tc_ld_32x32b_x32(ob + 32 * c, o1);
+            ptx::tc_wait_ld();
+            ptx::tc_reg_fence(o1);
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            float v = __uint_as_float(o[x]) * w0;
+            if (has1) v = fmaf(__uint_as_float(o1[x]), w1, v);
+            o[x] = __float_as_uint(v);
+          }
+        }
+        if (fix && valid && !none) {
+          // infinities and NaN that the cleaning took out of V: a row that sees them gets them back
+          const int j0 = max(sg->kt0 * kTileKeys, sg->all) & ~(kTileKeys - 1);
+          const int j1 = min((sg->kt0 + n_all) * kTileKeys, sg->end);
+          const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + int64_t(sg->hk) * p.v_hs + col0 + 32 * c;
+          for (int j = j0; j < j1; ++j) {
+            if (!attn_sees(p, sg->sq, i, j)) continue;
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(v + (int64_t(sg->sq.k0) + j) * p.v_ts);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const uint32_t u = __ldg(e + x);
+              if (bad_bf16(u)) o[2 * x] = __float_as_uint(__uint_as_float(o[2 * x]) + __uint_as_float(u << 16));
+              if (bad_bf16(u >> 16))
+                o[2 * x + 1] = __float_as_uint(__uint_as_float(o[2 * x + 1]) + __uint_as_float(u & 0xFFFF0000u));
+            }
+          }
+        }
+        if (sg->whole) {
+          if (valid) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + grow_row * p.o_ts + int64_t(head) * p.o_hs +
+                                 col0 + 32 * c;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 u;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                e[y] = none ? 0u
+                            : ptx::pack_bf16(__uint_as_float(o[8 * x + 2 * y]) * inv,
+                                             __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 8 * x) = u;
+            }
+          }
+        } else if (prow < slot_rows) {
+          float4* dst = reinterpret_cast<float4*>(pslot + size_t(prow) * D + col0 + 32 * c);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                 __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+        }
+      }
+      if (TWO || g == 0) {
+        if (sg->whole) {
+          if (valid && p.lse)
+            p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+        } else if (prow < slot_rows) {
+          pslot[size_t(slot_rows) * D + 2 * prow] = m;
+          pslot[size_t(slot_rows) * D + 2 * prow + 1] = l;
+        }
+      }
+      if (n_all > 0) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(o_free);
+        ++finals;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(seg_empty + is % kSegRing);
+    }
+    ptx::tc_fence_before();
+  }
+  // ------------------------------------------------------------------------------ teardown
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && misc->abort) record_error(hdr, KPOOL_ERR_DEVICE_TIMEOUT);
+  if (warp == 9) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------- join
+//
+// CTA i (x) looks at the border between the runs i and i + 1 of the persistent kernel. If
+// it cuts the rows of one item, and is the first border to do so, the CTA adds up that item's
+// partial results in the order of the runs. y: 8 rows each, a warp per row, its lanes the channels.
+constexpr int kJoinRows = 8;
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int tt, int ttb, int runs,
+                                                        const float* part, int slot_rows) {
+  extern __shared__ int64_t scratch[];
+  __shared__ Misc m;
+  const int64_t bi = int64_t(blockIdx.x) + 1;
+  const int64_t total = find_run(p, ttb, scratch, bi, runs, &m);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
+  const int64_t pos = total * bi / runs;
+  if (pos >= total || total == 0 || m.lo >= m.hi) {
+    // an empty run starts where the next one does: that one's border is looked at there
+    return;
+  }
+  const AttnSeq sq = attn_seq(p, m.b);
+  const int64_t per_head = seq_cost(p, sq, ttb) / p.Hkv;
+  const int hk = int((pos - m.base) / per_head);
+  int64_t item = m.base + hk * per_head;
+  int t = 0, c = tile_cost(p, sq, 0, ttb);
+  while (pos >= item + c) {
+    item += c;
+    c = tile_cost(p, sq, ++t, ttb);
+  }
+  if (item == pos) return;                          // the border falls between two items
+  // runs that hold tiles of the item: first is the one that contains its first tile
+  auto run_lo = [&](int64_t r) { return total * r / runs; };
+  int64_t first = bi - 1;
+  while (first > 0 && run_lo(first) > item) --first;
+  // the first border inside the item with a non-empty run behind it does the work
+  for (int64_t r = first + 1; r < bi; ++r)
+    if (run_lo(r) > item && run_lo(r) < run_lo(r + 1)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t item_end = item + c;
+  const float c2 = p.scale * kLog2e;
+  const int rows_q = kTileRows;
+  const int vr = blockIdx.y * kJoinRows + warp;
+  if (vr >= slot_rows) return;
+  const int q_tile = vr / rows_q, row = vr - q_tile * rows_q;
+  const int tok_in = row / p.G, i = t * ttb + q_tile * tt + tok_in;
+  if (tok_in >= tt || i >= sq.nq) return;
+  constexpr int kPer = D / 32;
+  float acc[kPer], mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) acc[x] = 0.0f;
+  for (int64_t r = first; r < runs && run_lo(r) < item_end; ++r) {
+    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
+    if (hi <= item || hi == lo) continue;
+    const int slot = lo >= item ? 0 : 1;
+    const float* s = part + (size_t(r) * 2 + slot) * size_t(slot_rows) * (D + 2);
+    const float2 ml = *reinterpret_cast<const float2*>(s + size_t(slot_rows) * D + 2 * vr);
+    const float mn = fmaxf(mm, ml.x);
+    const float base = mn == -INFINITY ? 0.0f : mn;
+    const float f = mm == -INFINITY ? 1.0f : exp2f((mm - base) * c2);
+    // a part without any weight adds nothing; with a NaN among its scores its sum passes on
+    const float w = ml.x == -INFINITY ? 1.0f : exp2f((ml.x - base) * c2);
+    ll = ll * f + ml.y * w;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * f + s[size_t(vr) * D + x * 32 + lane] * w;
+    mm = mn;
+  }
+  const bool none = mm == -INFINITY && ll == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / ll;
+  const int head = hk * p.G + (row - tok_in * p.G);
+  const int64_t grow_row = int64_t(sq.q0) + i;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + grow_row * p.o_ts + int64_t(head) * p.o_hs;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) dst[x * 32 + lane] = __float2bfloat16_rn(none ? 0.0f : acc[x] * inv);
+  if (lane == 0 && p.lse) p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (mm * c2 + log2f(ll)) * kLn2;
+}
+
+template <int D, bool TWO>
+cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
+  using C = Cfg<D, TWO>;
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int tt = kTileRows / p.G, ttb = C::kQTiles * tt;
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), D, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)) ||
+      !make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
+      !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = attn_tiles(p.R, p.S, ttb);
+  const int64_t items = tiles * p.Hkv;
+  // One CTA per row tile once there are several per SM (the hardware deals them out, deepest
+  // first); below that equal runs of K/V tiles, whose join costs a few microseconds. The one-tile
+  // form always takes runs: its items are short, and a persistent CTA pays its start once.
+  const bool direct = p.S > kAttnMaxRunSeqs || (TWO && items >= int64_t(kAttnDirectItems) * sms);
+  if (items > INT32_MAX) return cudaErrorInvalidValue;
+  const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
+  const int slot_rows = attn_slot_rows(p.R, p.G, C::kQTiles * kTileRows);
+  float* part = reinterpret_cast<float*>(ws + sizeof(WorkspaceHeader));
+  WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
+  auto kernel = attn_tc_kernel<D, TWO>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreadsTc, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, hdr);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || direct) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + kJoinRows - 1) / kJoinRows));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = size_t(p.S) * 8;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (grid < 2) return cudaSuccess;
+  e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxRunSeqs * 8);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p, tt, ttb, grid, static_cast<const float*>(part), slot_rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim) {
+  return dtype == KPOOL_BF16 && (head_dim == 64 || head_dim == 128);
+}
+
+cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
+  // two row tiles per CTA read K and V half as often, but want sequences that fill them
+  const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
+  if (p.D == 64) return two ? launch<64, true>(p, ws, stream) : launch<64, false>(p, ws, stream);
+  return two ? launch<128, true>(p, ws, stream) : launch<128, false>(p, ws, stream);
+}
+
+}  // namespace kpool

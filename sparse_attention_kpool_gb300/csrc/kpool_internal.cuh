@@ -189,6 +189,12 @@ kpool_status select_check_args(const void* q, const void* kin, const float* w, c
 // unavailable or rejects the arguments (base not 16-byte aligned, too many rows).
 bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
 
+// TMA descriptor of a [tokens, heads, dim] bf16 tensor with any token and head strides
+// (elements, multiples of 8), read in boxes of 64 channels x box_heads x box_tokens with
+// 128-byte swizzle; a box's rows in shared memory run over heads first, then tokens.
+bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t dim,
+                          int64_t token_stride, int64_t head_stride, uint32_t box_tokens, uint32_t box_heads);
+
 // Remembers a failing CUDA call of this thread for kpool_last_cuda_error; true on success.
 bool note_cuda_error(cudaError_t e);
 

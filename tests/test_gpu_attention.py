@@ -162,6 +162,23 @@ def test_many_sequences():
     A.check(out, lse, A.reference(q, k, v, A.see_tree(nodes, extents, prefixes, None), scale))
 
 
+@pytest.mark.parametrize("ql,kl,heads", [
+    ([500], [500], (128, 1, 128)), ([4000], [4000], (32, 8, 128)), ([70, 500, 3], [900, 500, 1500], (128, 1, 64)),
+    ([1] * 40, [3000] * 40, (8, 2, 128)), ([6000, 1, 900], [6000, 7000, 1000], (32, 8, 64)), ([12000], [12000], (32, 8, 128)),
+    ([20, 7, 1], [300, 20000, 4000], (24, 4, 64)),
+], ids=str)
+def test_runs_of_many_segments(ql, kl, heads):
+    """Every split of the work (one CTA per row tile; equal runs with several segments, joined or not)
+    against the CUDA-core kernel, twice bit for bit."""
+    (q, k, v, scale), out, lse = run_prompt(ql, kl, heads, BF, "auto", seed=41)
+    _, want, wlse = run_prompt(ql, kl, heads, BF, "simt", tensors=(q, k, v))
+    # both sides are within the weights' and the output's rounding of the true value; |v| sums stay below 4
+    assert ((out.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -6).all()
+    assert ((lse - wlse).abs() <= 1e-4).all()
+    _, again, alse = run_prompt(ql, kl, heads, BF, "auto", tensors=(q, k, v))
+    assert torch.equal(out, again) and torch.equal(lse, alse)
+
+
 SELECT_HEADS = HEADS + [(32, 8, 128, BF), (64, 1, 128, BF), (20, 1, 64, BF), (24, 2, 128, BF)]
 
 
