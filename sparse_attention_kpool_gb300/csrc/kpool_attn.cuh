@@ -35,6 +35,7 @@ struct AttnParams {
   int32_t Hq, Hkv, G, D;
   float scale;
   AttnMode mode;
+  int32_t gx_k, gr_k, gx_v, gr_v;            // column and row step of a key head in the gathered views (selected)
 };
 
 // Query rows, keys and committed prefix of one sequence, clipped so that nothing
@@ -130,6 +131,7 @@ __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader*
     }
   }
   if (p.mode == kAttnSelected && p.row_seq != nullptr)
+#pragma unroll 4
     for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
       const int b = __ldg(p.row_seq + r);
       if (b < 0 || b >= p.S) bad = 1;
@@ -163,9 +165,11 @@ inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
   return size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
 }
 
-// Tensor-core kernel of prompt and tree attention: bf16, head_dim 64 or 128, at least one key token.
+// Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens
+// also heads that lie in k and v as attn_gather_supported wants.
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
-cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
+bool attn_gather_supported(const AttnParams& p);
+cudaError_t launch_attn_tc(AttnParams& p, char* ws, cudaStream_t stream);
 
 // CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);

@@ -48,7 +48,7 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
   const int32_t group = shape->q_heads / shape->kv_heads;
   if (shape->head_dim > 256 || group > 128 || shape->q_heads > 4096) return KPOOL_ERR_UNSUPPORTED;
   const kpool_dtype dtype = kpool_dtype(shape->dtype);
-  const bool tc_ok = p.mode != kAttnSelected && attn_tc_supported(dtype, shape->head_dim);
+  const bool tc_ok = attn_tc_supported(dtype, shape->head_dim);
   if (opt.score_kernel == KPOOL_SCORE_TC && !tc_ok) return KPOOL_ERR_UNSUPPORTED;
   if (q_rows == 0) return KPOOL_OK;
   if (!heads_ok(q, *shape) || !heads_ok(out, *shape)) return KPOOL_ERR_INVALID_ARG;
@@ -84,7 +84,8 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
   p.scale = shape->scale;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const bool tc = tc_ok && k_tokens > 0 && opt.score_kernel != KPOOL_SCORE_SIMT;
+  const bool tc = tc_ok && k_tokens > 0 && opt.score_kernel != KPOOL_SCORE_SIMT &&
+                  (p.mode != kAttnSelected || attn_gather_supported(p));
   const cudaError_t e = tc ? launch_attn_tc(p, ws, stream) : launch_attn_simt(p, dtype, ws, stream);
   return note_cuda_error(e) ? KPOOL_OK : KPOOL_ERR_CUDA;
 }

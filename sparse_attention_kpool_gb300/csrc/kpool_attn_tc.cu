@@ -48,10 +48,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
 constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are microseconds
+// Gathered tiles whose validity bits are held: the producer is at most the ring of tiles (8 slots,
+// four K and four V) plus the two K tiles of lead ahead of the softmax.
+constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
-template <int D, bool TWO>
+// The forms of the kernel: one or two row tiles of consecutive tokens, or one token's heads over gathered keys.
+enum Form { kOne, kTwo, kGather };
+
+template <int D, Form F>
 struct Cfg {
+  static constexpr bool TWO = F == kTwo;
   static constexpr int kTileBytes = kTileKeys * D * 2;   // one K or V tile, one Q tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
   static constexpr int kBlocks = D / 64;
@@ -62,10 +69,12 @@ struct Cfg {
   // full[stages] empty[stages] clean[stages] dirty[stages] q_full q_empty s_full[2] p_ready[2] o_final o_free done
   // seg_full[ring] seg_empty[ring]
   static constexpr int kNumBars = 4 * kStages + 9 + 2 * kSegRing;
-  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;  // 16-byte words follow
   static constexpr int kOffSeg = kOffMisc + 64;
   static constexpr int kOffStat = kOffSeg + 64 * kSegRing;         // [2][128] float2 (m, l), one-tile form only
-  static constexpr int kSmem = kOffStat + (TWO ? 0 : 2 * kTileRows * 8);
+  static constexpr int kOffBits = kOffStat + (TWO ? 0 : 2 * kTileRows * 8);  // [kBitsRing] x 128 bits
+  static_assert(kOffBits % 16 == 0 && kOffSeg % 16 == 0 && kOffStat % 16 == 0, "16-byte accesses");
+  static constexpr int kSmem = kOffBits + (F == kGather ? 16 * kBitsRing : 0);
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
 };
 
@@ -161,6 +170,34 @@ __device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int til
   s->n = tile_cost(p, s->sq, s->tok0 / ttb, ttb);
   s->whole = 1;
   s->slot = 0;
+  return true;
+}
+
+// Gathered form: every row and key head has the same number of tiles, and positions run over
+// rows, then key heads (the heads of a token lie together in memory).
+__device__ __forceinline__ int gather_tiles(const AttnParams& p) { return max(1, (p.width + kTileKeys - 1) / kTileKeys); }
+
+__device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, int64_t lo, int64_t hi, Seg* s) {
+  if (*pos >= hi) return false;
+  const int nt = gather_tiles(p);
+  const int64_t item = *pos / nt;
+  const int r = int(item / p.Hkv);
+  s->hk = int(item - int64_t(r) * p.Hkv);
+  s->kt0 = int(*pos - item * nt);
+  s->n = int(min(int64_t(nt - s->kt0), hi - *pos));
+  s->whole = s->n == nt;
+  s->slot = *pos == lo ? 0 : 1;
+  *pos += s->n;
+  attn_selected_seq(p, r, &s->sq.k0, &s->sq.nk);
+  s->sq.q0 = r;
+  s->sq.nq = 1;
+  s->sq.prefix = 0;
+  s->sq.ok = true;
+  s->tok0 = 0;
+  s->end = s->sq.nk > 0 ? p.width : 0;
+  if (s->end == 0) s->n = 0;
+  s->n0 = s->n;
+  s->all = 0;
   return true;
 }
 
@@ -270,12 +307,13 @@ __device__ __forceinline__ bool bad_bf16(uint32_t x) { return (x & 0x7F80u) == 0
 
 // -------------------------------------------------------------------- the kernel
 
-template <int D, bool TWO>
+template <int D, Form F>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
                    int direct, float* part, int slot_rows, WorkspaceHeader* hdr) {
-  using C = Cfg<D, TWO>;
+  using C = Cfg<D, F>;
+  constexpr bool TWO = C::TWO, GATHER = F == kGather;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -294,11 +332,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   Seg* ring = reinterpret_cast<Seg*>(smem + C::kOffSeg);
   Misc* misc = reinterpret_cast<Misc*>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tt = kTileRows / p.G, ttb = C::kQTiles * tt;  // tokens of a row tile, of the CTA's row tiles
+  const int tt = GATHER ? 1 : kTileRows / p.G, ttb = C::kQTiles * tt;  // tokens of a row tile, of the CTA's row tiles
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
   if (blockIdx.x == 0) attn_check(p, hdr);
-  if (!direct) {
+  if (GATHER) {
+    if (threadIdx.x == 0) {
+      const int64_t total = int64_t(p.R) * p.Hkv * gather_tiles(p);
+      misc->lo = total * blockIdx.x / gridDim.x;
+      misc->hi = total * (blockIdx.x + 1) / gridDim.x;
+    }
+  } else if (!direct) {
     find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, misc);
     ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
   }
@@ -341,13 +385,85 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
+    if (GATHER && warp == 8) {  // ---------------------------------------- gathering producer
+      // Lane i holds ids 4 i .. 4 i + 3 of a tile and fetches those rows. An id outside the
+      // sequence fetches its first token instead, its bit is cleared and its V row is zeroed.
+      const int64_t lo = misc->lo, hi = misc->hi;
+      int64_t pos = lo;
+      uint32_t fills = 0, q_loads = 0, tile = 0;
+      bool ok = true;
+      Seg sg{};
+      uint4* bits_ring = reinterpret_cast<uint4*>(smem + C::kOffBits);
+      auto load_kv = [&](const CUtensorMap* tm, int kt, int gx, int gr, bool is_k) {
+        const int st = fills % C::kStages;
+        int id[4];
+        const int32_t* src = p.ids + int64_t(sg.sq.q0) * p.width;
+        uint32_t good = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int j = kt * kTileKeys + 4 * lane + x;
+          id[x] = j < p.width ? __ldg(src + j) : -1;
+          const bool in = id[x] >= 0 && id[x] < sg.sq.nk;
+          good |= in ? 1u << x : 0u;
+          id[x] = gr * sg.hk + sg.sq.k0 + (in ? id[x] : 0);
+        }
+        if (is_k) {  // the tile's 128 bits: eight lanes make a word
+          uint32_t w = good << (4 * (lane & 7));
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, d);
+          if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(bits_ring + tile % kBitsRing)[lane >> 3] = w;
+          ++tile;
+        }
+        if (fills >= C::kStages &&
+            !__all_sync(0xffffffffu, wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)))
+          return false;
+        __syncwarp();
+        uint8_t* dst = smem + C::kOffRing + st * C::kTileBytes + lane * 512;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, C::kTileBytes);
+        __syncwarp();
+        ++fills;
+#pragma unroll
+        for (int h = 0; h < C::kBlocks; ++h)
+          ptx::tma_gather4(dst + h * C::kHalf, tm, full + st, gx * sg.hk + 64 * h, id[0], id[1], id[2], id[3]);
+        if (!is_k && lane == 0) ptx::mbar_arrive(dirty + st);
+        return true;
+      };
+      for (int i = 0;; ++i) {
+        const bool more = gather_seg(p, &pos, lo, hi, &sg);
+        if (!more) sg.n = -1;
+        if (i >= kSegRing &&
+            !__all_sync(0xffffffffu, wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)))
+          break;
+        if (lane == 0) {
+          ring[i % kSegRing] = sg;
+          ptx::mbar_arrive(seg_full + i % kSegRing);
+        }
+        if (!more) break;
+        if (sg.n == 0) continue;
+        if (q_loads > 0 && !__all_sync(0xffffffffu, wait_bar(q_empty, (q_loads - 1) & 1, misc))) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(q_full, C::kBlocks * uint32_t(p.G) * 128);
+#pragma unroll
+          for (int h = 0; h < C::kBlocks; ++h)
+            ptx::tma_load_3d(smem + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G, sg.sq.q0);
+        }
+        ++q_loads;
+        for (int j = 0; ok && j < sg.n + 2; ++j) {
+          if (j < sg.n) ok = load_kv(&tm_k, sg.kt0 + j, p.gx_k, p.gr_k, true);
+          if (ok && j >= 2) ok = load_kv(&tm_v, sg.kt0 + j - 2, p.gx_v, p.gr_v, false);
+        }
+        if (!ok) break;
+      }
+      for (uint32_t s2 = 0; s2 < uint32_t(C::kStages) && s2 < fills; ++s2)
+        ptx::mbar_wait_bounded(full + s2, ((fills - 1 - s2) / C::kStages) & 1, int64_t(1) << 40, kMaxWaitNs);
+      if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
+    } else if (warp == 8) {
       if (lane == 0) {  // -------------------------------------------------- TMA producer
         SegIter it;
         if (!direct) it.start(p, misc, ttb);
         uint32_t fills = 0, q_loads = 0;
         bool ok = true;
-        Seg sg;
+        Seg sg{};
         auto load_kv = [&](const CUtensorMap* tm, int kt) {
           const int st = fills % C::kStages;
           if (fills >= C::kStages && !wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)) return false;
@@ -428,7 +544,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         };
         auto take_v = [&](uint32_t* slot, int kt) {
           if (!take(slot)) return false;
-          if (tile_masked(sg, kt)) {
+          if (GATHER || tile_masked(sg, kt)) {
             if (!wait_bar(clean + *slot, (clean_par >> *slot) & 1, misc)) return false;
             clean_par ^= 1u << *slot;
             ptx::tc_fence_after();
@@ -523,10 +639,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       bool ok = true;
       const int part_id = warp - 10;
       const Seg* sg;
+      uint32_t tile = 0;
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
         constexpr int kAhead = TWO ? 1 : 2;
         const int n = sg->n;
-        for (int j = max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
+        for (int j = GATHER ? 0 : max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
           // before tile j's V come the V tiles [0, j) and the K tiles [0, j + kAhead]
           const uint32_t u = use + uint32_t(min(n, j + kAhead + 1) + j);
           const uint32_t slot = u % C::kStages;
@@ -537,6 +654,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           dirty_par ^= 1u << slot;
           if (!ok) break;
           uint8_t* v = smem + C::kOffRing + slot * C::kTileBytes;
+          if (GATHER) {  // every row of the tile sees the same keys: only the invalid ids' rows are zeroed
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
+            if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
+              for (int x = part_id * 32 + lane; x < C::kTileBytes / 16; x += 64) {
+                const int key = (x & (C::kHalf / 16 - 1)) >> 3;
+                if (!((w[key >> 5] >> (key & 31)) & 1u)) reinterpret_cast<uint4*>(v)[x] = make_uint4(0, 0, 0, 0);
+              }
+              ptx::fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(clean + slot);
+            continue;
+          }
           const int live = sg->end - (sg->kt0 + j) * kTileKeys;  // rows of the tile that some row sees
           bool bad = false;
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
@@ -570,6 +700,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (lane == 0) ptx::mbar_arrive(clean + slot);
         }
         use += 2 * n;
+        tile += n;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
@@ -583,7 +714,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint32_t o_col = tmem + lane_base + 256 + g * D;
     const int tok_in = row / p.G, head_in = row - tok_in * p.G;
     const float c2 = p.scale * kLog2e;
-    uint32_t s_uses = 0, finals = 0;
+    uint32_t s_uses = 0, finals = 0, tile = 0;
     bool ok = true;
     for (int is = 0;; ++is) {
       const Seg* sg = segment(is);
@@ -608,7 +739,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         ptx::tc_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tc_reg_fence(s[c]);
-        if (tile_masked(sg, kt)) {
+        if (GATHER) {
+          const uint4 w = reinterpret_cast<const uint4*>(smem + C::kOffBits)[(tile + j) % kBitsRing];
+          if ((w.x & w.y & w.z & w.w) != 0xffffffffu) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;  // -inf
+            }
+          }
+        } else if (tile_masked(sg, kt)) {
           const int im = min(i, sg->sq.nq - 1);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -699,7 +841,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (TWO ? !ok : group_bar_or(!ok)) break;  // (one: the statistics have been read, too)
       ptx::tc_fence_after();
       const bool none = m == -INFINITY && l == 0.0f;
-      const bool fix = n_all > 0 && misc->bad_seg[is % kSegRing] == is + 1;
+      const bool fix = !GATHER && n_all > 0 && misc->bad_seg[is % kSegRing] == is + 1;
       const int64_t grow_row = int64_t(sg->sq.q0) + i;
       const int head = sg->hk * p.G + head_in;
       const float inv = none ? 0.0f : 1.0f / l;
@@ -789,6 +931,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (lane == 0) ptx::mbar_arrive(o_free);
         ++finals;
       }
+      tile += n_all;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(seg_empty + is % kSegRing);
     }
@@ -812,27 +955,41 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 // partial results in the order of the runs. y: 8 rows each, a warp per row, its lanes the channels.
 constexpr int kJoinRows = 8;
 
-template <int D>
+template <int D, bool GATHER>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int tt, int ttb, int runs,
                                                         const float* part, int slot_rows) {
   extern __shared__ int64_t scratch[];
   __shared__ Misc m;
   const int64_t bi = int64_t(blockIdx.x) + 1;
-  const int64_t total = find_run(p, ttb, scratch, bi, runs, &m);
+  int64_t total, item;
+  int c, hk, t = 0;
+  AttnSeq sq{};
+  if (GATHER) {
+    c = gather_tiles(p);
+    total = int64_t(p.R) * p.Hkv * c;
+  } else {
+    total = find_run(p, ttb, scratch, bi, runs, &m);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
   const int64_t pos = total * bi / runs;
-  if (pos >= total || total == 0 || m.lo >= m.hi) {
-    // an empty run starts where the next one does: that one's border is looked at there
-    return;
-  }
-  const AttnSeq sq = attn_seq(p, m.b);
-  const int64_t per_head = seq_cost(p, sq, ttb) / p.Hkv;
-  const int hk = int((pos - m.base) / per_head);
-  int64_t item = m.base + hk * per_head;
-  int t = 0, c = tile_cost(p, sq, 0, ttb);
-  while (pos >= item + c) {
-    item += c;
-    c = tile_cost(p, sq, ++t, ttb);
+  // an empty run starts where the next one does: that one's border is looked at there
+  if (total == 0 || pos >= total * (bi + 1) / runs) return;
+  if (GATHER) {
+    const int64_t number = pos / c;
+    item = number * c;
+    sq.q0 = int(number / p.Hkv);
+    sq.nq = 1;
+    hk = int(number - int64_t(sq.q0) * p.Hkv);
+  } else {
+    sq = attn_seq(p, m.b);
+    const int64_t per_head = seq_cost(p, sq, ttb) / p.Hkv;
+    hk = int((pos - m.base) / per_head);
+    item = m.base + hk * per_head;
+    c = tile_cost(p, sq, 0, ttb);
+    while (pos >= item + c) {
+      item += c;
+      c = tile_cost(p, sq, ++t, ttb);
+    }
   }
   if (item == pos) return;                          // the border falls between two items
   // runs that hold tiles of the item: first is the one that contains its first tile
@@ -881,49 +1038,70 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   if (lane == 0 && p.lse) p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (mm * c2 + log2f(ll)) * kLn2;
 }
 
-template <int D, bool TWO>
-cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
-  using C = Cfg<D, TWO>;
+// How the rows of one head lie in memory for a gather: as rows of a matrix whose columns hold
+// the heads side by side, or whose rows hold one head's tokens after another's.
+bool gather_view(CUtensorMap* tm, const void* base, const AttnParams& p, int64_t ts, int64_t hs, int32_t* gx,
+                 int32_t* gr) {
+  const int64_t span = int64_t(p.Hkv - 1) * hs + p.D;
+  if (span <= ts) {
+    *gx = int32_t(hs);
+    *gr = 0;
+    return span <= INT32_MAX && make_tmap_bf16_rows(tm, base, uint64_t(p.T), uint64_t(span), ts);
+  }
+  if (hs % ts != 0 || int64_t(p.Hkv) * (hs / ts) + p.T > INT32_MAX) return false;
+  *gx = 0;
+  *gr = int32_t(hs / ts);
+  return make_tmap_bf16_rows(tm, base, uint64_t(int64_t(p.Hkv - 1) * *gr + p.T), uint64_t(p.D), ts);
+}
+
+template <int D, Form F>
+cudaError_t launch(AttnParams& p, char* ws, cudaStream_t stream) {
+  using C = Cfg<D, F>;
+  constexpr bool GATHER = F == kGather;
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int tt = kTileRows / p.G, ttb = C::kQTiles * tt;
+  const int tt = GATHER ? 1 : kTileRows / p.G, ttb = C::kQTiles * tt;
   CUtensorMap tq, tk, tv;
-  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), D, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)) ||
-      !make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
-      !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1))
+  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), D, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
     return cudaErrorInvalidValue;
-  const int64_t tiles = attn_tiles(p.R, p.S, ttb);
+  if (GATHER ? !gather_view(&tk, p.k, p, p.k_ts, p.k_hs, &p.gx_k, &p.gr_k) ||
+                   !gather_view(&tv, p.v, p, p.v_ts, p.v_hs, &p.gx_v, &p.gr_v)
+             : !make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
+                   !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
   // One CTA per row tile once there are several per SM (the hardware deals them out, deepest
-  // first); below that equal runs of K/V tiles, whose join costs a few microseconds. The one-tile
-  // form always takes runs: its items are short, and a persistent CTA pays its start once.
-  const bool direct = p.S > kAttnMaxRunSeqs || (TWO && items >= int64_t(kAttnDirectItems) * sms);
-  if (items > INT32_MAX) return cudaErrorInvalidValue;
+  // first); below that equal runs of K/V tiles, whose join costs a few microseconds. The forms of
+  // one row tile always take runs: their items are short, and a persistent CTA pays its start once.
+  const bool direct = !GATHER && (p.S > kAttnMaxRunSeqs || (C::TWO && items >= int64_t(kAttnDirectItems) * sms));
+  if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
-  const int slot_rows = attn_slot_rows(p.R, p.G, C::kQTiles * kTileRows);
+  const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
   float* part = reinterpret_cast<float*>(ws + sizeof(WorkspaceHeader));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
-  auto kernel = attn_tc_kernel<D, TWO>;
+  auto kernel = attn_tc_kernel<D, F>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreadsTc, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, hdr);
   e = cudaGetLastError();
-  if (e != cudaSuccess || direct) return e;
+  if (e != cudaSuccess || direct || grid < 2) return e;
+  auto join = attn_join_kernel<D, GATHER>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = size_t(p.S) * 8;
+  cfg.dynamicSmemBytes = GATHER ? 0 : size_t(p.S) * 8;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (grid < 2) return cudaSuccess;
-  e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxRunSeqs * 8);
+  e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxRunSeqs * 8);
   if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p, tt, ttb, grid, static_cast<const float*>(part), slot_rows);
+  e = cudaLaunchKernelEx(&cfg, join, static_cast<const AttnParams&>(p), tt, ttb, grid, static_cast<const float*>(part),
+                         slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -933,11 +1111,21 @@ bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim) {
   return dtype == KPOOL_BF16 && (head_dim == 64 || head_dim == 128);
 }
 
-cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
+bool attn_gather_supported(const AttnParams& p) {
+  auto view = [&](int64_t ts, int64_t hs) {
+    return int64_t(p.Hkv - 1) * hs + p.D <= ts ? ts <= INT32_MAX
+                                               : hs % ts == 0 && int64_t(p.Hkv) * (hs / ts) + p.T <= INT32_MAX;
+  };
+  return view(p.k_ts, p.k_hs) && view(p.v_ts, p.v_hs);
+}
+
+cudaError_t launch_attn_tc(AttnParams& p, char* ws, cudaStream_t stream) {
+  if (p.mode == kAttnSelected)
+    return p.D == 64 ? launch<64, kGather>(p, ws, stream) : launch<128, kGather>(p, ws, stream);
   // two row tiles per CTA read K and V half as often, but want sequences that fill them
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
-  if (p.D == 64) return two ? launch<64, true>(p, ws, stream) : launch<64, false>(p, ws, stream);
-  return two ? launch<128, true>(p, ws, stream) : launch<128, false>(p, ws, stream);
+  if (p.D == 64) return two ? launch<64, kTwo>(p, ws, stream) : launch<64, kOne>(p, ws, stream);
+  return two ? launch<128, kTwo>(p, ws, stream) : launch<128, kOne>(p, ws, stream);
 }
 
 }  // namespace kpool
