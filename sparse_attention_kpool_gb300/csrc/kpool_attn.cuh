@@ -35,7 +35,6 @@ struct AttnParams {
   int32_t Hq, Hkv, G, D;
   float scale;
   AttnMode mode;
-  int32_t gx_k, gr_k, gx_v, gr_v;            // column and row step of a key head in the gathered views (selected)
 };
 
 // Query rows, keys and committed prefix of one sequence, clipped so that nothing
@@ -166,10 +165,10 @@ inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
 }
 
 // Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens
-// also heads that lie in k and v as attn_gather_supported wants.
+// also strides that attn_gather_supported takes.
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
 bool attn_gather_supported(const AttnParams& p);
-cudaError_t launch_attn_tc(AttnParams& p, char* ws, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
 
 // CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);

@@ -41,13 +41,13 @@
 namespace kpool {
 namespace {
 
-constexpr int kThreadsTc = 384;
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
 constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are microseconds
+constexpr int kGatherWarps = 4;
 // Gathered tiles whose validity bits are held: the producer is at most the ring of tiles (8 slots,
 // four K and four V) plus the two K tiles of lead ahead of the softmax.
 constexpr int kBitsRing = 8;
@@ -59,6 +59,7 @@ enum Form { kOne, kTwo, kGather };
 template <int D, Form F>
 struct Cfg {
   static constexpr bool TWO = F == kTwo;
+  static constexpr int kThreads = F == kGather ? 512 : 384;
   static constexpr int kTileBytes = kTileKeys * D * 2;   // one K or V tile, one Q tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
   static constexpr int kBlocks = D / 64;
@@ -308,7 +309,7 @@ __device__ __forceinline__ bool bad_bf16(uint32_t x) { return (x & 0x7F80u) == 0
 // -------------------------------------------------------------------- the kernel
 
 template <int D, Form F>
-__global__ void __launch_bounds__(kThreadsTc, 1)
+__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
                    int direct, float* part, int slot_rows, WorkspaceHeader* hdr) {
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      ptx::mbar_init(full + i, 1);
+      ptx::mbar_init(full + i, GATHER ? 33 * kGatherWarps : 1);
       ptx::mbar_init(empty + i, 1);
       ptx::mbar_init(clean + i, 2);
       ptx::mbar_init(dirty + i, 1);
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     ptx::mbar_init(done, 1);
     for (int i = 0; i < kSegRing; ++i) {
       ptx::mbar_init(seg_full + i, 1);
-      ptx::mbar_init(seg_empty + i, 11);
+      ptx::mbar_init(seg_empty + i, 9 + (GATHER ? kGatherWarps : 2));
     }
     ptx::fence_mbar_init();
     misc->abort = 0;
@@ -384,79 +385,93 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? ring + i % kSegRing : nullptr;
   };
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (GATHER && warp == 8) {  // ---------------------------------------- gathering producer
-      // Lane i holds ids 4 i .. 4 i + 3 of a tile and fetches those rows. An id outside the
-      // sequence fetches its first token instead, its bit is cleared and its V row is zeroed.
-      const int64_t lo = misc->lo, hi = misc->hi;
-      int64_t pos = lo;
-      uint32_t fills = 0, q_loads = 0, tile = 0;
-      bool ok = true;
-      Seg sg{};
-      uint4* bits_ring = reinterpret_cast<uint4*>(smem + C::kOffBits);
-      auto load_kv = [&](const CUtensorMap* tm, int kt, int gx, int gr, bool is_k) {
-        const int st = fills % C::kStages;
-        int id[4];
-        const int32_t* src = p.ids + int64_t(sg.sq.q0) * p.width;
-        uint32_t good = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = kt * kTileKeys + 4 * lane + x;
-          id[x] = j < p.width ? __ldg(src + j) : -1;
-          const bool in = id[x] >= 0 && id[x] < sg.sq.nk;
-          good |= in ? 1u << x : 0u;
-          id[x] = gr * sg.hk + sg.sq.k0 + (in ? id[x] : 0);
-        }
-        if (is_k) {  // the tile's 128 bits: eight lanes make a word
-          uint32_t w = good << (4 * (lane & 7));
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, d);
-          if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(bits_ring + tile % kBitsRing)[lane >> 3] = w;
-          ++tile;
-        }
-        if (fills >= C::kStages &&
-            !__all_sync(0xffffffffu, wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)))
-          return false;
-        __syncwarp();
-        uint8_t* dst = smem + C::kOffRing + st * C::kTileBytes + lane * 512;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, C::kTileBytes);
-        __syncwarp();
-        ++fills;
-#pragma unroll
-        for (int h = 0; h < C::kBlocks; ++h)
-          ptx::tma_gather4(dst + h * C::kHalf, tm, full + st, gx * sg.hk + 64 * h, id[0], id[1], id[2], id[3]);
-        if (!is_k && lane == 0) ptx::mbar_arrive(dirty + st);
-        return true;
-      };
-      for (int i = 0;; ++i) {
-        const bool more = gather_seg(p, &pos, lo, hi, &sg);
-        if (!more) sg.n = -1;
-        if (i >= kSegRing &&
-            !__all_sync(0xffffffffu, wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)))
-          break;
-        if (lane == 0) {
+    // (512 x 128 or 384 x 168 registers at launch cover 256 x 200 + 256 x 56 and 256 x 208 + 128 x 72)
+    if (GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (GATHER && warp == 8) {
+      if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
+        const int64_t lo = misc->lo, hi = misc->hi;
+        int64_t pos = lo;
+        uint32_t q_loads = 0;
+        Seg sg{};
+        for (int i = 0;; ++i) {
+          const bool more = gather_seg(p, &pos, lo, hi, &sg);
+          if (!more) sg.n = -1;
+          if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
           ring[i % kSegRing] = sg;
           ptx::mbar_arrive(seg_full + i % kSegRing);
-        }
-        if (!more) break;
-        if (sg.n == 0) continue;
-        if (q_loads > 0 && !__all_sync(0xffffffffu, wait_bar(q_empty, (q_loads - 1) & 1, misc))) break;
-        if (lane == 0) {
+          if (!more) break;
+          if (sg.n == 0) continue;
+          if (q_loads > 0 && !wait_bar(q_empty, (q_loads - 1) & 1, misc)) break;
           ptx::mbar_arrive_expect_tx(q_full, C::kBlocks * uint32_t(p.G) * 128);
+          ++q_loads;
 #pragma unroll
           for (int h = 0; h < C::kBlocks; ++h)
             ptx::tma_load_3d(smem + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G, sg.sq.q0);
         }
-        ++q_loads;
-        for (int j = 0; ok && j < sg.n + 2; ++j) {
-          if (j < sg.n) ok = load_kv(&tm_k, sg.kt0 + j, p.gx_k, p.gr_k, true);
-          if (ok && j >= 2) ok = load_kv(&tm_v, sg.kt0 + j - 2, p.gx_v, p.gr_v, false);
+        if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
+      }
+    } else if (GATHER && warp >= 12) {  // ------------------------------------ gathering warps
+      // Warp w fetches keys [32 w, 32 w + 32) of every tile, 16 bytes a lane, into the swizzled
+      // layout that TMA would write. An id outside the sequence reads nothing and leaves zeros,
+      // so no weight of zero meets an infinity or NaN.
+      constexpr int kChunks = D / 8;               // 16-byte pieces of a row
+      constexpr int kRowsPer = 32 / kChunks;       // rows per warp instruction
+      const int w = warp - 12, c = lane % kChunks, rsub = lane / kChunks;
+      const uint32_t dst0 = ptx::smem_addr(smem + C::kOffRing) + uint32_t(c >> 3) * C::kHalf + uint32_t(w * 32) * 128;
+      uint32_t fills = 0, tile = 0;
+      bool ok = true;
+      const Seg* sg;
+      auto load_id = [&](int kt) {
+        const int j = kt * kTileKeys + w * 32 + lane;
+        return j < p.width ? __ldg(p.ids + int64_t(sg->sq.q0) * p.width + j) : -1;
+      };
+      // tok: the lane's key as a token of k and v, -1 where it is not seen
+      auto load_kv = [&](const void* src, int64_t hs, uint32_t ts_bytes, int tok, bool is_k) {
+        const int st = fills % C::kStages;
+        if (fills >= C::kStages &&
+            !__all_sync(0xffffffffu, wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)))
+          return false;
+        __syncwarp();
+        ++fills;
+        if (is_k) {
+          const uint32_t bits = __ballot_sync(0xffffffffu, tok >= 0);
+          if (lane == 0) reinterpret_cast<uint32_t*>(smem + C::kOffBits)[4 * (tile % kBitsRing) + w] = bits;
+          ++tile;
+        }
+        const char* base = static_cast<const char*>(src) + (int64_t(sg->hk) * hs + c * 8) * 2;
+        const uint32_t dst = dst0 + st * C::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < 32 / kRowsPer; ++i) {
+          const int row = rsub + kRowsPer * i;     // of the warp's 32
+          const int t = __shfl_sync(0xffffffffu, tok, row);
+          const char* from = base + uint64_t(uint32_t(max(t, 0))) * ts_bytes;
+          ptx::cp_async_16(dst + uint32_t(row) * 128 + uint32_t(((c & 7) ^ (row & 7)) << 4), from, t >= 0 ? 16u : 0u);
+        }
+        ptx::cp_async_arrive(full + st);                     // when this lane's pieces have landed
+        if (lane == 0) ptx::mbar_arrive(full + st);          // and the warp's word of bits is written
+        return true;
+      };
+      for (int i = 0;; ++i) {
+        sg = segment(i);
+        if (!__all_sync(0xffffffffu, sg != nullptr) || sg->n < 0) break;
+        const int n = sg->n, kt0 = sg->kt0, nk = sg->sq.nk, k0 = sg->sq.k0;
+        int next = n > 0 ? load_id(kt0) : 0, tok = -1, tok1 = -1, tok2 = -1;  // tokens of tiles j, j - 1, j - 2
+        for (int j = 0; ok && n > 0 && j < n + 2; ++j) {
+          tok2 = tok1;
+          tok1 = tok;
+          if (j < n) {
+            tok = next >= 0 && next < nk ? next + k0 : -1;
+            if (j + 1 < n) next = load_id(kt0 + j + 1);
+            ok = load_kv(p.k, p.k_hs, uint32_t(p.k_ts * 2), tok, true);
+          }
+          if (ok && j >= 2) ok = load_kv(p.v, p.v_hs, uint32_t(p.v_ts * 2), tok2, false);
         }
         if (!ok) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
-      for (uint32_t s2 = 0; s2 < uint32_t(C::kStages) && s2 < fills; ++s2)
-        ptx::mbar_wait_bounded(full + s2, ((fills - 1 - s2) / C::kStages) & 1, int64_t(1) << 40, kMaxWaitNs);
-      if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
+      ptx::cp_async_wait_all();                    // every copy has landed before the CTA exits
     } else if (warp == 8) {
       if (lane == 0) {  // -------------------------------------------------- TMA producer
         SegIter it;
@@ -539,12 +554,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           *slot = use % C::kStages;
           const bool r = wait_bar(full + *slot, (use / C::kStages) & 1, misc);
           ++use;
+          if (GATHER) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
           ptx::tc_fence_after();
           return r;
         };
         auto take_v = [&](uint32_t* slot, int kt) {
           if (!take(slot)) return false;
-          if (GATHER || tile_masked(sg, kt)) {
+          if (!GATHER && tile_masked(sg, kt)) {
             if (!wait_bar(clean + *slot, (clean_par >> *slot) & 1, misc)) return false;
             clean_par ^= 1u << *slot;
             ptx::tc_fence_after();
@@ -634,16 +650,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
         ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
       }
-    } else {  // ------------------------------------------------------- V cleaning warps
+    } else if (!GATHER) {  // --------------------------------------------- V cleaning warps
       uint32_t use = 0, dirty_par = 0;
       bool ok = true;
       const int part_id = warp - 10;
       const Seg* sg;
-      uint32_t tile = 0;
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
         constexpr int kAhead = TWO ? 1 : 2;
         const int n = sg->n;
-        for (int j = GATHER ? 0 : max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
+        for (int j = max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
           // before tile j's V come the V tiles [0, j) and the K tiles [0, j + kAhead]
           const uint32_t u = use + uint32_t(min(n, j + kAhead + 1) + j);
           const uint32_t slot = u % C::kStages;
@@ -654,19 +669,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           dirty_par ^= 1u << slot;
           if (!ok) break;
           uint8_t* v = smem + C::kOffRing + slot * C::kTileBytes;
-          if (GATHER) {  // every row of the tile sees the same keys: only the invalid ids' rows are zeroed
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
-            if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-              for (int x = part_id * 32 + lane; x < C::kTileBytes / 16; x += 64) {
-                const int key = (x & (C::kHalf / 16 - 1)) >> 3;
-                if (!((w[key >> 5] >> (key & 31)) & 1u)) reinterpret_cast<uint4*>(v)[x] = make_uint4(0, 0, 0, 0);
-              }
-              ptx::fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(clean + slot);
-            continue;
-          }
           const int live = sg->end - (sg->kt0 + j) * kTileKeys;  // rows of the tile that some row sees
           bool bad = false;
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
@@ -700,13 +702,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (lane == 0) ptx::mbar_arrive(clean + slot);
         }
         use += 2 * n;
-        tile += n;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
     }
   } else {  // -------------------------------------------------------------- softmax groups
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int g = warp >> 2;                 // group
     const int row = threadIdx.x & 127;       // row of the tile
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -1038,24 +1040,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   if (lane == 0 && p.lse) p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (mm * c2 + log2f(ll)) * kLn2;
 }
 
-// How the rows of one head lie in memory for a gather: as rows of a matrix whose columns hold
-// the heads side by side, or whose rows hold one head's tokens after another's.
-bool gather_view(CUtensorMap* tm, const void* base, const AttnParams& p, int64_t ts, int64_t hs, int32_t* gx,
-                 int32_t* gr) {
-  const int64_t span = int64_t(p.Hkv - 1) * hs + p.D;
-  if (span <= ts) {
-    *gx = int32_t(hs);
-    *gr = 0;
-    return span <= INT32_MAX && make_tmap_bf16_rows(tm, base, uint64_t(p.T), uint64_t(span), ts);
-  }
-  if (hs % ts != 0 || int64_t(p.Hkv) * (hs / ts) + p.T > INT32_MAX) return false;
-  *gx = 0;
-  *gr = int32_t(hs / ts);
-  return make_tmap_bf16_rows(tm, base, uint64_t(int64_t(p.Hkv - 1) * *gr + p.T), uint64_t(p.D), ts);
-}
-
 template <int D, Form F>
-cudaError_t launch(AttnParams& p, char* ws, cudaStream_t stream) {
+cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   using C = Cfg<D, F>;
   constexpr bool GATHER = F == kGather;
   int sms = 0;
@@ -1065,11 +1051,12 @@ cudaError_t launch(AttnParams& p, char* ws, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), D, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
     return cudaErrorInvalidValue;
-  if (GATHER ? !gather_view(&tk, p.k, p, p.k_ts, p.k_hs, &p.gx_k, &p.gr_k) ||
-                   !gather_view(&tv, p.v, p, p.v_ts, p.v_hs, &p.gx_v, &p.gr_v)
-             : !make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
-                   !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1))
+  if (GATHER) {
+    tk = tv = tq;  // (not used: keys and values come by plain copies)
+  } else if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
+             !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1)) {
     return cudaErrorInvalidValue;
+  }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
   // One CTA per row tile once there are several per SM (the hardware deals them out, deepest
@@ -1084,7 +1071,7 @@ cudaError_t launch(AttnParams& p, char* ws, cudaStream_t stream) {
   auto kernel = attn_tc_kernel<D, F>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreadsTc, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, hdr);
+  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || grid < 2) return e;
   auto join = attn_join_kernel<D, GATHER>;
@@ -1100,7 +1087,7 @@ cudaError_t launch(AttnParams& p, char* ws, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxRunSeqs * 8);
   if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, join, static_cast<const AttnParams&>(p), tt, ttb, grid, static_cast<const float*>(part),
+  e = cudaLaunchKernelEx(&cfg, join, p, tt, ttb, grid, static_cast<const float*>(part),
                          slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1112,14 +1099,10 @@ bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim) {
 }
 
 bool attn_gather_supported(const AttnParams& p) {
-  auto view = [&](int64_t ts, int64_t hs) {
-    return int64_t(p.Hkv - 1) * hs + p.D <= ts ? ts <= INT32_MAX
-                                               : hs % ts == 0 && int64_t(p.Hkv) * (hs / ts) + p.T <= INT32_MAX;
-  };
-  return view(p.k_ts, p.k_hs) && view(p.v_ts, p.v_hs);
+  return p.k_ts < (int64_t(1) << 31) && p.v_ts < (int64_t(1) << 31);  // byte strides in 32 bits
 }
 
-cudaError_t launch_attn_tc(AttnParams& p, char* ws, cudaStream_t stream) {
+cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
   if (p.mode == kAttnSelected)
     return p.D == 64 ? launch<64, kGather>(p, ws, stream) : launch<128, kGather>(p, ws, stream);
   // two row tiles per CTA read K and V half as often, but want sequences that fill them

@@ -195,9 +195,6 @@ bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint
 bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t dim,
                           int64_t token_stride, int64_t head_stride, uint32_t box_tokens, uint32_t box_heads);
 
-// TMA descriptor of a [rows, cols] bf16 matrix for gathers of four rows x 64 columns.
-bool make_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, int64_t row_stride);
-
 // Remembers a failing CUDA call of this thread for kpool_last_cuda_error; true on success.
 bool note_cuda_error(cudaError_t e);
 

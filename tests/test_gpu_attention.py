@@ -212,8 +212,10 @@ def test_selected_few_and_many_rows(rows, heads, family):
     ids = torch.stack([torch.randperm(lens[0], generator=g)[:width] for _ in range(rows)]).to(torch.int32)
     ids[rows // 2, 17:900] = -1
     q, k, v = make(rows, rows, lens[0], heads, BF)
-    out, lse = K.kpool_attention_selected(q, k, v, ids.cuda(), i32([0, lens[0]]), 0.1,
-                                          row_seq=i32([0] * rows), return_lse=True, score_kernel=FAMILIES[family])
+    ws = K.new_attention_workspace(rows, 1, *heads, BF)
+    out, lse = K.kpool_attention_selected(q, k, v, ids.cuda(), i32([0, lens[0]]), 0.1, row_seq=i32([0] * rows),
+                                          return_lse=True, workspace=ws, score_kernel=FAMILIES[family])
+    assert K.kpool_last_device_error(ws) == K.KPOOL_OK
     pick = sorted({0, rows // 2, rows - 1, rows // 3, rows // 7})
     ref = A.reference(q[pick], k, v, A.see_selected(ids[pick], [0] * len(pick), lens), 0.1)
     A.check(out[pick], lse[pick], ref)
