@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? ring + i % kSegRing : nullptr;
   };
   if (warp >= 8) {
-    // (512 x 128 or 384 x 168 registers at launch cover 256 x 200 + 256 x 56 and 256 x 208 + 128 x 72)
-    if (GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // (512 x 128 or 384 x 168 registers at launch cover 256 x 208 + 256 x 48 and 256 x 208 + 128 x 72)
+    if (GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (GATHER && warp == 8) {
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       }
     }
   } else {  // -------------------------------------------------------------- softmax groups
-    if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int g = warp >> 2;                 // group
     const int row = threadIdx.x & 127;       // row of the tile
@@ -782,14 +782,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
             l2[0] = ptx::fma_f32x2(l2[0], ff, 0);
             l2[1] = ptx::fma_f32x2(l2[1], ff, 0);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              ptx::tc_ld_32x32b_x32(o_col + 32 * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              ptx::tc_ld_32x32b_x16(o_col + 16 * c, o);
               ptx::tc_wait_ld();
               ptx::tc_reg_fence(o);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              ptx::tc_st_32x32b_x32(o_col + 32 * c, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              ptx::tc_st_32x32b_x16(o_col + 16 * c, o);
             }
           }
         }
