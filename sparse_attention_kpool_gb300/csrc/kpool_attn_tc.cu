@@ -9,7 +9,8 @@
 // added up at the end).
 //
 // Roles (12 warps): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread per row; warp 8
-// loads by TMA; warp 9 issues the MMAs and owns TMEM; warps 10-11 clean V tiles (below). Per
+// loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns TMEM); warp 11
+// cleans V tiles (below). Per
 // 128-key tile of a group: S = Q K^T (128 x 128, fp32 in TMEM); its thread reads the row, takes
 // the maximum, writes P = 2^(c s - c m) as bf16 over S in TMEM and adds its fp32 sum; O += P V
 // with P read from TMEM. The tensor core works on one group while the other does its softmax.
@@ -23,8 +24,8 @@
 //
 // Masked places. A key that a row does not see gets s = -inf, so what K holds there does not
 // matter. A weight of zero does not silence V, though (0 * NaN): in the tiles that some row
-// does not see entirely, warps 10-11 first overwrite V rows past the last visible key with
-// zeros, replace every other infinity or NaN by zero and raise a flag; rows that do see such
+// does not see entirely, warp 11 first overwrites V rows past the last visible key with
+// zeros, replaces every other infinity or NaN by zero and raises a flag; rows that do see such
 // a value add it in the epilogue.
 //
 // Work. A pass over (sequence, key head, row tile, K/V tile). Many row tiles: one CTA each,
@@ -59,6 +60,9 @@ enum Form { kOne, kTwo, kGather };
 template <int D, Form F>
 struct Cfg {
   static constexpr bool TWO = F == kTwo;
+  // The ring holds K(0) .. K(kAhead - 1), then K(j), V(j - kAhead) in turn: the order in which the MMAs use
+  // them, K one tile (one-tile form: one per group) ahead.
+  static constexpr int kAhead = TWO ? 1 : 2;
   static constexpr int kThreads = F == kGather ? 512 : 384;
   static constexpr int kTileBytes = kTileKeys * D * 2;   // one K or V tile, one Q tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
@@ -68,8 +72,8 @@ struct Cfg {
   static constexpr int kOffRing = kQTiles * kTileBytes;
   static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
   // full[stages] empty[stages] clean[stages] dirty[stages] q_full q_empty s_full[2] p_ready[2] o_final o_free done
-  // seg_full[ring] seg_empty[ring]
-  static constexpr int kNumBars = 4 * kStages + 9 + 2 * kSegRing;
+  // seg_full[ring] seg_empty[ring] turn[2]
+  static constexpr int kNumBars = 4 * kStages + 11 + 2 * kSegRing;
   static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;  // 16-byte words follow
   static constexpr int kOffSeg = kOffMisc + 64;
   static constexpr int kOffStat = kOffSeg + 64 * kSegRing;         // [2][128] float2 (m, l), one-tile form only
@@ -78,6 +82,12 @@ struct Cfg {
   static constexpr int kSmem = kOffBits + (F == kGather ? 16 * kBitsRing : 0);
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
 };
+
+// Ring use, within its segment of n tiles, of tile j's K and V.
+template <int kAhead>
+__device__ __forceinline__ uint32_t k_use(int j) { return uint32_t(j + max(0, j - kAhead)); }
+template <int kAhead>
+__device__ __forceinline__ uint32_t v_use(int j, int n) { return uint32_t(min(n, j + kAhead + 1) + j); }
 
 struct Misc {
   int64_t base;       // persistent form: first position of sequence b
@@ -329,7 +339,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   uint64_t* o_free = q_full + 7;
   uint64_t* done = q_full + 8;
   uint64_t* seg_full = q_full + 9;              // [kSegRing]
-  uint64_t* seg_empty = seg_full + kSegRing;    // [kSegRing]: 8 softmax and 2 cleaning warps and the MMA issuer
+  uint64_t* seg_empty = seg_full + kSegRing;    // [kSegRing]: 8 softmax warps, 2 MMA issuers, the cleaning or gathering warps
+  uint64_t* turn = seg_empty + kSegRing;        // [2]: it is this issuer's turn
   Seg* ring = reinterpret_cast<Seg*>(smem + C::kOffSeg);
   Misc* misc = reinterpret_cast<Misc*>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -350,22 +361,23 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       ptx::mbar_init(full + i, GATHER ? 33 * kGatherWarps : 1);
-      ptx::mbar_init(empty + i, 1);
-      ptx::mbar_init(clean + i, 2);
+      ptx::mbar_init(empty + i, 2);
+      ptx::mbar_init(clean + i, 1);
       ptx::mbar_init(dirty + i, 1);
     }
     ptx::mbar_init(q_full, 1);
-    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(q_empty, 2);
     for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(turn + g, 1);
       ptx::mbar_init(s_full + g, 1);
       ptx::mbar_init(p_ready + g, 4);
     }
-    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(o_final, 2);
     ptx::mbar_init(o_free, 8);
-    ptx::mbar_init(done, 1);
+    ptx::mbar_init(done, 2);
     for (int i = 0; i < kSegRing; ++i) {
       ptx::mbar_init(seg_full + i, 1);
-      ptx::mbar_init(seg_empty + i, 9 + (GATHER ? kGatherWarps : 2));
+      ptx::mbar_init(seg_empty + i, 10 + (GATHER ? kGatherWarps : 1));
     }
     ptx::fence_mbar_init();
     misc->abort = 0;
@@ -507,11 +519,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
             for (int h = 0; h < C::kBlocks; ++h)
               ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
                                sg.sq.q0 + sg.tok0 + g * tt);
-          // the order in which the MMAs use them: K runs one tile (two: one per group) ahead of V
-          constexpr int kAhead = TWO ? 1 : 2;
-          for (int j = 0; ok && j < sg.n + kAhead; ++j) {
+          for (int j = 0; ok && j < sg.n + C::kAhead; ++j) {
             if (j < sg.n) ok = load_kv(&tm_k, sg.kt0 + j);
-            if (ok && j >= kAhead) ok = load_kv(&tm_v, sg.kt0 + j - kAhead);
+            if (ok && j >= C::kAhead) ok = load_kv(&tm_v, sg.kt0 + j - C::kAhead);
           }
           if (!ok) break;
         }
@@ -522,145 +532,129 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         }
         if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
       }
-    } else if (warp == 9) {
-      if (lane == 0) {  // ---------------------------------------------------- MMA issuer
+    } else if (warp == 9 || warp == 10) {
+      if (lane == 0) {  // ------------------------------------ MMA issuers, one per softmax group
+        const int g = warp - 9;
+        // Descriptors of the Q tile and of the first ring slot; the others differ in the address field
+        // (bytes / 16) only, so a step is one addition.
+        const uint64_t q_desc =
+            ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + (TWO ? g * C::kTileBytes : 0)));
+        const uint64_t k_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + C::kOffRing));
+        const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + C::kOffRing), C::kHalf);
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kTileRows, kTileKeys);
         constexpr uint32_t idesc_o = ptx::idesc_bf16_f32_bn(kTileRows, D);
-        const uint32_t q_addr = ptx::smem_addr(smem), r_addr = ptx::smem_addr(smem + C::kOffRing);
-        uint32_t use = 0, q_uses = 0, p_uses[2] = {0, 0}, segs = 0;
-        uint32_t clean_par = 0;  // bit per ring slot
+        const uint32_t s_acc = tmem + g * kTileKeys, o_acc = tmem + 256 + g * D;
+        uint32_t use = 0, q_uses = 0, p_uses = 0, turns = 0;  // ring uses before this segment, Q tiles, P tiles
+        uint32_t clean_par = 0;                    // bit per ring slot
         bool ok = true;
         const Seg* sg;
-        auto qk = [&](int g, uint32_t slot) {
-          const uint32_t a = q_addr + (TWO ? g : 0) * C::kTileBytes, b = r_addr + slot * C::kTileBytes;
+        auto landed = [&](uint32_t u) {
+          const bool r = wait_bar(full + u % C::kStages, (u / C::kStages) & 1, misc);
+          if (GATHER) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
+          return r;
+        };
+        // The issuers take turns, a tile's P V and the next tile's Q K^T at a time. Left to themselves
+        // the groups fall into step: both do their softmax while the tensor core idles, then both wait
+        // for it (7.8 against 6.1 ms for one 32,768-token prompt of 32 heads).
+        if (g == 1) ptx::mbar_arrive(turn);
+        auto my_turn = [&]() {
+          const bool r = wait_bar(turn + g, turns & 1, misc);
+          ++turns;
+          return r;
+        };
+        auto qk = [&](uint32_t u, bool pass) {
+          const uint64_t b = k_desc + (u % C::kStages) * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            ptx::tc_mma_f16(tmem + g * kTileKeys,
-                            ptx::smem_desc_kmajor_sw128(a + (kk >> 2) * C::kHalf + (kk & 3) * 32),
-                            ptx::smem_desc_kmajor_sw128(b + (kk >> 2) * C::kHalf + (kk & 3) * 32), idesc_s,
-                            kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            // handed on a little early: the other's first product follows without a gap
+            if (kk == D / 32 && pass) ptx::mbar_arrive(turn + (g ^ 1));
+            const uint32_t step = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+            ptx::tc_mma_f16(s_acc, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
+          }
           ptx::tc_commit(s_full + g);
         };
-        auto pv = [&](int g, uint32_t slot, bool first) {
-          const uint32_t b = r_addr + slot * C::kTileBytes;
+        auto pv = [&](uint32_t u, bool first) {
+          const uint64_t b = v_desc + (u % C::kStages) * (C::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
-            ptx::tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * kTileKeys + kk * 8,
-                               ptx::smem_desc_mnmajor_sw128(b + kk * 2048, C::kHalf), idesc_o,
-                               (kk > 0 || !first) ? 1u : 0u);
-        };
-        // ring slot of the next tile, once it has landed
-        auto take = [&](uint32_t* slot) {
-          *slot = use % C::kStages;
-          const bool r = wait_bar(full + *slot, (use / C::kStages) & 1, misc);
-          ++use;
-          if (GATHER) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
-          ptx::tc_fence_after();
-          return r;
-        };
-        auto take_v = [&](uint32_t* slot, int kt) {
-          if (!take(slot)) return false;
-          if (!GATHER && tile_masked(sg, kt)) {
-            if (!wait_bar(clean + *slot, (clean_par >> *slot) & 1, misc)) return false;
-            clean_par ^= 1u << *slot;
-            ptx::tc_fence_after();
-          }
-          return true;
-        };
-        auto take_p = [&](int g) {
-          const bool r = wait_bar(p_ready + g, p_uses[g] & 1, misc);
-          ++p_uses[g];
-          ptx::tc_fence_after();
-          return r;
+            ptx::tc_mma_f16_ts(o_acc, s_acc + kk * 8, b + kk * (2048 >> 4), idesc_o, (kk > 0 || !first) ? 1u : 0u);
         };
         for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
-          const int n = sg->n;
+          const int n = sg->n, kt0 = sg->kt0;
           if (n > 0) {
-            if (!wait_bar(q_full, q_uses & 1, misc)) {
-              ok = false;
-              break;
+            // Every tile of the ring is waited for in order and released by both issuers, used or not:
+            // a slot's barriers then never get two phases ahead of either.
+            const int n0 = TWO && g == 0 ? sg->n0 : n;
+            auto mine = [&](int j) { return TWO ? j < n0 : (j & 1) == g; };
+            const int last = TWO ? n0 - 1 : n - 1 - ((n - 1 - g) & 1);  // the group's last tile (< 0: none)
+            auto score = [&](int j, uint32_t u, bool pass) {
+              if (mine(j)) {
+                qk(u, pass);
+                if (j == last) ptx::tc_commit(q_empty);
+                ptx::tc_commit(empty + u % C::kStages);
+              } else {
+                ptx::mbar_arrive(empty + u % C::kStages);
+                if (pass) ptx::mbar_arrive(turn + (g ^ 1));
+              }
+            };
+            if (!(ok = wait_bar(q_full, q_uses & 1, misc))) break;
+            if (last < 0) ptx::mbar_arrive(q_empty);
+            for (int j = 0; j < min(n, C::kAhead); ++j) {
+              const uint32_t u = use + k_use<C::kAhead>(j);
+              if (!(ok = landed(u))) break;
+              ptx::tc_fence_after();
+              score(j, u, false);
             }
+            if (!ok) break;
+            if (q_uses > 0 && !(ok = wait_bar(o_free, (q_uses - 1) & 1, misc))) break;
             ++q_uses;
-            uint32_t ks, vs;
-            if (TWO) {
-              // group 0's rows come first: they may need fewer tiles
-              const int n0 = sg->n0;
-              ok = take(&ks);
-              if (!ok) break;
-              if (n0 > 0) qk(0, ks);
-              qk(1, ks);
-              ptx::tc_commit(empty + ks);
-              if (n == 1) ptx::tc_commit(q_empty);
-              if (segs > 0 && !wait_bar(o_free, (segs - 1) & 1, misc)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
-              for (int j = 0; j < n; ++j) {
-                if (j + 1 < n && !(ok = take(&ks))) break;
-                if (!(ok = take_v(&vs, sg->kt0 + j))) break;
-                if (j < n0) {
-                  if (!(ok = take_p(0))) break;
-                  pv(0, vs, j == 0);
-                  if (j + 1 < n0) qk(0, ks);
+            for (int j = 0; j < n; ++j) {
+              const int jk = j + C::kAhead;
+              const uint32_t uk = use + k_use<C::kAhead>(jk), uv = use + v_use<C::kAhead>(j, n);
+              if (jk < n && !(ok = landed(uk))) break;
+              if (!(ok = landed(uv))) break;
+              const uint32_t slot = uv % C::kStages;
+              const bool masked = !GATHER && tile_masked(sg, kt0 + j);
+              if (mine(j)) {
+                if (masked && !(ok = wait_bar(clean + slot, (clean_par >> slot) & 1, misc))) break;
+                if (!(ok = wait_bar(p_ready + g, p_uses & 1, misc))) break;
+                ++p_uses;
+                if (!(ok = my_turn())) break;
+                ptx::tc_fence_after();
+                pv(uv, TWO ? j == 0 : j < 2);
+                if (jk < n) score(jk, uk, true);
+                else ptx::mbar_arrive(turn + (g ^ 1));
+                ptx::tc_commit(empty + slot);
+              } else {
+                if (TWO) {  // (one: a turn belongs to a pair of tiles)
+                  if (!(ok = my_turn())) break;
+                  ptx::mbar_arrive(turn + (g ^ 1));
                 }
-                if (!(ok = take_p(1))) break;
-                pv(1, vs, j == 0);
-                ptx::tc_commit(empty + vs);
-                if (j + 1 < n) {
-                  qk(1, ks);
-                  ptx::tc_commit(empty + ks);
-                  if (j + 2 == n) ptx::tc_commit(q_empty);
-                }
+                if (jk < n) score(jk, uk, false);
+                ptx::mbar_arrive(empty + slot);
               }
-            } else {
-              for (int j = 0; ok && j < min(n, 2); ++j) {
-                ok = take(&ks);
-                if (!ok) break;
-                qk(j, ks);
-                ptx::tc_commit(empty + ks);
-              }
-              if (!ok) break;
-              if (n <= 2) ptx::tc_commit(q_empty);
-              if (segs > 0 && !wait_bar(o_free, (segs - 1) & 1, misc)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
-              for (int j = 0; j < n; ++j) {
-                const int g = j & 1;
-                if (j + 2 < n && !(ok = take(&ks))) break;
-                if (!(ok = take_v(&vs, sg->kt0 + j))) break;
-                if (!(ok = take_p(g))) break;
-                pv(g, vs, j < 2);
-                ptx::tc_commit(empty + vs);
-                if (j + 2 < n) {
-                  qk(g, ks);
-                  ptx::tc_commit(empty + ks);
-                  if (j + 3 == n) ptx::tc_commit(q_empty);
-                }
-              }
+              if (masked) clean_par ^= 1u << slot;
+            }
+            if (ok && !TWO && g == 1 && (n & 1)) {
+              if ((ok = my_turn())) ptx::mbar_arrive(turn);
             }
             if (!ok) break;
             ptx::tc_commit(o_final);
-            ++segs;
+            use += 2 * n;
           }
           ptx::mbar_arrive(seg_empty + i % kSegRing);
         }
         ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
         ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
       }
-    } else if (!GATHER) {  // --------------------------------------------- V cleaning warps
+    } else if (!GATHER) {  // ------------------------------------------------ V cleaning warp
       uint32_t use = 0, dirty_par = 0;
       bool ok = true;
-      const int part_id = warp - 10;
       const Seg* sg;
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
-        constexpr int kAhead = TWO ? 1 : 2;
         const int n = sg->n;
         for (int j = max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
-          // before tile j's V come the V tiles [0, j) and the K tiles [0, j + kAhead]
-          const uint32_t u = use + uint32_t(min(n, j + kAhead + 1) + j);
+          const uint32_t u = use + v_use<C::kAhead>(j, n);
           const uint32_t slot = u % C::kStages;
           // The producer says when it has begun to fill the slot with this tile: the slot's
           // full barrier is then in this tile's phase, not one of the same parity before.
@@ -672,7 +666,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const int live = sg->end - (sg->kt0 + j) * kTileKeys;  // rows of the tile that some row sees
           bool bad = false;
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
-          for (int x = part_id * 32 + lane; x < C::kTileBytes / 16; x += 64) {
+#pragma unroll 4
+          for (int x = lane; x < C::kTileBytes / 16; x += 32) {
             uint4* w = reinterpret_cast<uint4*>(v) + x;
             const int key = (x & (C::kHalf / 16 - 1)) >> 3;
             if (key >= live) {
