@@ -155,13 +155,14 @@ __device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, in
 constexpr int kAttnMaxRuns = 152;
 constexpr int kAttnMaxRunSeqs = 8192;
 constexpr int kAttnDirectItems = 6;
+constexpr int kAttnJoinBytes = 64;   // per run: what the join of the rows before it needs
 inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
   const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned
   return int(rows < tile_rows ? rows : tile_rows);
 }
 // Partial results of the persistent form: two per run, [rows][D] fp32 and (m, l) per row.
 inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
-  return size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
+  return size_t(kAttnMaxRuns) * kAttnJoinBytes + size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
 }
 
 // Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens

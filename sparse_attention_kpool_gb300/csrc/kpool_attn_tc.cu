@@ -110,7 +110,7 @@ struct Seg {
   int end;         // keys that some row sees
   int all;         // keys that every row sees
   int8_t whole;    // no other CTA has tiles of these rows
-  int8_t slot;     // partial slot of the CTA (0: the run's first segment, 1: a later one)
+  int8_t slot;     // partial slot of the CTA: 0 when an earlier run began the item, else 1
 };
 static_assert(sizeof(Seg) <= 64, "Seg fits its space");
 
@@ -119,21 +119,27 @@ __device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, 
   return max(1, (end + kTileKeys - 1) / kTileKeys);
 }
 
+// Beginning and finishing an item (Q, first product, epilogue) takes about as long as this
+// many tiles; it is counted when runs are cut, as positions before the item's first tile.
+constexpr int kItemCost = 2;
+
 __device__ __forceinline__ int64_t seq_cost(const AttnParams& p, const AttnSeq& s, int ttb) {
   int64_t c = 0;
-  for (int t = 0; t * ttb < s.nq; ++t) c += tile_cost(p, s, t, ttb);
+  for (int t = 0; t * ttb < s.nq; ++t) c += kItemCost + tile_cost(p, s, t, ttb);
   return c * p.Hkv;
 }
 
 // The segments of a CTA. Positions number the K/V tiles of the call: by sequence, key
-// head, row tile, then key tile; a row tile without any key counts as one.
+// head, row tile, then key tile (after kItemCost positions for the item itself); a row tile
+// without any key counts as one. A border among an item's first positions lies before its first tile.
 struct SegIter {
-  int64_t pos, hi, lo, base, cost;
-  int b;
+  int64_t pos, hi, base, cost;
+  int64_t first_tile;  // position of the first tile of the segment's item
+  int b, tiles;        // sequence; K/V tiles of the item
   AttnSeq sq;
 
   __device__ __forceinline__ void start(const AttnParams& p, const Misc* m, int ttb) {
-    lo = pos = m->lo;
+    pos = m->lo;
     hi = m->hi;
     base = m->base;
     b = m->b;
@@ -155,16 +161,23 @@ struct SegIter {
     s->hk = int((pos - base) / per_head);
     int64_t off = (pos - base) - s->hk * per_head;
     int t = 0, c = tile_cost(p, sq, 0, ttb);
-    while (off >= c) {
-      off -= c;
+    while (off >= kItemCost + c) {
+      off -= kItemCost + c;
       c = tile_cost(p, sq, ++t, ttb);
     }
+    const int64_t tile0 = pos - off + kItemCost;  // position of the item's first tile
+    if (hi <= tile0) {                            // (only as the run's last item)
+      pos = hi;
+      return false;
+    }
     s->tok0 = t * ttb;
-    s->kt0 = int(off);
-    s->n = int(min(int64_t(c) - off, hi - pos));
+    s->kt0 = int(max(pos - tile0, int64_t(0)));
+    s->n = int(min(int64_t(c), hi - tile0)) - s->kt0;
+    tiles = c;
     s->whole = s->n == c;
-    s->slot = pos == lo ? 0 : 1;
-    pos += s->n;
+    s->slot = s->kt0 > 0 ? 0 : 1;
+    first_tile = tile0;
+    pos = tile0 + s->kt0 + s->n;
     return true;
   }
 };
@@ -188,7 +201,7 @@ __device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int til
 // rows, then key heads (the heads of a token lie together in memory).
 __device__ __forceinline__ int gather_tiles(const AttnParams& p) { return max(1, (p.width + kTileKeys - 1) / kTileKeys); }
 
-__device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, int64_t lo, int64_t hi, Seg* s) {
+__device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, int64_t hi, Seg* s) {
   if (*pos >= hi) return false;
   const int nt = gather_tiles(p);
   const int64_t item = *pos / nt;
@@ -197,7 +210,7 @@ __device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, in
   s->kt0 = int(*pos - item * nt);
   s->n = int(min(int64_t(nt - s->kt0), hi - *pos));
   s->whole = s->n == nt;
-  s->slot = *pos == lo ? 0 : 1;
+  s->slot = s->kt0 > 0 ? 0 : 1;
   *pos += s->n;
   attn_selected_seq(p, r, &s->sq.k0, &s->sq.nk);
   s->sq.q0 = r;
@@ -262,6 +275,36 @@ __device__ __forceinline__ int64_t find_run(const AttnParams& p, int ttb, int64_
   return m->total;
 }
 
+// What the join of the rows that the border before run r cuts needs; runs = 0: nothing to join here.
+struct JoinItem {
+  int64_t item, total;   // position of the first tile of the rows' item, positions of the call
+  int32_t tiles;         // K/V tiles of the item
+  int32_t runs;
+  int32_t q0, nq;        // query rows of the sequence
+  int32_t tok0, hk;
+  int32_t pad[6];
+};
+static_assert(sizeof(JoinItem) == kAttnJoinBytes, "join items are laid out in the workspace");
+
+// Run r begins with the segment s of an item of c tiles, the first at position tile0. The join is
+// left to the first non-empty run that begins inside an item.
+__device__ __forceinline__ void write_join(JoinItem* out, const Seg& s, int64_t tile0, int c, int64_t total, int r,
+                                           int n) {
+  JoinItem j{};
+  j.item = tile0;
+  bool own = s.kt0 > 0;
+  const int64_t pos = total * r / n;
+  for (int b = r - 1; own && b > 0 && total * b / n > tile0; --b) own = total * b / n == pos;
+  j.total = total;
+  j.tiles = c;
+  j.runs = own ? n : 0;
+  j.q0 = s.sq.q0;
+  j.nq = s.sq.nq;
+  j.tok0 = s.tok0;
+  j.hk = s.hk;
+  *out = j;
+}
+
 // ------------------------------------------------------------------------- waits
 
 // Bounded wait; also gives up when another role did.
@@ -322,7 +365,7 @@ template <int D, Form F>
 __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
-                   int direct, float* part, int slot_rows, WorkspaceHeader* hdr) {
+                   int direct, float* part, int slot_rows, JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<D, F>;
   constexpr bool TWO = C::TWO, GATHER = F == kGather;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -402,12 +445,18 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (GATHER && warp == 8) {
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
-        const int64_t lo = misc->lo, hi = misc->hi;
-        int64_t pos = lo;
+        const int64_t hi = misc->hi;
+        int64_t pos = misc->lo;
         uint32_t q_loads = 0;
         Seg sg{};
         for (int i = 0;; ++i) {
-          const bool more = gather_seg(p, &pos, lo, hi, &sg);
+          const int64_t at = pos;
+          const bool more = gather_seg(p, &pos, hi, &sg);
+          if (i == 0) {
+            const int nt = gather_tiles(p);
+            if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, int64_t(p.R) * p.Hkv * nt, blockIdx.x, gridDim.x);
+            else joins[blockIdx.x].runs = 0;
+          }
           if (!more) sg.n = -1;
           if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
           ring[i % kSegRing] = sg;
@@ -505,6 +554,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         };
         for (int i = 0;; ++i) {
           const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          if (i == 0 && !direct) {
+            if (more) write_join(joins + blockIdx.x, sg, it.first_tile, it.tiles, misc->total, blockIdx.x, gridDim.x);
+            else joins[blockIdx.x].runs = 0;
+          }
           if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
           if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
           ring[i % kSegRing] = sg;
@@ -947,92 +1000,97 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 
 // ------------------------------------------------------------------------------- join
 //
-// CTA i (x) looks at the border between the runs i and i + 1 of the persistent kernel. If
-// it cuts the rows of one item, and is the first border to do so, the CTA adds up that item's
-// partial results in the order of the runs. y: 8 rows each, a warp per row, its lanes the channels.
-constexpr int kJoinRows = 8;
+// CTA x adds up, in the order of the runs, the partial results of the rows that the border
+// before run x + 1 cuts (if that run was the first to begin inside them: its producer left the
+// item's data). y: 32 rows each, four at a time to a warp, a lane holds D / 32 channels. Reads a
+// few MB that the runs have just written, from L2.
+constexpr int kJoinRows = 32;
 
-template <int D, bool GATHER>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int tt, int ttb, int runs,
-                                                        const float* part, int slot_rows) {
-  extern __shared__ int64_t scratch[];
-  __shared__ Misc m;
-  const int64_t bi = int64_t(blockIdx.x) + 1;
-  int64_t total, item;
-  int c, hk, t = 0;
-  AttnSeq sq{};
-  if (GATHER) {
-    c = gather_tiles(p);
-    total = int64_t(p.R) * p.Hkv * c;
-  } else {
-    total = find_run(p, ttb, scratch, bi, runs, &m);
-  }
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_join_kernel(const __grid_constant__ AttnParams p, int tt, const JoinItem* joins, const float* part,
+                     int slot_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
-  const int64_t pos = total * bi / runs;
-  // an empty run starts where the next one does: that one's border is looked at there
-  if (total == 0 || pos >= total * (bi + 1) / runs) return;
-  if (GATHER) {
-    const int64_t number = pos / c;
-    item = number * c;
-    sq.q0 = int(number / p.Hkv);
-    sq.nq = 1;
-    hk = int(number - int64_t(sq.q0) * p.Hkv);
-  } else {
-    sq = attn_seq(p, m.b);
-    const int64_t per_head = seq_cost(p, sq, ttb) / p.Hkv;
-    hk = int((pos - m.base) / per_head);
-    item = m.base + hk * per_head;
-    c = tile_cost(p, sq, 0, ttb);
-    while (pos >= item + c) {
-      item += c;
-      c = tile_cost(p, sq, ++t, ttb);
+  const JoinItem it = joins[blockIdx.x + 1];
+  if (it.runs == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the runs that hold tiles of the item: from `first` while they begin before its end
+  auto run_lo = [&](int64_t r) { return it.total * r / it.runs; };
+  int first = blockIdx.x;
+  while (first > 0 && run_lo(first) > it.item) --first;
+  const float c2 = p.scale * kLog2e;
+  constexpr int kPer = D / 32;
+  const size_t stride = size_t(slot_rows) * (D + 2);
+  // the warp's rows: four of the block's 32
+  int vr[4], tok[4];
+  float acc[4][kPer], mm[4], ll[4];
+  bool any = false;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    vr[x] = blockIdx.y * kJoinRows + warp * 4 + x;
+    const int q_tile = vr[x] / kTileRows, row = vr[x] - q_tile * kTileRows, in = row / p.G;
+    tok[x] = vr[x] < slot_rows && in < tt && it.tok0 + q_tile * tt + in < it.nq ? it.tok0 + q_tile * tt + in : -1;
+    any |= tok[x] >= 0;
+    mm[x] = -INFINITY;
+    ll[x] = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[x][y] = 0.0f;
+  }
+  if (!any) return;
+  for (int64_t r = first; r < it.runs; ++r) {
+    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
+    if (lo >= it.item + it.tiles) break;
+    if (hi <= it.item || hi == lo) continue;
+    const float* s = part + (size_t(r) * 2 + (lo > it.item ? 0 : 1)) * stride;
+    float o[4][kPer];
+    float2 ml[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (tok[x] < 0) continue;
+      ml[x] = *reinterpret_cast<const float2*>(s + size_t(slot_rows) * D + 2 * vr[x]);
+      if (D == 128) {
+        const float4 f = *reinterpret_cast<const float4*>(s + size_t(vr[x]) * D + 4 * lane);
+        o[x][0] = f.x;
+        o[x][1] = f.y;
+        o[x][kPer - 2] = f.z;
+        o[x][kPer - 1] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(s + size_t(vr[x]) * D + 2 * lane);
+        o[x][0] = f.x;
+        o[x][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (tok[x] < 0) continue;
+      const float mn = fmaxf(mm[x], ml[x].x);
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float f = mm[x] == -INFINITY ? 1.0f : exp2f((mm[x] - base) * c2);
+      // a part without any weight adds nothing; with a NaN among its scores its sum passes on
+      const float w = ml[x].x == -INFINITY ? 1.0f : exp2f((ml[x].x - base) * c2);
+      ll[x] = ll[x] * f + ml[x].y * w;
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) acc[x][y] = acc[x][y] * f + o[x][y] * w;
+      mm[x] = mn;
     }
   }
-  if (item == pos) return;                          // the border falls between two items
-  // runs that hold tiles of the item: first is the one that contains its first tile
-  auto run_lo = [&](int64_t r) { return total * r / runs; };
-  int64_t first = bi - 1;
-  while (first > 0 && run_lo(first) > item) --first;
-  // the first border inside the item with a non-empty run behind it does the work
-  for (int64_t r = first + 1; r < bi; ++r)
-    if (run_lo(r) > item && run_lo(r) < run_lo(r + 1)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t item_end = item + c;
-  const float c2 = p.scale * kLog2e;
-  const int rows_q = kTileRows;
-  const int vr = blockIdx.y * kJoinRows + warp;
-  if (vr >= slot_rows) return;
-  const int q_tile = vr / rows_q, row = vr - q_tile * rows_q;
-  const int tok_in = row / p.G, i = t * ttb + q_tile * tt + tok_in;
-  if (tok_in >= tt || i >= sq.nq) return;
-  constexpr int kPer = D / 32;
-  float acc[kPer], mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) acc[x] = 0.0f;
-  for (int64_t r = first; r < runs && run_lo(r) < item_end; ++r) {
-    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
-    if (hi <= item || hi == lo) continue;
-    const int slot = lo >= item ? 0 : 1;
-    const float* s = part + (size_t(r) * 2 + slot) * size_t(slot_rows) * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(s + size_t(slot_rows) * D + 2 * vr);
-    const float mn = fmaxf(mm, ml.x);
-    const float base = mn == -INFINITY ? 0.0f : mn;
-    const float f = mm == -INFINITY ? 1.0f : exp2f((mm - base) * c2);
-    // a part without any weight adds nothing; with a NaN among its scores its sum passes on
-    const float w = ml.x == -INFINITY ? 1.0f : exp2f((ml.x - base) * c2);
-    ll = ll * f + ml.y * w;
+  for (int x = 0; x < 4; ++x) {
+    if (tok[x] < 0) continue;
+    const bool none = mm[x] == -INFINITY && ll[x] == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / ll[x];
+    const int head = it.hk * p.G + (vr[x] % kTileRows) % p.G;
+    const int64_t row = int64_t(it.q0) + tok[x];
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.o_ts + int64_t(head) * p.o_hs + kPer * lane;
+    uint32_t u[kPer / 2];
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * f + s[size_t(vr) * D + x * 32 + lane] * w;
-    mm = mn;
+    for (int y = 0; y < kPer / 2; ++y)
+      u[y] = none ? 0u : ptx::pack_bf16(acc[x][2 * y] * inv, acc[x][2 * y + 1] * inv);
+    if (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[kPer / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(dst) = u[0];
+    if (lane == 0 && p.lse)
+      p.lse[row * p.Hq + head] = none ? -INFINITY : (mm[x] * c2 + log2f(ll[x])) * kLn2;
   }
-  const bool none = mm == -INFINITY && ll == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / ll;
-  const int head = hk * p.G + (row - tok_in * p.G);
-  const int64_t grow_row = int64_t(sq.q0) + i;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + grow_row * p.o_ts + int64_t(head) * p.o_hs;
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) dst[x * 32 + lane] = __float2bfloat16_rn(none ? 0.0f : acc[x] * inv);
-  if (lane == 0 && p.lse) p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (mm * c2 + log2f(ll)) * kLn2;
 }
 
 template <int D, Form F>
@@ -1061,29 +1119,26 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
-  float* part = reinterpret_cast<float*>(ws + sizeof(WorkspaceHeader));
+  JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader));
+  float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   auto kernel = attn_tc_kernel<D, F>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, hdr);
+  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, joins, hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || grid < 2) return e;
-  auto join = attn_join_kernel<D, GATHER>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = GATHER ? 0 : size_t(p.S) * 8;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxRunSeqs * 8);
-  if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, join, p, tt, ttb, grid, static_cast<const float*>(part),
-                         slot_rows);
+  e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p, tt, static_cast<const JoinItem*>(joins),
+                         static_cast<const float*>(part), slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
