@@ -155,6 +155,7 @@ __device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, in
 constexpr int kAttnMaxRuns = 152;
 constexpr int kAttnMaxRunSeqs = 8192;
 constexpr int kAttnDirectItems = 6;
+constexpr int kAttnDirectKeys = 8192;
 constexpr int kAttnJoinBytes = 64;   // per run: what the join of the rows before it needs
 inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
   const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned

@@ -123,60 +123,102 @@ __device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, 
 // many tiles; it is counted when runs are cut, as positions before the item's first tile.
 constexpr int kItemCost = 2;
 
+// sum over i in [0, n) of floor((a i + b) / m), in steps of Euclid's algorithm on (m, a)
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  int64_t ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += int64_t(n) * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += int64_t(n) * (b / m);
+      b %= m;
+    }
+    const uint64_t y = uint64_t(a) * n + b;
+    if (y < m) break;
+    n = uint32_t(y / m);
+    b = uint32_t(y % m);
+    const uint32_t x = m;
+    m = a;
+    a = x;
+  }
+  return ans;
+}
+
+__device__ __forceinline__ int row_tiles(const AttnSeq& s, int ttb) { return (s.nq + ttb - 1) / ttb; }
+
+// Positions of one head's row tiles [0, t), t <= row_tiles: tile u ends at key prefix + (u + 1) ttb
+// (the last at prefix + nq) and counts at least one key tile.
+__device__ __forceinline__ int64_t head_cost(const AttnParams& p, const AttnSeq& s, int t, int ttb) {
+  if (t == 0) return 0;
+  if (!s.ok || s.nk == 0) return int64_t(t) * (kItemCost + 1);
+  if (p.mask != nullptr) return int64_t(t) * (kItemCost + (s.nk + kTileKeys - 1) / kTileKeys);
+  const int nt = row_tiles(s, ttb), m = min(t, nt - 1);
+  const int z = s.prefix < 0 ? min(m, -s.prefix / ttb) : 0;  // tiles without any key
+  int64_t c = int64_t(t) * kItemCost + z;
+  c += floor_sum(uint32_t(m - z), kTileKeys, uint32_t(ttb), uint32_t(s.prefix + (z + 1) * ttb + kTileKeys - 1));
+  if (t == nt) c += max(1, (s.prefix + s.nq + kTileKeys - 1) / kTileKeys);
+  return c;
+}
+
 __device__ __forceinline__ int64_t seq_cost(const AttnParams& p, const AttnSeq& s, int ttb) {
-  int64_t c = 0;
-  for (int t = 0; t * ttb < s.nq; ++t) c += kItemCost + tile_cost(p, s, t, ttb);
-  return c * p.Hkv;
+  return head_cost(p, s, row_tiles(s, ttb), ttb) * p.Hkv;
 }
 
 // The segments of a CTA. Positions number the K/V tiles of the call: by sequence, key
 // head, row tile, then key tile (after kItemCost positions for the item itself); a row tile
 // without any key counts as one. A border among an item's first positions lies before its first tile.
 struct SegIter {
-  int64_t pos, hi, base, cost;
-  int64_t first_tile;  // position of the first tile of the segment's item
-  int b, tiles;        // sequence; K/V tiles of the item
+  int64_t pos, hi;
+  int64_t item;            // first position of the present item
+  int b, hk, t, nt, c;     // its sequence, key head and row tile; the head's row tiles, the item's key tiles
   AttnSeq sq;
 
   __device__ __forceinline__ void start(const AttnParams& p, const Misc* m, int ttb) {
     pos = m->lo;
     hi = m->hi;
-    base = m->base;
     b = m->b;
-    if (pos < hi) {
-      sq = attn_seq(p, b);
-      cost = seq_cost(p, sq, ttb);
+    if (pos >= hi) return;
+    sq = attn_seq(p, b);
+    nt = row_tiles(sq, ttb);
+    const int64_t per_head = head_cost(p, sq, nt, ttb), off = pos - m->base;
+    hk = int(off / per_head);
+    const int64_t in_head = off - hk * per_head;
+    t = 0;
+    for (int top = nt - 1; t < top;) {  // the last tile that begins at or before the position
+      const int mid = (t + top + 1) >> 1;
+      if (head_cost(p, sq, mid, ttb) <= in_head) t = mid; else top = mid - 1;
     }
+    item = pos - (in_head - head_cost(p, sq, t, ttb));
+    c = tile_cost(p, sq, t, ttb);
   }
+  __device__ __forceinline__ int64_t first_tile() const { return item + kItemCost; }
   __device__ __forceinline__ bool next(const AttnParams& p, int ttb, Seg* s) {
     if (pos >= hi) return false;
-    while (pos >= base + cost) {
-      base += cost;
-      ++b;
-      sq = attn_seq(p, b);
-      cost = seq_cost(p, sq, ttb);
+    if (pos == first_tile() + c) {  // the item is done
+      item = pos;
+      if (++t == nt) {
+        t = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          do {
+            sq = attn_seq(p, ++b);
+          } while (sq.nq == 0);
+          nt = row_tiles(sq, ttb);
+        }
+      }
+      c = tile_cost(p, sq, t, ttb);
     }
-    const int64_t per_head = cost / p.Hkv;
+    const int64_t tile0 = first_tile();
+    if (hi <= tile0) return false;  // (only as the run's last item)
     s->sq = sq;
-    s->hk = int((pos - base) / per_head);
-    int64_t off = (pos - base) - s->hk * per_head;
-    int t = 0, c = tile_cost(p, sq, 0, ttb);
-    while (off >= kItemCost + c) {
-      off -= kItemCost + c;
-      c = tile_cost(p, sq, ++t, ttb);
-    }
-    const int64_t tile0 = pos - off + kItemCost;  // position of the item's first tile
-    if (hi <= tile0) {                            // (only as the run's last item)
-      pos = hi;
-      return false;
-    }
+    s->hk = hk;
     s->tok0 = t * ttb;
     s->kt0 = int(max(pos - tile0, int64_t(0)));
     s->n = int(min(int64_t(c), hi - tile0)) - s->kt0;
-    tiles = c;
     s->whole = s->n == c;
     s->slot = s->kt0 > 0 ? 0 : 1;
-    first_tile = tile0;
     pos = tile0 + s->kt0 + s->n;
     return true;
   }
@@ -555,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         for (int i = 0;; ++i) {
           const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
           if (i == 0 && !direct) {
-            if (more) write_join(joins + blockIdx.x, sg, it.first_tile, it.tiles, misc->total, blockIdx.x, gridDim.x);
+            if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, gridDim.x);
             else joins[blockIdx.x].runs = 0;
           }
           if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
@@ -1112,10 +1154,8 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
-  // One CTA per row tile once there are several per SM (the hardware deals them out, deepest
-  // first); below that equal runs of K/V tiles, whose join costs a few microseconds. The forms of
-  // one row tile always take runs: their items are short, and a persistent CTA pays its start once.
-  const bool direct = !GATHER && (p.S > kAttnMaxRunSeqs || (C::TWO && items >= int64_t(kAttnDirectItems) * sms));
+  const bool direct = !GATHER && (p.S > kAttnMaxRunSeqs || (C::TWO && items >= int64_t(kAttnDirectItems) * sms &&
+                                                            p.T >= int64_t(kAttnDirectKeys) * p.S));
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
