@@ -121,7 +121,7 @@ __device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, 
 
 // Beginning and finishing an item (Q, first product, epilogue) takes about as long as this
 // many tiles; it is counted when runs are cut, as positions before the item's first tile.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 4;
 
 // sum over i in [0, n) of floor((a i + b) / m), in steps of Euclid's algorithm on (m, a)
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
@@ -398,6 +398,25 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnSeq
 
 // K/V tile kt holds keys that some row of the segment does not see.
 __device__ __forceinline__ bool tile_masked(const Seg* s, int kt) { return (kt + 1) * kTileKeys > s->all; }
+
+// Transposes 4 x 4 pieces of 16 bytes within each quad of lanes: piece r of lane i becomes piece i of
+// lane r. A thread holds a row of the result; after this four lanes hold 64 contiguous bytes of one row,
+// and a store instruction of the warp touches 8 lines instead of 32.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int d) {  // lanes without bit d give b and get b, the others a
+    const bool up = lane & d;
+    uint4 t = up ? a : b;
+    t.x = __shfl_xor_sync(0xffffffffu, t.x, d);
+    t.y = __shfl_xor_sync(0xffffffffu, t.y, d);
+    t.z = __shfl_xor_sync(0xffffffffu, t.z, d);
+    t.w = __shfl_xor_sync(0xffffffffu, t.w, d);
+    if (up) a = t; else b = t;
+  };
+  swap(v[0], v[1], 1);
+  swap(v[2], v[3], 1);
+  swap(v[0], v[2], 2);
+  swap(v[1], v[3], 2);
+}
 
 __device__ __forceinline__ bool bad_bf16(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
 
@@ -747,8 +766,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       bool ok = true;
       const Seg* sg;
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
-        const int n = sg->n;
-        for (int j = max(0, sg->all / kTileKeys - sg->kt0); j < n; ++j) {
+        const int n = sg->n, kt0 = sg->kt0;
+        for (int j = max(0, sg->all / kTileKeys - kt0); j < n; ++j) {
           const uint32_t u = use + v_use<C::kAhead>(j, n);
           const uint32_t slot = u % C::kStages;
           // The producer says when it has begun to fill the slot with this tile: the slot's
@@ -758,33 +777,34 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           dirty_par ^= 1u << slot;
           if (!ok) break;
           uint8_t* v = smem + C::kOffRing + slot * C::kTileBytes;
-          const int live = sg->end - (sg->kt0 + j) * kTileKeys;  // rows of the tile that some row sees
+          // Keys before `seen` are seen by every row and stay as they are; keys from `live` on by none.
+          const int base = (kt0 + j) * kTileKeys, live = sg->end - base, seen = max(0, sg->all - base);
           bool bad = false;
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
-#pragma unroll 4
-          for (int x = lane; x < C::kTileBytes / 16; x += 32) {
-            uint4* w = reinterpret_cast<uint4*>(v) + x;
-            const int key = (x & (C::kHalf / 16 - 1)) >> 3;
-            if (key >= live) {
-              *w = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 q = *w;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&q);
-            bool hit = false;
+          for (int h = 0; h < C::kBlocks; ++h) {
+            uint4* block = reinterpret_cast<uint4*>(v + h * C::kHalf);
+#pragma unroll 8
+            for (int x = seen * 8 + lane; x < kTileKeys * 8; x += 32) {
+              if ((x >> 3) >= live) {
+                block[x] = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 q = block[x];
+                // an exponent of all ones carries into bit 15 or 31
+                constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+                if ((((q.x & kExp) + kOne) | ((q.y & kExp) + kOne) | ((q.z & kExp) + kOne) | ((q.w & kExp) + kOne)) &
+                    0x80008000u) {
+                  bad = true;
+                  uint4 f = q;
+                  uint32_t* e = reinterpret_cast<uint32_t*>(&f);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if (bad_bf16(e[y])) {
-                e[y] &= 0xFFFF0000u;
-                hit = true;
-              }
-              if (bad_bf16(e[y] >> 16)) {
-                e[y] &= 0x0000FFFFu;
-                hit = true;
+                  for (int y = 0; y < 4; ++y) {
+                    if (bad_bf16(e[y])) e[y] &= 0xFFFF0000u;
+                    if (bad_bf16(e[y] >> 16)) e[y] &= 0x0000FFFFu;
+                  }
+                  block[x] = f;
+                }
               }
             }
-            if (hit) *w = q;
-            bad |= hit;
           }
           if (bad) misc->bad_seg[i % kSegRing] = i + 1;
           ptx::fence_proxy_async_smem();
@@ -937,6 +957,16 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       const int64_t grow_row = int64_t(sg->sq.q0) + i;
       const int head = sg->hk * p.G + head_in;
       const float inv = none ? 0.0f : 1.0f / l;
+      // where this lane's pieces of the quad's rows go
+      int64_t out_at[4];
+      {
+        const int64_t own = valid ? grow_row * p.o_ts + int64_t(head) * p.o_hs : -1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          out_at[r] = __shfl_sync(0xffffffffu, own, (lane & 28) + r);
+          if (out_at[r] >= 0) out_at[r] += (TWO ? 0 : g * (D / 2)) + 8 * (lane & 3);
+        }
+      }
       const int prow = TWO ? g * kTileRows + row : row;
       float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slot_rows) * (D + 2);
       // columns of this thread: all (two), or the group's half (one)
@@ -969,7 +999,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         }
         if (fix && valid && !none) {
           // infinities and NaN that the cleaning took out of V: a row that sees them gets them back
-          const int j0 = max(sg->kt0 * kTileKeys, sg->all) & ~(kTileKeys - 1);
+          const int j0 = max(sg->kt0 * kTileKeys, sg->all);
           const int j1 = min((sg->kt0 + n_all) * kTileKeys, sg->end);
           const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + int64_t(sg->hk) * p.v_hs + col0 + 32 * c;
           for (int j = j0; j < j1; ++j) {
@@ -985,27 +1015,33 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           }
         }
         if (sg->whole) {
-          if (valid) {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + grow_row * p.o_ts + int64_t(head) * p.o_hs +
-                                 col0 + 32 * c;
+          uint4 u[4];
+          uint32_t* e = reinterpret_cast<uint32_t*>(u);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 u;
-              uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+          for (int x = 0; x < 16; ++x)
+            e[x] = none ? 0u
+                        : ptx::pack_bf16(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+          quad_transpose(u, lane);
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                e[y] = none ? 0u
-                            : ptx::pack_bf16(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                             __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 8 * x) = u;
+          for (int r = 0; r < 4; ++r) {
+            if (out_at[r] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + out_at[r] + 32 * c) = u[r];
+          }
+        } else {
+          float* dst = pslot + col0 + 32 * c + 4 * (lane & 3);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 u[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              u[x] = make_uint4(o[16 * h + 4 * x], o[16 * h + 4 * x + 1], o[16 * h + 4 * x + 2], o[16 * h + 4 * x + 3]);
+            quad_transpose(u, lane);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int to = (prow & ~3) + r;
+              if (to < slot_rows) *reinterpret_cast<uint4*>(dst + size_t(to) * D + 16 * h) = u[r];
             }
           }
-        } else if (prow < slot_rows) {
-          float4* dst = reinterpret_cast<float4*>(pslot + size_t(prow) * D + col0 + 32 * c);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                 __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
         }
       }
       if (TWO || g == 0) {
