@@ -845,33 +845,33 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         if (!ok) break;
         ++s_uses;
         ptx::tc_fence_after();
+        // Keys that some row does not see: -inf over their scores in TMEM, 32 columns at a time and only
+        // where a row of the warp needs it. (As straight code on the 128 registers below it took three
+        // times as long: it runs once or twice per row tile and is fetched anew each time.)
+        if (GATHER || tile_masked(sg, kt)) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
+          const int im = min(i, sg->sq.nq - 1);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = GATHER ? w[c] : seen_bits(p, sg->sq, im, kt * kTileKeys + 32 * c);
+            if (!__any_sync(0xffffffffu, bits != 0xffffffffu)) continue;
+            uint32_t x32[32];
+            ptx::tc_ld_32x32b_x32(s_col + 32 * c, x32);
+            ptx::tc_wait_ld();
+            ptx::tc_reg_fence(x32);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((bits >> x) & 1u)) x32[x] = 0xFF800000u;  // -inf
+            ptx::tc_st_32x32b_x32(s_col + 32 * c, x32);
+          }
+          ptx::tc_wait_st();
+        }
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tc_ld_32x32b_x32(s_col + 32 * c, s[c]);
         ptx::tc_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tc_reg_fence(s[c]);
-        if (GATHER) {
-          const uint4 w = reinterpret_cast<const uint4*>(smem + C::kOffBits)[(tile + j) % kBitsRing];
-          if ((w.x & w.y & w.z & w.w) != 0xffffffffu) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t bits = c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w;
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;  // -inf
-            }
-          }
-        } else if (tile_masked(sg, kt)) {
-          const int im = min(i, sg->sq.nq - 1);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = seen_bits(p, sg->sq, im, kt * kTileKeys + 32 * c);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;  // -inf
-          }
-        }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       constexpr int kCols = TWO ? D : D / 2;
       const int col0 = TWO ? 0 : g * kCols;
       const uint32_t oa = tmem + lane_base + 256 + (TWO ? g * D : 0) + col0, ob = tmem + lane_base + 256 + D + col0;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kCols / 32; ++c) {
         uint32_t o[32];
 #pragma unroll
