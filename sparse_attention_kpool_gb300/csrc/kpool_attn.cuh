@@ -16,6 +16,15 @@ namespace kpool {
 
 enum AttnMode { kAttnPrompt = 0, kAttnTree = 1, kAttnSelected = 2 };
 
+// A prompt's selection as masked dense attention (kpool_attn_dense.cu): written on the device by
+// the call's first kernels.
+struct AttnDense {
+  int32_t words;     // 32-bit words of a row of the mask, a multiple of 4
+  int32_t enabled;   // the mask fits: the dense kernel works, the gathering one only on the listed rows
+  int32_t causal;    // no row selected a key after its own
+  int32_t listed;    // rows that name a key twice
+};
+
 struct AttnParams {
   const void* q;
   const void* k;
@@ -30,6 +39,8 @@ struct AttnParams {
   const int32_t* ids;                        // [R, width] (selected)
   const int32_t* row_seq;                    // [R] or null (selected)
   int32_t mask_words, width;
+  const AttnDense* dense;                    // null, or what the dense form of a selection goes by
+  const int32_t* list;                       // with dense, gathering: the listed rows
   int32_t S, R;
   int64_t T;
   int32_t Hq, Hkv, G, D;
@@ -64,7 +75,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
   s.nq = int32_t(q1 - s.q0);
   const int64_t extent = k1 - s.k0;
   if (p.mode == kAttnTree) {
-    const int64_t pre = __ldg(p.prefix + b);
+    const int64_t pre = p.prefix ? __ldg(p.prefix + b) : 0;
     if (pre < 0 || pre + s.nq > extent) {
       s.ok = false;
       s.nk = s.prefix = 0;
@@ -79,19 +90,29 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
   return s;
 }
 
+__device__ __forceinline__ int attn_mask_words(const AttnParams& p) {
+  return p.dense ? __ldg(&p.dense->words) : p.mask_words;
+}
+
+// No row sees keys after prefix + its own index (without a mask, or by what the mask was made from).
+__device__ __forceinline__ bool attn_causal(const AttnParams& p) {
+  return p.mask == nullptr || (p.dense && __ldg(&p.dense->causal));
+}
+
 // Does row i of the sequence (global query row q0 + i) see key j? (prompt, tree; j < nk)
 __device__ __forceinline__ bool attn_sees(const AttnParams& p, const AttnSeq& s, int i, int j) {
   const int slot = j - s.prefix;
   if (p.mask == nullptr) return slot <= i;
   if (slot < 0) return true;
-  if (slot >= 32 * p.mask_words || slot >= s.nq) return false;
-  return (uint32_t(__ldg(p.mask + int64_t(s.q0 + i) * p.mask_words + (slot >> 5))) >> (slot & 31)) & 1u;
+  const int words = attn_mask_words(p);
+  if (slot >= 32 * words || slot >= s.nq) return false;
+  return (uint32_t(__ldg(p.mask + int64_t(s.q0 + i) * words + (slot >> 5))) >> (slot & 31)) & 1u;
 }
 
 // Keys [0, end) hold every key that some row before i1 sees.
 __device__ __forceinline__ int attn_keys_end(const AttnParams& p, const AttnSeq& s, int i1) {
   if (!s.ok || s.nk == 0) return 0;
-  if (p.mask != nullptr) return s.nk;
+  if (!attn_causal(p)) return s.nk;
   return int(max(int64_t(0), min(int64_t(s.nk), int64_t(s.prefix) + i1)));
 }
 
@@ -123,7 +144,7 @@ __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader*
     const int q = __ldg(p.cu_q + b);
     if (b == 0 ? q != 0 : q < __ldg(p.cu_q + b - 1)) bad = 1;
     if (b == p.S && q != p.R) bad = 1;
-    if (p.mode == kAttnTree && b < p.S) {
+    if (p.mode == kAttnTree && b < p.S && p.prefix) {
       const int64_t pre = __ldg(p.prefix + b);
       const int64_t rows = int64_t(__ldg(p.cu_q + b + 1)) - q, extent = int64_t(__ldg(p.cu_k + b + 1)) - k;
       if (pre < 0 || pre + rows > extent) bad = 1;
@@ -161,10 +182,22 @@ inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
   const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned
   return int(rows < tile_rows ? rows : tile_rows);
 }
-// Partial results of the persistent form: two per run, [rows][D] fp32 and (m, l) per row.
+// AttnDense, the runs' join items and the partial results of the persistent form: two per run,
+// [rows][D] fp32 and (m, l) per row.
 inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
-  return size_t(kAttnMaxRuns) * kAttnJoinBytes + size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
+  return 256 + size_t(kAttnMaxRuns) * kAttnJoinBytes + size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
 }
+
+// The dense form of a selection: whether the host tries it, the bytes of its mask for R rows, and the
+// kernels that fill the mask. (Longer prompts than the mask holds are gathered.)
+inline size_t attn_mask_bytes(int64_t R) {
+  const int64_t all = R * ((R + 127) / 128) * 16;
+  return size_t(all < (int64_t(128) << 20) ? all : (int64_t(128) << 20));
+}
+inline size_t attn_list_bytes(int64_t R) { return (size_t(R) * 4 + 255) & ~size_t(255); }
+bool attn_dense_wanted(const AttnParams& p);
+cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t* mask, int32_t* list,
+                                   cudaStream_t stream);
 
 // Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens
 // also strides that attn_gather_supported takes.

@@ -101,7 +101,8 @@ size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const k
   if (!shape_ok(shape) || !sizes_ok(q_rows, 0, num_seqs)) return 0;
   size_t bytes = sizeof(WorkspaceHeader);
   if (attn_tc_supported(kpool_dtype(shape->dtype), shape->head_dim))
-    bytes += attn_partial_bytes(q_rows, shape->q_heads / shape->kv_heads, shape->head_dim);
+    bytes += ((attn_partial_bytes(q_rows, shape->q_heads / shape->kv_heads, shape->head_dim) + 255) & ~size_t(255)) +
+             attn_list_bytes(q_rows) + attn_mask_bytes(q_rows);
   return bytes;
 }
 

@@ -153,7 +153,7 @@ __device__ __forceinline__ int row_tiles(const AttnSeq& s, int ttb) { return (s.
 __device__ __forceinline__ int64_t head_cost(const AttnParams& p, const AttnSeq& s, int t, int ttb) {
   if (t == 0) return 0;
   if (!s.ok || s.nk == 0) return int64_t(t) * (kItemCost + 1);
-  if (p.mask != nullptr) return int64_t(t) * (kItemCost + (s.nk + kTileKeys - 1) / kTileKeys);
+  if (!attn_causal(p)) return int64_t(t) * (kItemCost + (s.nk + kTileKeys - 1) / kTileKeys);
   const int nt = row_tiles(s, ttb), m = min(t, nt - 1);
   const int z = s.prefix < 0 ? min(m, -s.prefix / ttb) : 0;  // tiles without any key
   int64_t c = int64_t(t) * kItemCost + z;
@@ -243,12 +243,18 @@ __device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int til
 // rows, then key heads (the heads of a token lie together in memory).
 __device__ __forceinline__ int gather_tiles(const AttnParams& p) { return max(1, (p.width + kTileKeys - 1) / kTileKeys); }
 
+__device__ __forceinline__ int64_t gather_total(const AttnParams& p) {
+  const int rows = p.list && p.dense->enabled ? p.dense->listed : p.R;
+  return int64_t(rows) * p.Hkv * gather_tiles(p);
+}
+
 __device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, int64_t hi, Seg* s) {
   if (*pos >= hi) return false;
   const int nt = gather_tiles(p);
   const int64_t item = *pos / nt;
-  const int r = int(item / p.Hkv);
+  int r = int(item / p.Hkv);
   s->hk = int(item - int64_t(r) * p.Hkv);
+  if (p.list && p.dense->enabled) r = __ldg(p.list + r);
   s->kt0 = int(*pos - item * nt);
   s->n = int(min(int64_t(nt - s->kt0), hi - *pos));
   s->whole = s->n == nt;
@@ -384,8 +390,9 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnSeq
   if (p.mask == nullptr) return low_bits(s.prefix + i + 1 - j);
   const int slot = j - s.prefix;  // first of the 32 keys as a node; negative: committed keys come first
   if (slot <= -32) return 0xffffffffu;
-  const int32_t* row = p.mask + int64_t(s.q0 + i) * p.mask_words;
-  auto word = [&](int w) { return w < p.mask_words ? uint32_t(__ldg(row + w)) : 0u; };
+  const int words = attn_mask_words(p);
+  const int32_t* row = p.mask + int64_t(s.q0 + i) * words;
+  auto word = [&](int w) { return w < words ? uint32_t(__ldg(row + w)) : 0u; };
   uint32_t bits;
   if (slot < 0) {
     bits = (word(0) & low_bits(s.nq)) << -slot | low_bits(-slot);
@@ -452,9 +459,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
   if (blockIdx.x == 0) attn_check(p, hdr);
+  if (!GATHER && p.dense && !p.dense->enabled) {  // the gathering kernel does all rows
+    if (threadIdx.x == 0 && !direct) joins[blockIdx.x].runs = 0;
+    return;
+  }
   if (GATHER) {
     if (threadIdx.x == 0) {
-      const int64_t total = int64_t(p.R) * p.Hkv * gather_tiles(p);
+      const int64_t total = gather_total(p);
       misc->lo = total * blockIdx.x / gridDim.x;
       misc->hi = total * (blockIdx.x + 1) / gridDim.x;
     }
@@ -515,7 +526,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const bool more = gather_seg(p, &pos, hi, &sg);
           if (i == 0) {
             const int nt = gather_tiles(p);
-            if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, int64_t(p.R) * p.Hkv * nt, blockIdx.x, gridDim.x);
+            if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, gather_total(p), blockIdx.x,
+                                 gridDim.x);
             else joins[blockIdx.x].runs = 0;
           }
           if (!more) sg.n = -1;
@@ -1195,7 +1207,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
-  JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader));
+  JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   auto kernel = attn_tc_kernel<D, F>;
@@ -1229,8 +1241,27 @@ bool attn_gather_supported(const AttnParams& p) {
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
-  if (p.mode == kAttnSelected)
-    return p.D == 64 ? launch<64, kGather>(p, ws, stream) : launch<128, kGather>(p, ws, stream);
+  if (p.mode == kAttnSelected) {
+    AttnParams g = p;
+    if (attn_dense_wanted(p)) {
+      AttnDense* ctl = reinterpret_cast<AttnDense*>(ws + sizeof(WorkspaceHeader));
+      char* at = ws + sizeof(WorkspaceHeader) + ((attn_partial_bytes(p.R, p.G, p.D) + 255) & ~size_t(255));
+      int32_t* list = reinterpret_cast<int32_t*>(at);
+      uint32_t* mask = reinterpret_cast<uint32_t*>(at + attn_list_bytes(p.R));
+      const cudaError_t e = launch_attn_dense_mask(p, ctl, mask, list, stream);
+      if (e != cudaSuccess) return e;
+      AttnParams d = p;
+      d.mode = kAttnTree;
+      d.cu_q = p.cu_k;
+      d.mask = reinterpret_cast<const int32_t*>(mask);
+      d.dense = ctl;
+      const cudaError_t f = launch_attn_tc(d, ws, stream);
+      if (f != cudaSuccess) return f;
+      g.dense = ctl;
+      g.list = list;
+    }
+    return p.D == 64 ? launch<64, kGather>(g, ws, stream) : launch<128, kGather>(g, ws, stream);
+  }
   // two row tiles per CTA read K and V half as often, but want sequences that fill them
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
   if (p.D == 64) return two ? launch<64, kTwo>(p, ws, stream) : launch<64, kOne>(p, ws, stream);

@@ -234,6 +234,47 @@ def test_selected_every_token_is_prompt():
     A.check(out2, lse2, ref)
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (16, 1, 64), (12, 2, 128)], ids=str)
+@pytest.mark.parametrize("kind", ["causal", "any", "twice", "bad_ids"])
+def test_selected_whole_prompt(kind, heads):
+    """A packed prompt whose rows attend to selected tokens (also as masked dense attention): ids in
+    rank order, ids after the row's own token, ids named twice, ids outside the sequence."""
+    lens = [700, 0, 1, 333, 129]
+    T, width = sum(lens), 150
+    g = torch.Generator().manual_seed(len(kind))
+    ids = torch.full((T, width), -1, dtype=torch.int32)
+    seq, pos = [], []
+    for b, n in enumerate(lens):
+        seq += [b] * n
+        pos += list(range(n))
+    for r in range(T):
+        top = lens[seq[r]] if kind == "any" else pos[r] + 1
+        pick = torch.randperm(top, generator=g)[:width - 9].to(torch.int32)
+        ids[r, :pick.numel()] = pick
+    if kind == "twice":
+        ids[5:T:17, -1] = ids[5:T:17, 0]
+        ids[40:T:50, 3] = ids[40:T:50, 2]
+    if kind == "bad_ids":
+        ids[::3, 4] = 10 ** 6
+        ids[::5, 6] = -7
+        ids[9] = -1
+    q, k, v = make(21, T, T, heads, BF)
+    ws = K.new_attention_workspace(T, len(lens), *heads, BF)
+    out, lse = K.kpool_attention_selected(q, k, v, ids.cuda(), i32(A.cu(lens)), 0.1, return_lse=True, workspace=ws)
+    assert K.kpool_last_device_error(ws) == K.KPOOL_OK
+    A.check(out, lse, A.reference(q, k, v, A.see_selected(ids, seq, lens), 0.1))
+    # tokens nobody named may hold anything
+    named = torch.zeros(T, dtype=torch.bool)
+    for j in A.see_selected(ids[:200], seq[:200], lens):
+        named[j] = True
+    ids[200:] = -1
+    kb, vb = k.clone(), v.clone()
+    for t in (kb, vb):
+        t[(~named).cuda()] = float("nan")
+    out, lse = K.kpool_attention_selected(q, kb, vb, ids.cuda(), i32(A.cu(lens)), 0.1, return_lse=True, workspace=ws)
+    A.check(out, lse, A.reference(q, k, v, A.see_selected(ids, seq, lens), 0.1), "unnamed")
+
+
 def strided(t, how):
     n, h, d = t.shape
     if how == "heads_first":            # [H, T, D]
