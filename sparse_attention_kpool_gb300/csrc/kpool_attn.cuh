@@ -23,6 +23,7 @@ struct AttnDense {
   int32_t enabled;   // the mask fits: the dense kernel works, the gathering one only on the listed rows
   int32_t causal;    // no row selected a key after its own
   int32_t listed;    // rows that name a key twice
+  int32_t finite;    // v holds no infinity or NaN
 };
 
 struct AttnParams {

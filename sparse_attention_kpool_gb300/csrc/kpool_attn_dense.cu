@@ -9,8 +9,9 @@
 // A bit cannot say that a row names a key twice: such rows are listed and the gathering kernel
 // recomputes them afterwards. The kernels of the call find the row stride of the mask (from the
 // longest sequence), whether it fits, and whether no row selected a key after its own on the device:
-//   init (1 CTA)          stride, enabled, causal = 1, no listed rows
-//   mask (a CTA per row)  bits in shared memory, then out; a listed row or a later key is noted
+//   init (1 CTA)          stride, enabled, causal = finite = 1, no listed rows
+//   mask (a CTA per row)  bits in shared memory, then out; a listed row, a later key or an infinity or NaN
+//                         among the token's values is noted (with none the dense kernel cleans no V tile)
 #include <cuda_runtime.h>
 
 #include "kpool_attn.cuh"
@@ -36,6 +37,7 @@ __global__ void __launch_bounds__(256) dense_init_kernel(const __grid_constant__
     ctl->enabled = int64_t(p.R) * words * 4 <= capacity;
     ctl->causal = 1;
     ctl->listed = 0;
+    ctl->finite = 1;
   }
 }
 
@@ -81,6 +83,18 @@ __global__ void __launch_bounds__(256) dense_mask_kernel(const __grid_constant__
     later |= id > pos;
     put(id >> 5, 1u << (id & 31));
   }
+  // The row's own values, every token's once over the grid: a bf16 exponent of all ones carries into bit 15 or 31.
+  const int pieces = p.D / 8;
+  bool wild = false;
+  for (int x = threadIdx.x; x < p.Hkv * pieces; x += 256) {
+    const int h = x / pieces, c = x - h * pieces;
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + int64_t(r) * p.v_ts +
+                                                         int64_t(h) * p.v_hs + 8 * c));
+    constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+    wild |= ((((q.x & kExp) + kOne) | ((q.y & kExp) + kOne) | ((q.z & kExp) + kOne) | ((q.w & kExp) + kOne)) &
+             0x80008000u) != 0;
+  }
+  if (wild) ctl->finite = 0;
   const int any = __syncthreads_or((twice ? 1 : 0) | (later ? 2 : 0));  // nonzero if any thread's is
   if (any) {
     const int dup = __syncthreads_or(twice), aft = __syncthreads_or(later);

@@ -54,12 +54,13 @@ constexpr int kGatherWarps = 4;
 constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
-// The forms of the kernel: one or two row tiles of consecutive tokens, or one token's heads over gathered keys.
-enum Form { kOne, kTwo, kGather };
+// The forms of the kernel: one or two row tiles of consecutive tokens, one token's heads over gathered keys, or
+// two row tiles under a mask of bits for all keys (the dense form of a selection).
+enum Form { kOne, kTwo, kGather, kDense };
 
 template <int D, Form F>
 struct Cfg {
-  static constexpr bool TWO = F == kTwo;
+  static constexpr bool TWO = F == kTwo || F == kDense;
   // The ring holds K(0) .. K(kAhead - 1), then K(j), V(j - kAhead) in turn: the order in which the MMAs use
   // them, K one tile (one-tile form: one per group) ahead.
   static constexpr int kAhead = TWO ? 1 : 2;
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
                    int direct, float* part, int slot_rows, JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<D, F>;
-  constexpr bool TWO = C::TWO, GATHER = F == kGather;
+  constexpr bool TWO = C::TWO, GATHER = F == kGather, DENSE = F == kDense;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -459,7 +460,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
   if (blockIdx.x == 0) attn_check(p, hdr);
-  if (!GATHER && p.dense && !p.dense->enabled) {  // the gathering kernel does all rows
+  // dense form: with nothing but finite values there is nothing to clean
+  const bool no_cleaning = GATHER || (DENSE && p.dense->finite);
+  if (DENSE && !p.dense->enabled) {  // the gathering kernel does all rows
     if (threadIdx.x == 0 && !direct) joins[blockIdx.x].runs = 0;
     return;
   }
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < C::kBlocks; ++h)
             ptx::tma_load_3d(dst + h * C::kHalf, tm, full + st, 64 * h, sg.hk, sg.sq.k0 + kt * kTileKeys);
-          if (tm == &tm_v && tile_masked(&sg, kt)) ptx::mbar_arrive(dirty + st);
+          if (tm == &tm_v && !no_cleaning && tile_masked(&sg, kt)) ptx::mbar_arrive(dirty + st);
           return true;
         };
         for (int i = 0;; ++i) {
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
               if (jk < n && !(ok = landed(uk))) break;
               if (!(ok = landed(uv))) break;
               const uint32_t slot = uv % C::kStages;
-              const bool masked = !GATHER && tile_masked(sg, kt0 + j);
+              const bool masked = !no_cleaning && tile_masked(sg, kt0 + j);
               if (mine(j)) {
                 if (masked && !(ok = wait_bar(clean + slot, (clean_par >> slot) & 1, misc))) break;
                 if (!(ok = wait_bar(p_ready + g, p_uses & 1, misc))) break;
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       const Seg* sg;
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
         const int n = sg->n, kt0 = sg->kt0;
-        for (int j = max(0, sg->all / kTileKeys - kt0); j < n; ++j) {
+        for (int j = no_cleaning ? n : max(0, sg->all / kTileKeys - kt0); j < n; ++j) {
           const uint32_t u = use + v_use<C::kAhead>(j, n);
           const uint32_t slot = u % C::kStages;
           // The producer says when it has begun to fill the slot with this tile: the slot's
@@ -853,6 +856,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       uint64_t l2[2] = {0, 0};
       for (int j = first; j < n; j += step) {
         const int kt = sg->kt0 + j;
+        uint4 seen;
+        if (DENSE) {  // the row's bits of the tile, 16-byte aligned words
+          const int words = attn_mask_words(p), im = min(i, sg->sq.nq - 1);
+          seen = __ldg(reinterpret_cast<const uint4*>(p.mask + int64_t(sg->sq.q0 + im) * words) + kt);
+        }
         ok = __all_sync(0xffffffffu, wait_bar(s_full + g, s_uses & 1, misc));
         if (!ok) break;
         ++s_uses;
@@ -860,7 +868,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         // Keys that some row does not see: -inf over their scores in TMEM, 32 columns at a time and only
         // where a row of the warp needs it. (As straight code on the 128 registers below it took three
         // times as long: it runs once or twice per row tile and is fetched anew each time.)
-        if (GATHER || tile_masked(sg, kt)) {
+        if (!DENSE && (GATHER || tile_masked(sg, kt))) {
           const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
           const int im = min(i, sg->sq.nq - 1);
 #pragma unroll 1
@@ -884,6 +892,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         ptx::tc_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tc_reg_fence(s[c]);
+        if (DENSE) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = c == 0 ? seen.x : c == 1 ? seen.y : c == 2 ? seen.z : seen.w;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;
+          }
+        }
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -1262,6 +1279,7 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
     }
     return p.D == 64 ? launch<64, kGather>(g, ws, stream) : launch<128, kGather>(g, ws, stream);
   }
+  if (p.dense) return p.D == 64 ? launch<64, kDense>(p, ws, stream) : launch<128, kDense>(p, ws, stream);
   // two row tiles per CTA read K and V half as often, but want sequences that fill them
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
   if (p.D == 64) return two ? launch<64, kTwo>(p, ws, stream) : launch<64, kOne>(p, ws, stream);
