@@ -133,32 +133,36 @@ __device__ __forceinline__ int attn_seq_of_tile(const AttnParams& p, int tile, i
   return lo;
 }
 
-// Every thread of one CTA of the grid: checks the device arrays of the whole call and
-// writes the header's error word (0 when all is well), so no kernel has to clear it.
+// The header's error word, first and last: one thread clears it at the start of the call, and one warp
+// checks the device arrays of the whole call (beside the work, which relies on none of it).
+__device__ __forceinline__ void attn_clear_error(WorkspaceHeader* hdr) { hdr->error = KPOOL_OK; }
+
 __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader* hdr) {
-  int bad = 0;
-  for (int b = threadIdx.x; b <= p.S; b += blockDim.x) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int b = lane; b <= p.S; b += 32) {
     const int k = __ldg(p.cu_k + b);
-    if (b == 0 ? k != 0 : k < __ldg(p.cu_k + b - 1)) bad = 1;
-    if (b == p.S && k != p.T) bad = 1;
+    if (b == 0 ? k != 0 : k < __ldg(p.cu_k + b - 1)) bad = true;
+    if (b == p.S && k != p.T) bad = true;
     if (p.mode == kAttnSelected) continue;
     const int q = __ldg(p.cu_q + b);
-    if (b == 0 ? q != 0 : q < __ldg(p.cu_q + b - 1)) bad = 1;
-    if (b == p.S && q != p.R) bad = 1;
+    if (b == 0 ? q != 0 : q < __ldg(p.cu_q + b - 1)) bad = true;
+    if (b == p.S && q != p.R) bad = true;
     if (p.mode == kAttnTree && b < p.S && p.prefix) {
       const int64_t pre = __ldg(p.prefix + b);
       const int64_t rows = int64_t(__ldg(p.cu_q + b + 1)) - q, extent = int64_t(__ldg(p.cu_k + b + 1)) - k;
-      if (pre < 0 || pre + rows > extent) bad = 1;
+      if (pre < 0 || pre + rows > extent) bad = true;
     }
   }
-  if (p.mode == kAttnSelected && p.row_seq != nullptr)
-#pragma unroll 4
-    for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+  if (p.mode == kAttnSelected && p.row_seq != nullptr) {
+#pragma unroll 8
+    for (int r = lane; r < p.R; r += 32) {
       const int b = __ldg(p.row_seq + r);
-      if (b < 0 || b >= p.S) bad = 1;
+      bad |= b < 0 || b >= p.S;
     }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) hdr->error = bad ? KPOOL_ERR_INVALID_ARG : KPOOL_OK;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0 && bad) record_error(hdr, KPOOL_ERR_INVALID_ARG);
 }
 
 // Key tokens of selected row r: first token and number (0 when the row has no valid sequence).
@@ -178,6 +182,7 @@ constexpr int kAttnMaxRuns = 152;
 constexpr int kAttnMaxRunSeqs = 8192;
 constexpr int kAttnDirectItems = 6;
 constexpr int kAttnDirectKeys = 8192;
+constexpr int kAttnWholeKeys = 512;
 constexpr int kAttnJoinBytes = 64;   // per run: what the join of the rows before it needs
 inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
   const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned

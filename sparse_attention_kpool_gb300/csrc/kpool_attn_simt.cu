@@ -1,12 +1,15 @@
 // kpool_attn_simt.cu -- the attention operators on the CUDA cores: fp32 inputs at fp32
 // precision, and the head sizes the tensor-core kernels do not take.
 //
-// One CTA of 4 warps holds 16 (query row, head) pairs that share a key head and walks the
-// keys in blocks of 32 with the running maximum and sum of a softmax (one pass over K and
-// V, nothing written but the result). A lane scores one key for its warp's four rows, so a
-// 16-byte read of K from shared memory feeds 16 multiply-adds; for the second product a
-// lane owns 4 (or 8) channels and reads V the same way. K rows are padded by 16 bytes, which
-// spreads the lanes' 16-byte reads over all banks.
+// One CTA holds 16 (query row, head) pairs that share a key head and walks the keys in
+// blocks of 32 with the running maximum and sum of a softmax (one pass over K and V, nothing
+// written but the result). Groups of 4 warps (four groups, two for heads above 128) take every
+// fourth (second) block and add up at the end: the calls that come here are small, and one
+// group alone waits out the latency of each block in turn (60 against 21 us for 345 rows of 8
+// heads of 64). A lane scores one key for its warp's four rows, so a 16-byte read of K from
+// shared memory feeds 16 multiply-adds; for the second product a lane owns 4 (or 8) channels and
+// reads V the same way. K rows are padded by 16 bytes, which spreads the lanes' 16-byte reads
+// over all banks.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -17,7 +20,7 @@ namespace {
 
 constexpr int kVRows = 16;        // (row, head) pairs per CTA
 constexpr int kPerWarp = 4;
-constexpr int kThreadsSimt = 128;
+constexpr int kGroupThreads = 128;
 constexpr int kKeys = 32;         // keys per block: one per lane
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -37,16 +40,25 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = u;
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParams p, int gt, int tt,
-                                                                 WorkspaceHeader* hdr) {
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(group + 1), "n"(kGroupThreads) : "memory");
+}
+
+// Shared memory, in floats: Q, then each group's K and V block; the groups' results overlay the blocks.
+inline __host__ __device__ int group_floats(int D) { return kKeys * (2 * D + 4); }
+
+template <typename E, int kGroups>
+__global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const AttnParams p, int gt, int tt,
+                                                                           WorkspaceHeader* hdr) {
   extern __shared__ __align__(16) float smem[];
   const int D = p.D, ldk = D + 4;
-  float* s_q = smem;                    // [kVRows][D]
-  float* s_k = s_q + kVRows * D;        // [kKeys][D + 4]
-  float* s_v = s_k + kKeys * ldk;       // [kKeys][D]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && blockIdx.y == 0) attn_check(p, hdr);
+  const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
+  float* s_q = smem;                                        // [kVRows][D]
+  float* s_k = s_q + kVRows * D + group * group_floats(D);  // [kKeys][D + 4]
+  float* s_v = s_k + kKeys * ldk;                           // [kKeys][D]
+  const int lane = tid & 31, warp = tid >> 5;
+  const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+  if (checks && threadIdx.x == 0) attn_clear_error(hdr);
 
   // the CTA's rows: tokens [i0, i1) of a sequence x heads [g0, g0 + gt) of key head hk
   const int gb_n = (p.G + gt - 1) / gt;
@@ -67,7 +79,11 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
     const int b = attn_seq_of_tile(p, blockIdx.x, tt);
     sq = attn_seq(p, b);
     i0 = (int(blockIdx.x) - (__ldg(p.cu_q + b) / tt + b)) * tt;
-    if (i0 < 0 || i0 >= sq.nq) return;
+    if (i0 < 0 || i0 >= sq.nq) {
+      __syncwarp();
+      if (checks && threadIdx.x < 32) attn_check(p, hdr);
+      return;
+    }
     i1 = min(i0 + tt, sq.nq);
     end = attn_keys_end(p, sq, i1);
   }
@@ -76,7 +92,7 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
   const E* kk = static_cast<const E*>(p.k) + int64_t(hk) * p.k_hs;
   const E* vv = static_cast<const E*>(p.v) + int64_t(hk) * p.v_hs;
   const int chunks = D / 4;
-  for (int x = threadIdx.x; x < kVRows * chunks; x += kThreadsSimt) {
+  for (int x = threadIdx.x; x < kVRows * chunks; x += kGroupThreads * kGroups) {
     const int r = x / chunks, c = x % chunks, i = i0 + r / gt, g = g0 + r % gt;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r / gt < tt && i < i1 && g < p.G)
@@ -98,9 +114,10 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
     o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
-  for (int j0 = 0; j0 < end; j0 += kKeys) {
-    __syncthreads();
-    for (int x = threadIdx.x; x < kKeys * chunks; x += kThreadsSimt) {
+  __syncthreads();
+  for (int j0 = group * kKeys; j0 < end; j0 += kGroups * kKeys) {
+    group_sync(group);
+    for (int x = tid; x < kKeys * chunks; x += kGroupThreads) {
       const int jj = x / chunks, c = x % chunks;
       int64_t t = -1;
       if (j0 + jj < end) {
@@ -115,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
       store4(s_k + jj * ldk + 4 * c, a);
       store4(s_v + jj * D + 4 * c, b);
     }
-    __syncthreads();
+    group_sync(group);
 
     float s[kPerWarp] = {0.f, 0.f, 0.f, 0.f};
     const float* kr = s_k + lane * ldk;
@@ -183,10 +200,47 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
     }
   }
 
+  // the groups' results: [group][kVRows][D] sums, then [group][kVRows] (m, l); group g finishes row g of each warp
+  __syncthreads();
+  float* s_o = smem + kVRows * D;
+  float2* s_ml = reinterpret_cast<float2*>(s_o + kGroups * kVRows * D);
+#pragma unroll
+  for (int r = 0; r < kPerWarp; ++r) {
+    const int vr = group * kVRows + warp * kPerWarp + r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h * 128 + lane * 4;
+      if (c < D) store4(s_o + vr * D + c, o[r][h]);
+    }
+    if (lane == 0) s_ml[vr] = make_float2(m[r], l[r]);
+  }
+  __syncthreads();
   E* out = static_cast<E*>(p.out);
 #pragma unroll
   for (int r = 0; r < kPerWarp; ++r) {
-    if (tok[r] < 0) continue;
+    if (tok[r] < 0 || r % kGroups != group) continue;
+    const int vr = warp * kPerWarp + r;
+    m[r] = -INFINITY;
+    for (int g = 0; g < kGroups; ++g) m[r] = fmaxf(m[r], s_ml[g * kVRows + vr].x);
+    const float base = m[r] == -INFINITY ? 0.f : m[r];
+    l[r] = 0.f;
+    o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < kGroups; ++g) {
+      const float2 ml = s_ml[g * kVRows + vr];
+      // a group without any weight adds nothing; with a NaN among its scores its sum passes on
+      const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - base);
+      l[r] = fmaf(ml.y, w, l[r]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = h * 128 + lane * 4;
+        if (c >= D) break;
+        const float4 f = load4(s_o + (g * kVRows + vr) * D + c);
+        o[r][h].x = fmaf(f.x, w, o[r][h].x);
+        o[r][h].y = fmaf(f.y, w, o[r][h].y);
+        o[r][h].z = fmaf(f.z, w, o[r][h].z);
+        o[r][h].w = fmaf(f.w, w, o[r][h].w);
+      }
+    }
     const int64_t row = sq.q0 + tok[r];
     const int head = hk * p.G + g0 + (warp * kPerWarp + r) % gt;
     const bool none = m[r] == -INFINITY && l[r] == 0.f;  // (a NaN score leaves l NaN: not empty)
@@ -201,6 +255,8 @@ __global__ void __launch_bounds__(kThreadsSimt) attn_simt_kernel(const AttnParam
     }
     if (lane == 0 && p.lse) p.lse[row * p.Hq + head] = none ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
   }
+  __syncwarp();
+  if (checks && threadIdx.x < 32) attn_check(p, hdr);
 }
 
 }  // namespace
@@ -210,16 +266,18 @@ cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, c
   const int gt = p.G < kVRows ? p.G : kVRows;
   const int tt = p.mode == kAttnSelected ? 1 : kVRows / gt;
   const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles(p.R, p.S, tt);
-  const size_t smem = sizeof(float) * (size_t(kVRows) * p.D + size_t(kKeys) * (p.D + 4) + size_t(kKeys) * p.D);
+  const int groups = p.D <= 128 ? 4 : 2;
+  const size_t smem = sizeof(float) * (size_t(kVRows) * p.D + size_t(groups) * group_floats(p.D));
   const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   auto go = [&](auto kernel) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreadsSimt, smem, stream>>>(p, gt, tt, hdr);
+    kernel<<<grid, kGroupThreads * groups, smem, stream>>>(p, gt, tt, hdr);
     return cudaGetLastError();
   };
-  return dtype == KPOOL_BF16 ? go(attn_simt_kernel<__nv_bfloat16>) : go(attn_simt_kernel<float>);
+  if (dtype == KPOOL_BF16) return groups == 4 ? go(attn_simt_kernel<__nv_bfloat16, 4>) : go(attn_simt_kernel<__nv_bfloat16, 2>);
+  return groups == 4 ? go(attn_simt_kernel<float, 4>) : go(attn_simt_kernel<float, 2>);
 }
 
 }  // namespace kpool

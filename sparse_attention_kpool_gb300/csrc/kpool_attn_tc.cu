@@ -36,6 +36,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "kpool_attn.cuh"
 #include "kpool_ptx.cuh"
 
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   const int tt = GATHER ? 1 : kTileRows / p.G, ttb = C::kQTiles * tt;  // tokens of a row tile, of the CTA's row tiles
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
-  if (blockIdx.x == 0) attn_check(p, hdr);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.list) attn_clear_error(hdr);
   // dense form: with nothing but finite values there is nothing to clean
   const bool no_cleaning = GATHER || (DENSE && p.dense->finite);
   if (DENSE && !p.dense->enabled) {  // the gathering kernel does all rows
@@ -529,7 +531,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const bool more = gather_seg(p, &pos, hi, &sg);
           if (i == 0) {
             const int nt = gather_tiles(p);
-            if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, gather_total(p), blockIdx.x,
+            if (direct) {
+              // whole items: nothing to join
+            } else if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, gather_total(p), blockIdx.x,
                                  gridDim.x);
             else joins[blockIdx.x].runs = 0;
           }
@@ -776,6 +780,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
         ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
       }
+    } else if (GATHER && warp == 11) {
+      if (blockIdx.x == 0) attn_check(p, hdr);
     } else if (!GATHER) {  // ------------------------------------------------ V cleaning warp
       uint32_t use = 0, dirty_par = 0;
       bool ok = true;
@@ -830,6 +836,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
+      __syncwarp();
+      if (blockIdx.x == 0) attn_check(p, hdr);
     }
   } else {  // -------------------------------------------------------------- softmax groups
     if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -1219,20 +1227,32 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
-  const bool direct = !GATHER && (p.S > kAttnMaxRunSeqs || (C::TWO && items >= int64_t(kAttnDirectItems) * sms &&
-                                                            p.T >= int64_t(kAttnDirectKeys) * p.S));
+  // Where an item has few tiles at most (the call's keys, the ids of a row), cutting them to fill the
+  // SMs saves less than the join costs: whole items, one to a CTA.
+  const bool small = (GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms && !p.list;
+  const bool direct = !GATHER && (small || p.S > kAttnMaxRunSeqs ||
+                                  (C::TWO && items >= int64_t(kAttnDirectItems) * sms &&
+                                   p.T >= int64_t(kAttnDirectKeys) * p.S));
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
-  const int grid = direct ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
+  const int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   auto kernel = attn_tc_kernel<D, F>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory limit is set
+  int dev = 0;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct ? 1 : 0, part, slot_rows, joins, hdr);
+  if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
+                                                  joins, hdr);
   e = cudaGetLastError();
-  if (e != cudaSuccess || direct || grid < 2) return e;
+  if (e != cudaSuccess || direct || small || grid < 2) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(256);

@@ -491,48 +491,80 @@ def new_attention_workspace(q_rows: int, num_seqs: int, q_heads: int, kv_heads: 
     return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
 
 
-def _heads(t: torch.Tensor, what: str) -> kpool_heads:
-    n, h, d = t.shape
+class _AttentionArgs(threading.local):
+    """A thread's argument structures, filled anew by every call (building them took most of a short call)."""
+
+    def __init__(self):
+        self.heads = [kpool_heads() for _ in range(4)]  # q, k, v, out
+        self.shape = kpool_attention_shape()
+        self.refs = [ctypes.byref(h) for h in self.heads]
+        self.shape_ref = ctypes.byref(self.shape)
+        self.options = {k: kpool_options(k) for k in (KPOOL_SCORE_TC, KPOOL_SCORE_SIMT)}
+
+
+_attention_args = _AttentionArgs()
+_ATTENTION_DTYPES = {torch.bfloat16: KPOOL_BF16, torch.float32: KPOOL_F32}
+
+
+def _set_heads(h: kpool_heads, t: torch.Tensor, shape, what: str):
     ts, hs, ds = t.stride()
+    n, heads, d = shape
     if not t.is_cuda or (ds != 1 and d > 1):
         raise ValueError(f"{what} must be a CUDA tensor whose last dimension is contiguous")
+    h.data = t.data_ptr()
     # the stride of a dimension of one element carries no meaning in torch
-    return kpool_heads(t.data_ptr(), ts if n > 1 else d, hs if h > 1 else d)
+    h.token_stride = ts if n > 1 else d
+    h.head_stride = hs if heads > 1 else d
 
 
 def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse, workspace, stream, score_kernel):
     """Marshals one kpool_attention_* call: `arrays` are its arguments between v and num_seqs."""
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or q.shape[2] != k.shape[2]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or v.shape != ks or qs[2] != ks[2]:
         raise ValueError("q is [rows, q_heads, head_dim]; k and v are [tokens, kv_heads, head_dim] alike")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype = q.dtype
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("k and v must match q's dtype")
-    R, hq, d = q.shape
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
+    R, hq, d = qs
     if out is None:
-        out = torch.empty((R, hq, d), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = torch.empty((R, hq, d), dtype=dtype, device=q.device)
+    elif out.shape != qs or out.dtype != dtype:
         raise TypeError("out must have q's shape and dtype")
     if out_lse is None:
         if return_lse:
             out_lse = torch.empty((R, hq), dtype=torch.float32, device=q.device)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (R, hq):
         raise TypeError("out_lse must be float32 [rows, q_heads]")
-    shape = _attention_shape(hq, k.shape[1], d, q.dtype, scale)
     if workspace is None:
-        workspace = new_attention_workspace(R, num_seqs, hq, k.shape[1], d, q.dtype, q.device)
+        workspace = new_attention_workspace(R, num_seqs, hq, ks[1], d, dtype, q.device)
+    a = _attention_args
+    h = a.heads
+    _set_heads(h[0], q, qs, "q")
+    _set_heads(h[1], k, ks, "k")
+    _set_heads(h[2], v, ks, "v")
+    _set_heads(h[3], out, qs, "out")
+    sh = a.shape
+    sh.q_heads, sh.kv_heads, sh.head_dim, sh.dtype, sh.scale = hq, ks[1], d, code, scale
     args = []
-    for a in arrays:
-        if torch.is_tensor(a):
-            if a.dtype != torch.int32:
+    for x in arrays:
+        if isinstance(x, torch.Tensor):
+            if x.dtype != torch.int32:
                 raise TypeError("cumulative lengths, prefix, mask, token ids and row_seq are int32")
-            _check_cuda(a)
-            args.append(a.data_ptr())
+            if not x.is_cuda or not x.is_contiguous():
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            args.append(x.data_ptr())
         else:
-            args.append(a)
+            args.append(x)
     _check_cuda(out_lse, workspace)
-    st = getattr(load(), name)(_heads(q, "q"), _heads(k, "k"), _heads(v, "v"), *args, num_seqs, R, k.shape[0], shape,
-                               _heads(out, "out"), None if out_lse is None else out_lse.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), _stream(stream),
-                               None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
+    r = a.refs
+    st = getattr(_lib or load(), name)(
+        r[0], r[1], r[2], *args, num_seqs, R, ks[0], a.shape_ref, r[3], None if out_lse is None else out_lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(),
+        torch._C._cuda_getCurrentRawStream(q.device.index) if stream is None else _stream(stream),
+        None if score_kernel == KPOOL_SCORE_AUTO else a.options.get(score_kernel, kpool_options(score_kernel)))
     if st != KPOOL_OK:
         raise KpoolError(st, name)
     return out, out_lse
