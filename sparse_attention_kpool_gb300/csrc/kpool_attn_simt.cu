@@ -45,17 +45,19 @@ __device__ __forceinline__ void group_sync(int group) {
 }
 
 // Shared memory, in floats: Q, then each group's K and V block; the groups' results overlay the blocks.
-inline __host__ __device__ int group_floats(int D) { return kKeys * (2 * D + 4); }
+inline __host__ __device__ int group_floats(int D) { return kKeys * (2 * D + 4 + 4 * kPerWarp); }
 
 template <typename E, int kGroups>
-__global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const AttnParams p, int gt, int tt,
-                                                                           WorkspaceHeader* hdr) {
+__global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
+    attn_simt_kernel(const __grid_constant__ AttnParams p, int gt, int tt, WorkspaceHeader* hdr) {
+  constexpr int kH = kGroups == 4 ? 1 : 2;  // 128-channel parts of a head
   extern __shared__ __align__(16) float smem[];
   const int D = p.D, ldk = D + 4;
   const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
   float* s_q = smem;                                        // [kVRows][D]
   float* s_k = s_q + kVRows * D + group * group_floats(D);  // [kKeys][D + 4]
   float* s_v = s_k + kKeys * ldk;                           // [kKeys][D]
+  float* s_p = s_v + kKeys * D;                             // [4 warps][kKeys][kPerWarp]
   const int lane = tid & 31, warp = tid >> 5;
   const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
   if (checks && threadIdx.x == 0) attn_clear_error(hdr);
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
 
   const float c2 = p.scale * kLog2e;
   float m[kPerWarp], l[kPerWarp];
-  float4 o[kPerWarp][2];
+  float4 o[kPerWarp][kH];
   int tok[kPerWarp];  // the warp's rows: token index, or -1 where the slot holds no row
 #pragma unroll
   for (int r = 0; r < kPerWarp; ++r) {
@@ -111,26 +113,36 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
     tok[r] = (vr / gt < tt && i < i1 && g0 + vr % gt < p.G) ? i : -1;
     m[r] = -INFINITY;
     l[r] = 0.f;
-    o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < kH; ++h) o[r][h] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
   __syncthreads();
   for (int j0 = group * kKeys; j0 < end; j0 += kGroups * kKeys) {
     group_sync(group);
-    for (int x = tid; x < kKeys * chunks; x += kGroupThreads) {
-      const int jj = x / chunks, c = x % chunks;
-      int64_t t = -1;
-      if (j0 + jj < end) {
+    // two pieces of K and V in flight per thread; piece x is channels 4 (x % chunks).. of key x / chunks
+    for (int x0 = tid; x0 < kKeys * chunks; x0 += 2 * kGroupThreads) {
+      float4 a[2], b[2];
+      int at[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int x = x0 + y * kGroupThreads, jj = x / chunks, c = 4 * (x - jj * chunks);
+        at[y] = x < kKeys * chunks ? jj * 1024 + c : -1;
+        a[y] = b[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at[y] < 0 || j0 + jj >= end) continue;
         const int id = selected ? __ldg(ids + j0 + jj) : j0 + jj;
-        if (id >= 0 && id < sq.nk) t = int64_t(sq.k0) + id;
+        if (id < 0 || id >= sq.nk) continue;
+        const int64_t t = int64_t(sq.k0) + id;
+        a[y] = load4(kk + t * p.k_ts + c);
+        b[y] = load4(vv + t * p.v_ts + c);
       }
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-      if (t >= 0) {
-        a = load4(kk + t * p.k_ts + 4 * c);
-        b = load4(vv + t * p.v_ts + 4 * c);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (at[y] < 0) continue;
+        const int jj = at[y] >> 10, c = at[y] & 1023;
+        store4(s_k + jj * ldk + c, a[y]);
+        store4(s_v + jj * D + c, b[y]);
       }
-      store4(s_k + jj * ldk + 4 * c, a);
-      store4(s_v + jj * D + 4 * c, b);
     }
     group_sync(group);
 
@@ -171,32 +183,45 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
       l[r] = fmaf(l[r], f, sum);
       m[r] = mx;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kH; ++h) {
         o[r][h].x *= f;
         o[r][h].y *= f;
         o[r][h].z *= f;
         o[r][h].w *= f;
       }
     }
+    // the rows' weights key by key: one 16-byte read gives a key's four
+    float4* pw = reinterpret_cast<float4*>(s_p) + warp * kKeys;
+    __syncwarp();
+    pw[lane] = make_float4(pr[0], pr[1], pr[2], pr[3]);
+    __syncwarp();
     const int n = min(kKeys, end - j0);
-    for (int jj = 0; jj < n; ++jj) {
-      float w[kPerWarp];
+    const bool all = (seen[0] & seen[1] & seen[2] & seen[3]) == 0xffffffffu;
+    auto add = [&](int jj, bool masked) {
+      const float4 w = pw[jj];
 #pragma unroll
-      for (int r = 0; r < kPerWarp; ++r) w[r] = __shfl_sync(0xffffffffu, pr[r], jj);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kH; ++h) {
         const int c = h * 128 + lane * 4;
         if (c >= D) break;
         const float4 b = load4(s_v + jj * D + c);
 #pragma unroll
-        for (int r = 0; r < kPerWarp; ++r)
-          if ((seen[r] >> jj) & 1u) {  // a key the row does not see adds nothing, whatever its value holds
-            o[r][h].x = fmaf(w[r], b.x, o[r][h].x);
-            o[r][h].y = fmaf(w[r], b.y, o[r][h].y);
-            o[r][h].z = fmaf(w[r], b.z, o[r][h].z);
-            o[r][h].w = fmaf(w[r], b.w, o[r][h].w);
-          }
+        for (int r = 0; r < kPerWarp; ++r) {
+          const float x = r == 0 ? w.x : r == 1 ? w.y : r == 2 ? w.z : w.w;
+          // a key the row does not see adds nothing, whatever its value holds
+          if (masked && !((seen[r] >> jj) & 1u)) continue;
+          o[r][h].x = fmaf(x, b.x, o[r][h].x);
+          o[r][h].y = fmaf(x, b.y, o[r][h].y);
+          o[r][h].z = fmaf(x, b.z, o[r][h].z);
+          o[r][h].w = fmaf(x, b.w, o[r][h].w);
+        }
       }
+    };
+    if (all) {
+#pragma unroll 4
+      for (int jj = 0; jj < kKeys; ++jj) add(jj, false);
+    } else {
+#pragma unroll 2
+      for (int jj = 0; jj < n; ++jj) add(jj, true);
     }
   }
 
@@ -208,7 +233,7 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
   for (int r = 0; r < kPerWarp; ++r) {
     const int vr = group * kVRows + warp * kPerWarp + r;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kH; ++h) {
       const int c = h * 128 + lane * 4;
       if (c < D) store4(s_o + vr * D + c, o[r][h]);
     }
@@ -224,14 +249,15 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
     for (int g = 0; g < kGroups; ++g) m[r] = fmaxf(m[r], s_ml[g * kVRows + vr].x);
     const float base = m[r] == -INFINITY ? 0.f : m[r];
     l[r] = 0.f;
-    o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < kH; ++h) o[r][h] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int g = 0; g < kGroups; ++g) {
       const float2 ml = s_ml[g * kVRows + vr];
       // a group without any weight adds nothing; with a NaN among its scores its sum passes on
       const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - base);
       l[r] = fmaf(ml.y, w, l[r]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kH; ++h) {
         const int c = h * 128 + lane * 4;
         if (c >= D) break;
         const float4 f = load4(s_o + (g * kVRows + vr) * D + c);
@@ -246,7 +272,7 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups) attn_simt_kernel(const
     const bool none = m[r] == -INFINITY && l[r] == 0.f;  // (a NaN score leaves l NaN: not empty)
     const float inv = none ? 0.f : 1.f / l[r];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kH; ++h) {
       const int c = h * 128 + lane * 4;
       if (c >= D) break;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
