@@ -37,6 +37,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <utility>
 
 #include "kpool_attn.cuh"
 #include "kpool_ptx.cuh"
@@ -409,6 +410,17 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnSeq
 // K/V tile kt holds keys that some row of the segment does not see.
 __device__ __forceinline__ bool tile_masked(const Seg* s, int kt) { return (kt + 1) * kTileKeys > s->all; }
 
+// Rows rsub + kRowsPer * I of a warp's 32, all present: the token a lane wants comes from the lane that
+// holds its id; the destination differs by constants but for two address bits.
+template <int kRowsPer, int... I>
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const char* base, int tok, uint32_t ts_bytes, int rsub,
+                                           std::integer_sequence<int, I...>) {
+  (ptx::cp_async_16_at<kRowsPer * I * 128>(
+       dst ^ (((kRowsPer * I) & 7) << 4),
+       base + uint64_t(uint32_t(__shfl_sync(0xffffffffu, tok, rsub + kRowsPer * I))) * ts_bytes),
+   ...);
+}
+
 // Transposes 4 x 4 pieces of 16 bytes within each quad of lanes: piece r of lane i becomes piece i of
 // lane r. A thread holds a row of the result; after this four lanes hold 64 contiguous bytes of one row,
 // and a store instruction of the warp touches 8 lines instead of 32.
@@ -559,7 +571,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       constexpr int kChunks = D / 8;               // 16-byte pieces of a row
       constexpr int kRowsPer = 32 / kChunks;       // rows per warp instruction
       const int w = warp - 12, c = lane % kChunks, rsub = lane / kChunks;
-      const uint32_t dst0 = ptx::smem_addr(smem + C::kOffRing) + uint32_t(c >> 3) * C::kHalf + uint32_t(w * 32) * 128;
+      // the lane's place in the warp's first rows; a row's pieces are permuted by its number's low bits
+      const uint32_t dst0 = ptx::smem_addr(smem + C::kOffRing) + uint32_t(c >> 3) * C::kHalf +
+                            uint32_t(w * 32 + rsub) * 128 + (((c & 7) ^ rsub) << 4);
       uint32_t fills = 0, tile = 0;
       bool ok = true;
       const Seg* sg;
@@ -582,12 +596,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         }
         const char* base = static_cast<const char*>(src) + (int64_t(sg->hk) * hs + c * 8) * 2;
         const uint32_t dst = dst0 + st * C::kTileBytes;
-#pragma unroll
-        for (int i = 0; i < 32 / kRowsPer; ++i) {
-          const int row = rsub + kRowsPer * i;     // of the warp's 32
-          const int t = __shfl_sync(0xffffffffu, tok, row);
-          const char* from = base + uint64_t(uint32_t(max(t, 0))) * ts_bytes;
-          ptx::cp_async_16(dst + uint32_t(row) * 128 + uint32_t(((c & 7) ^ (row & 7)) << 4), from, t >= 0 ? 16u : 0u);
+        if (__all_sync(0xffffffffu, tok >= 0)) {
+          fetch_rows<kRowsPer>(dst, base, tok, ts_bytes, rsub, std::make_integer_sequence<int, 32 / kRowsPer>{});
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < 32 / kRowsPer; ++i) {
+            const int t = __shfl_sync(0xffffffffu, tok, rsub + kRowsPer * i);
+            const char* from = base + uint64_t(uint32_t(max(t, 0))) * ts_bytes;
+            ptx::cp_async_16((dst ^ (((kRowsPer * i) & 7) << 4)) + kRowsPer * i * 128, from, t >= 0 ? 16u : 0u);
+          }
         }
         ptx::cp_async_arrive(full + st);                     // when this lane's pieces have landed
         if (lane == 0) ptx::mbar_arrive(full + st);          // and the warp's word of bits is written
@@ -1229,7 +1246,11 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   const int64_t items = tiles * p.Hkv;
   // Where an item has few tiles at most (the call's keys, the ids of a row), cutting them to fill the
   // SMs saves less than the join costs: whole items, one to a CTA.
-  const bool small = (GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms && !p.list;
+  // Gathered items all have the same tiles: one CTA each (and two tiles' time for its start and end) against
+  // runs of all tiles and a join of about five tiles' time.
+  const int64_t nt = (p.width + kTileKeys - 1) / kTileKeys;
+  const bool whole = GATHER && !p.list && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
+  const bool small = whole || ((GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms && !p.list);
   const bool direct = !GATHER && (small || p.S > kAttnMaxRunSeqs ||
                                   (C::TWO && items >= int64_t(kAttnDirectItems) * sms &&
                                    p.T >= int64_t(kAttnDirectKeys) * p.S));

@@ -107,6 +107,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// 16 bytes to dst + kOffset.
+template <int kOffset>
+__device__ __forceinline__ void cp_async_16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(dst), "l"(src), "n"(kOffset) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // This thread's arrival on `bar` once all its earlier cp_async_16 have landed (counts as one arrival).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
