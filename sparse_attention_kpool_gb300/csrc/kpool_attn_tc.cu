@@ -47,6 +47,7 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 128;
+constexpr int kPCol = 64;      // a tile's weights, bf16 in 64 columns, replace the upper half of its scores
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
@@ -421,6 +422,31 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const char* base, int t
    ...);
 }
 
+// 32 N columns of scores from TMEM column `col` on.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t col, uint32_t (&s)[N][32]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) ptx::tc_ld_32x32b_x32(col + 32 * c, s[c]);
+  ptx::tc_wait_ld();
+#pragma unroll
+  for (int c = 0; c < N; ++c) ptx::tc_reg_fence(s[c]);
+}
+
+template <int N>
+__device__ __forceinline__ float max_score(const uint32_t (&s)[N][32]) {
+  float mx[4];  // four chains
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int first = c * N / 4, from = N == 4 ? 0 : 16 * (c & 1), n = N * 8;
+    mx[c] = __uint_as_float(s[first][from]);
+#pragma unroll
+    for (int x = 1; x < n - 1; x += 2)
+      mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[first][from + x])), __uint_as_float(s[first][from + x + 1]));
+    mx[c] = fmaxf(mx[c], __uint_as_float(s[first][from + n - 1]));
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
 // Transposes 4 x 4 pieces of 16 bytes within each quad of lanes: piece r of lane i becomes piece i of
 // lane r. A thread holds a row of the result; after this four lanes hold 64 contiguous bytes of one row,
 // and a store instruction of the warp touches 8 lines instead of 32.
@@ -529,8 +555,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? ring + i % kSegRing : nullptr;
   };
   if (warp >= 8) {
-    // (512 x 128 or 384 x 168 registers at launch cover 256 x 208 + 256 x 48 and 256 x 208 + 128 x 72)
-    if (GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    // (512 x 128 or 384 x 168 registers at launch cover 256 x 176 + 256 x 80 and 256 x 208 + 128 x 72)
+    if (GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (GATHER && warp == 8) {
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
@@ -727,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const uint64_t b = v_desc + (u % C::kStages) * (C::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
-            ptx::tc_mma_f16_ts(o_acc, s_acc + kk * 8, b + kk * (2048 >> 4), idesc_o, (kk > 0 || !first) ? 1u : 0u);
+            ptx::tc_mma_f16_ts(o_acc, s_acc + kPCol + kk * 8, b + kk * (2048 >> 4), idesc_o, (kk > 0 || !first) ? 1u : 0u);
         };
         for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
           const int n = sg->n, kt0 = sg->kt0;
@@ -797,9 +823,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
         ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
       }
-    } else if (GATHER && warp == 11) {
+    } else if (GATHER) {  // (warp 11)
       if (blockIdx.x == 0) attn_check(p, hdr);
-    } else if (!GATHER) {  // ------------------------------------------------ V cleaning warp
+    } else {  // --------------------------------------------------------- V cleaning warp
       uint32_t use = 0, dirty_par = 0;
       bool ok = true;
       const Seg* sg;
@@ -857,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       if (blockIdx.x == 0) attn_check(p, hdr);
     }
   } else {  // -------------------------------------------------------------- softmax groups
-    if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int g = warp >> 2;                 // group
     const int row = threadIdx.x & 127;       // row of the tile
@@ -875,6 +901,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       if (sg->n < 0) break;
       const int i = sg->tok0 + (TWO ? g * tt : 0) + tok_in;   // token of the sequence
       const bool valid = tok_in < tt && i < sg->sq.nq;
+      // a warp without any row only keeps the barriers going (two row tiles: not worth a test)
+      const bool live = TWO || __any_sync(0xffffffffu, valid);
       const int n_all = sg->n, n = TWO && g == 0 ? sg->n0 : n_all;
       const int first = TWO ? 0 : g, step = TWO ? 1 : 2;
       float m = -INFINITY;
@@ -882,19 +910,23 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       for (int j = first; j < n; j += step) {
         const int kt = sg->kt0 + j;
         uint4 seen;
-        if (DENSE) {  // the row's bits of the tile, 16-byte aligned words
+        if (DENSE && live) {  // the row's bits of the tile, 16-byte aligned words
           const int words = attn_mask_words(p), im = min(i, sg->sq.nq - 1);
           seen = __ldg(reinterpret_cast<const uint4*>(p.mask + int64_t(sg->sq.q0 + im) * words) + kt);
         }
         ok = __all_sync(0xffffffffu, wait_bar(s_full + g, s_uses & 1, misc));
         if (!ok) break;
         ++s_uses;
+        if (!live) {
+          if (lane == 0) ptx::mbar_arrive(p_ready + g);
+          continue;
+        }
         ptx::tc_fence_after();
         // Keys that some row does not see: -inf over their scores in TMEM, 32 columns at a time and only
         // where a row of the warp needs it. (As straight code on the 128 registers below it took three
         // times as long: it runs once or twice per row tile and is fetched anew each time.)
-        if (!DENSE && (GATHER || tile_masked(sg, kt))) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
+        if (GATHER ? (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu : !DENSE && tile_masked(sg, kt)) {
           const int im = min(i, sg->sq.nq - 1);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -911,31 +943,27 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           }
           ptx::tc_wait_st();
         }
-        uint32_t s[4][32];
+        // Two row tiles: the row's 128 scores stay in registers. One row tile: 64 at a time, the upper ones last,
+        // and the lower ones are read again for their weights; half the code and registers, which is what
+        // counts beside the gathering warps (350 -> 319 us for 2048 rows x 2052 ids of 64 heads; with two
+        // row tiles the second read costs 5 % at 32,768 tokens).
+        constexpr int kHeld = TWO ? 4 : 2;
+        uint32_t s[kHeld][32];
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 4 / kHeld; ++h) {
+          load_scores<kHeld>(s_col + 64 * h, s);
+          if (DENSE) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tc_ld_32x32b_x32(s_col + 32 * c, s[c]);
-        ptx::tc_wait_ld();
+            for (int c = 0; c < kHeld; ++c) {
+              const uint32_t bits = c == 0 ? seen.x : c == 1 ? seen.y : c == 2 ? seen.z : seen.w;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tc_reg_fence(s[c]);
-        if (DENSE) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = c == 0 ? seen.x : c == 1 ? seen.y : c == 2 ? seen.z : seen.w;
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;
+              for (int x = 0; x < 32; ++x)
+                if (!((bits >> x) & 1u)) s[c][x] = 0xFF800000u;
+            }
           }
+          mt = fmaxf(mt, max_score<kHeld>(s));
         }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int x = 1; x < 31; x += 2)
-            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
-          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool grow = mt > m && (mt - m) * c2 > kLazy;
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = grow ? mt : m;
@@ -959,21 +987,25 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         }
         const float nb = m == -INFINITY ? 0.0f : -m * c2;
         const uint64_t c22 = ptx::pack_f32x2(c2, c2), nb2 = ptx::pack_f32x2(nb, nb);
+#pragma unroll 1
+        for (int h = 4 / kHeld - 1; h >= 0; --h) {
+          if (!TWO && h == 0) load_scores<kHeld>(s_col, s);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < kHeld; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const uint64_t e = ptx::fma_f32x2(
-                ptx::pack_f32x2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), c22, nb2);
-            float a, b;
-            ptx::unpack_f32x2(e, a, b);
-            a = ptx::exp2_approx(a);
-            b = ptx::exp2_approx(b);
-            l2[x & 1] = ptx::add_f32x2(l2[x & 1], ptx::pack_f32x2(a, b));
-            pk[x] = ptx::pack_bf16(a, b);
+            for (int x = 0; x < 16; ++x) {
+              const uint64_t e = ptx::fma_f32x2(
+                  ptx::pack_f32x2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), c22, nb2);
+              float a, b;
+              ptx::unpack_f32x2(e, a, b);
+              a = ptx::exp2_approx(a);
+              b = ptx::exp2_approx(b);
+              l2[x & 1] = ptx::add_f32x2(l2[x & 1], ptx::pack_f32x2(a, b));
+              pk[x] = ptx::pack_bf16(a, b);
+            }
+            ptx::tc_st_32x32b_x16(s_col + kPCol + 32 * h + 16 * c, pk);
           }
-          ptx::tc_st_32x32b_x16(s_col + 16 * c, pk);
         }
         ptx::tc_wait_st();
         ptx::tc_fence_before();
@@ -1028,7 +1060,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       const int col0 = TWO ? 0 : g * kCols;
       const uint32_t oa = tmem + lane_base + 256 + (TWO ? g * D : 0) + col0, ob = tmem + lane_base + 256 + D + col0;
 #pragma unroll 1
-      for (int c = 0; c < kCols / 32; ++c) {
+      for (int c = 0; live && c < kCols / 32; ++c) {
         uint32_t o[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = 0;
