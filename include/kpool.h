@@ -328,7 +328,8 @@ kpool_status kpool_select_rows_ex(const void* q, const float* w, const int32_t* 
  * sequence or row with an out-of-range prefix or sequence id gets out = 0 and
  * lse = -INFINITY; with malformed cumulative lengths the outputs' values are
  * unspecified, and nothing outside the given arrays is read or written.
- * The calls allocate and synchronise nothing and can be captured into a graph.
+ * The calls allocate and synchronise nothing and can be captured into a graph; the
+ * same inputs give the same bits. out and out_lse overlap no input.
  */
 
 /* A [tokens, heads, head_dim] tensor on the device: element (t, h, c) is at
@@ -350,7 +351,9 @@ typedef struct {
   int32_t reserved; /* must be zero */
 } kpool_attention_shape;
 
-/* Workspace size for q_rows query rows of num_seqs sequences; 0 for shapes the calls reject. */
+/* Workspace size for up to q_rows query rows of up to num_seqs sequences, for any of the three
+ * calls; 0 for shapes the calls reject. bf16 at head_dim 64 or 128: partial results of up to 41 MB, and
+ * the bits of a prompt's selection (q_rows^2 / 8 bytes, at most 128 MiB; longer prompts do without them). */
 size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_attention_shape* shape);
 
 /*
