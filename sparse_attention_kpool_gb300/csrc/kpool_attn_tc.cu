@@ -847,18 +847,26 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
           for (int h = 0; h < C::kBlocks; ++h) {
             uint4* block = reinterpret_cast<uint4*>(v + h * C::kHalf);
-#pragma unroll 8
-            for (int x = seen * 8 + lane; x < kTileKeys * 8; x += 32) {
-              if ((x >> 3) >= live) {
-                block[x] = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 q = block[x];
+            const int first = seen * 8, checked = min(live, kTileKeys) * 8;
+            // eight pieces at a time are read and tested together; they are all but always as they should be
+            for (int x0 = first + lane; x0 < checked; x0 += 8 * 32) {
+              uint4 q[8];
+              uint32_t wild = 0;
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                q[y] = x0 + 32 * y < checked ? block[x0 + 32 * y] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
                 // an exponent of all ones carries into bit 15 or 31
                 constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
-                if ((((q.x & kExp) + kOne) | ((q.y & kExp) + kOne) | ((q.z & kExp) + kOne) | ((q.w & kExp) + kOne)) &
-                    0x80008000u) {
-                  bad = true;
-                  uint4 f = q;
+                wild |= ((q[y].x & kExp) + kOne) | ((q[y].y & kExp) + kOne) | ((q[y].z & kExp) + kOne) |
+                        ((q[y].w & kExp) + kOne);
+              }
+              if (wild & 0x80008000u) {
+                bad = true;
+#pragma unroll 1
+                for (int x = x0; x < min(checked, x0 + 8 * 32); x += 32) {
+                  uint4 f = block[x];
                   uint32_t* e = reinterpret_cast<uint32_t*>(&f);
 #pragma unroll
                   for (int y = 0; y < 4; ++y) {
@@ -869,6 +877,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
                 }
               }
             }
+#pragma unroll 4
+            for (int x = max(first, checked) + lane; x < kTileKeys * 8; x += 32) block[x] = make_uint4(0, 0, 0, 0);
           }
           if (bad) misc->bad_seg[i % kSegRing] = i + 1;
           ptx::fence_proxy_async_smem();
