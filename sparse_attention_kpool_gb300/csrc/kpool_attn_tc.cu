@@ -126,7 +126,7 @@ __device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, 
 
 // Beginning and finishing an item (Q, first product, epilogue) takes about as long as this
 // many tiles; it is counted when runs are cut, as positions before the item's first tile.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 3;
 
 // sum over i in [0, n) of floor((a i + b) / m), in steps of Euclid's algorithm on (m, a)
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
