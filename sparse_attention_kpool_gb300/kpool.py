@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -492,29 +493,22 @@ def new_attention_workspace(q_rows: int, num_seqs: int, q_heads: int, kv_heads: 
 
 
 class _AttentionArgs(threading.local):
-    """A thread's argument structures, filled anew by every call (building them took most of a short call)."""
+    """A thread's argument structures (q, k, v, out and the shape in one buffer), filled anew by every
+    call: building them took most of a short call."""
 
     def __init__(self):
-        self.heads = [kpool_heads() for _ in range(4)]  # q, k, v, out
-        self.shape = kpool_attention_shape()
+        size = ctypes.sizeof(kpool_heads)
+        self.buffer = bytearray(4 * size + ctypes.sizeof(kpool_attention_shape))
+        self.heads = [kpool_heads.from_buffer(self.buffer, i * size) for i in range(4)]
+        self.shape = kpool_attention_shape.from_buffer(self.buffer, 4 * size)
         self.refs = [ctypes.byref(h) for h in self.heads]
         self.shape_ref = ctypes.byref(self.shape)
-        self.options = {k: kpool_options(k) for k in (KPOOL_SCORE_TC, KPOOL_SCORE_SIMT)}
+        # data, token_stride, head_stride four times; q_heads, kv_heads, head_dim, dtype, scale, reserved
+        self.pack = struct.Struct("=" + "Qqq" * 4 + "iiiifi").pack_into
 
 
 _attention_args = _AttentionArgs()
 _ATTENTION_DTYPES = {torch.bfloat16: KPOOL_BF16, torch.float32: KPOOL_F32}
-
-
-def _set_heads(h: kpool_heads, t: torch.Tensor, shape, what: str):
-    ts, hs, ds = t.stride()
-    n, heads, d = shape
-    if not t.is_cuda or (ds != 1 and d > 1):
-        raise ValueError(f"{what} must be a CUDA tensor whose last dimension is contiguous")
-    h.data = t.data_ptr()
-    # the stride of a dimension of one element carries no meaning in torch
-    h.token_stride = ts if n > 1 else d
-    h.head_stride = hs if heads > 1 else d
 
 
 def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse, workspace, stream, score_kernel):
@@ -529,6 +523,7 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     if code is None:
         raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
     R, hq, d = qs
+    T, hkv, _ = ks
     if out is None:
         out = torch.empty((R, hq, d), dtype=dtype, device=q.device)
     elif out.shape != qs or out.dtype != dtype:
@@ -539,15 +534,14 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     elif out_lse.dtype != torch.float32 or out_lse.shape != (R, hq):
         raise TypeError("out_lse must be float32 [rows, q_heads]")
     if workspace is None:
-        workspace = new_attention_workspace(R, num_seqs, hq, ks[1], d, dtype, q.device)
-    a = _attention_args
-    h = a.heads
-    _set_heads(h[0], q, qs, "q")
-    _set_heads(h[1], k, ks, "k")
-    _set_heads(h[2], v, ks, "v")
-    _set_heads(h[3], out, qs, "out")
-    sh = a.shape
-    sh.q_heads, sh.kv_heads, sh.head_dim, sh.dtype, sh.scale = hq, ks[1], d, code, scale
+        workspace = new_attention_workspace(R, num_seqs, hq, hkv, d, dtype, q.device)
+    fields = []
+    for t, n, h in ((q, R, hq), (k, T, hkv), (v, T, hkv), (out, R, hq)):
+        ts, hs, ds = t.stride()
+        if not t.is_cuda or (ds != 1 and d > 1):
+            raise ValueError("q, k, v and out must be CUDA tensors whose last dimension is contiguous")
+        # the stride of a dimension of one element carries no meaning in torch
+        fields += (t.data_ptr(), ts if n > 1 else d, hs if h > 1 else d)
     args = []
     for x in arrays:
         if isinstance(x, torch.Tensor):
@@ -558,13 +552,20 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
             args.append(x.data_ptr())
         else:
             args.append(x)
-    _check_cuda(out_lse, workspace)
-    r = a.refs
+    lse = None
+    if out_lse is not None:
+        if not out_lse.is_cuda or not out_lse.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+        lse = out_lse.data_ptr()
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    a = _attention_args
+    a.pack(a.buffer, 0, *fields, hq, hkv, d, code, scale, 0)
+    rq, rk, rv, ro = a.refs
     st = getattr(_lib or load(), name)(
-        r[0], r[1], r[2], *args, num_seqs, R, ks[0], a.shape_ref, r[3], None if out_lse is None else out_lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(),
+        rq, rk, rv, *args, num_seqs, R, T, a.shape_ref, ro, lse, workspace.data_ptr(), workspace.nbytes,
         torch._C._cuda_getCurrentRawStream(q.device.index) if stream is None else _stream(stream),
-        None if score_kernel == KPOOL_SCORE_AUTO else a.options.get(score_kernel, kpool_options(score_kernel)))
+        None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
     if st != KPOOL_OK:
         raise KpoolError(st, name)
     return out, out_lse
