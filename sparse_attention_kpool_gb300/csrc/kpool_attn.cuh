@@ -176,14 +176,17 @@ __device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, in
   *nk = hi - lo;
 }
 
-// Runs of the persistent tensor-core form: CTAs, sequences it takes, row tiles per SM from
-// which one CTA per row tile is used instead, and the rows of one partial result.
+// The persistent tensor-core form: its runs (CTAs) and the sequences it takes. Beside it, whole row tiles per CTA
+// (kpool_attn_tc.cu, launch): up to kAttnWholeKeys keys; kAttnLikeKeys keys a sequence at one or two row tiles
+// per SM; from kAttnDirectItems row tiles per SM and kAttnDirectKeys keys a sequence on.
 constexpr int kAttnMaxRuns = 152;
 constexpr int kAttnMaxRunSeqs = 8192;
+constexpr int kAttnWholeKeys = 1024;
+constexpr int kAttnLikeKeys = 2600;
 constexpr int kAttnDirectItems = 6;
 constexpr int kAttnDirectKeys = 8192;
-constexpr int kAttnWholeKeys = 512;
 constexpr int kAttnJoinBytes = 64;   // per run: what the join of the rows before it needs
+// Rows of one partial result.
 inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
   const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned
   return int(rows < tile_rows ? rows : tile_rows);

@@ -80,7 +80,7 @@ struct Cfg {
   // seg_full[ring] seg_empty[ring] turn[2]
   static constexpr int kNumBars = 4 * kStages + 11 + 2 * kSegRing;
   static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;  // 16-byte words follow
-  static constexpr int kOffSeg = kOffMisc + 64;
+  static constexpr int kOffSeg = kOffMisc + 80;
   static constexpr int kOffStat = kOffSeg + 64 * kSegRing;         // [2][128] float2 (m, l), one-tile form only
   static constexpr int kOffBits = kOffStat + (TWO ? 0 : 2 * kTileRows * 8);  // [kBitsRing] x 128 bits
   static_assert(kOffBits % 16 == 0 && kOffSeg % 16 == 0 && kOffStat % 16 == 0, "16-byte accesses");
@@ -98,12 +98,13 @@ struct Misc {
   int64_t base;       // persistent form: first position of sequence b
   int64_t lo, hi;     // positions of this CTA
   int64_t total;
+  int32_t runs;       // runs that have tiles
   int32_t b;
   uint32_t tmem;
   volatile int32_t abort;
   volatile int32_t bad_seg[kSegRing];  // 1 + the last segment of this slot with an infinity or NaN in a cleaned V tile
 };
-static_assert(sizeof(Misc) <= 64, "Misc fits its space");
+static_assert(sizeof(Misc) <= 80, "Misc fits its space");
 
 // ------------------------------------------------------------------ work segments
 
@@ -287,10 +288,18 @@ __device__ __forceinline__ void finish_seg(const AttnParams& p, int tt, int ttb,
   s->all = p.mask ? s->sq.prefix : s->sq.prefix + s->tok0 + 1;
 }
 
+// A run has at least this many positions: shorter ones would spend their time on their start, and a row
+// on joining them.
+constexpr int kMinRun = 3;
+__host__ __device__ __forceinline__ int64_t run_count(int64_t total, int64_t ctas) {
+  const int64_t n = total / kMinRun < ctas ? total / kMinRun : ctas;
+  return n < 1 ? 1 : n;
+}
+
 // Every thread of the CTA: this CTA's run of positions [total * i / n, total * (i + 1) / n)
 // and the sequence it starts in. `scratch` holds S 64-bit words of shared memory.
-__device__ __forceinline__ int64_t find_run(const AttnParams& p, int ttb, int64_t* scratch, int64_t i, int64_t n,
-                                            Misc* m) {
+__device__ __forceinline__ void find_run(const AttnParams& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas,
+                                         Misc* m) {
   for (int b = threadIdx.x; b < p.S; b += blockDim.x) scratch[b] = seq_cost(p, attn_seq(p, b), ttb);
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -299,7 +308,7 @@ __device__ __forceinline__ int64_t find_run(const AttnParams& p, int ttb, int64_
     for (int b = lane; b < p.S; b += 32) sum += scratch[b];
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const int64_t lo = sum * i / n, hi = sum * (i + 1) / n;
+    const int64_t n = run_count(sum, ctas), lo = i < n ? sum * i / n : sum, hi = i < n ? sum * (i + 1) / n : sum;
     int64_t run = 0;
     bool found = false;
     for (int b0 = 0; b0 < p.S && !found; b0 += 32) {
@@ -322,10 +331,10 @@ __device__ __forceinline__ int64_t find_run(const AttnParams& p, int ttb, int64_
       m->lo = lo;
       m->hi = found ? hi : lo;
       m->total = sum;
+      m->runs = int(n);
     }
   }
   __syncthreads();
-  return m->total;
 }
 
 // What the join of the rows that the border before run r cuts needs; runs = 0: nothing to join here.
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         for (int i = 0;; ++i) {
           const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
           if (i == 0 && !direct) {
-            if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, gridDim.x);
+            if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
             else joins[blockIdx.x].runs = 0;
           }
           if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
@@ -1176,14 +1185,38 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 //
 // CTA x adds up, in the order of the runs, the partial results of the rows that the border
 // before run x + 1 cuts (if that run was the first to begin inside them: its producer left the
-// item's data). y: 32 rows each, four at a time to a warp, a lane holds D / 32 channels. Reads a
-// few MB that the runs have just written, from L2.
-constexpr int kJoinRows = 32;
+// item's data). A warp takes four rows, a lane D / 32 channels. kSplit: the 8 warps of a CTA share
+// four rows and each takes every eighth run (few items, each cut into many runs); else they take
+// 32 rows, most of them cut into two or three runs. What is read is a few MB just written; with kSplit
+// four runs are read at a time, since the latency of one read after the other made 100 us of 154 runs.
 
 template <int D>
+struct JoinRow {
+  static constexpr int kPer = D / 32;
+  float acc[kPer], m, l;
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[y] = 0.0f;
+  }
+  // adds the part (o, pm, pl); one without any weight adds nothing, with a NaN among its scores its sum passes on
+  __device__ __forceinline__ void add(const float (&o)[kPer], float pm, float pl, float c2) {
+    const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
+    const float f = m == -INFINITY ? 1.0f : exp2f((m - base) * c2);
+    const float w = pm == -INFINITY ? 1.0f : exp2f((pm - base) * c2);
+    l = l * f + pl * w;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[y] = acc[y] * f + o[y] * w;
+    m = mn;
+  }
+};
+
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(256)
     attn_join_kernel(const __grid_constant__ AttnParams p, int tt, const JoinItem* joins, const float* part,
                      int slot_rows) {
+  constexpr int kPer = D / 32, kRows = 4, kJoinBatch = kSplit ? 4 : 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
   const JoinItem it = joins[blockIdx.x + 1];
   if (it.runs == 0) return;
@@ -1193,77 +1226,94 @@ __global__ void __launch_bounds__(256)
   int first = blockIdx.x;
   while (first > 0 && run_lo(first) > it.item) --first;
   const float c2 = p.scale * kLog2e;
-  constexpr int kPer = D / 32;
   const size_t stride = size_t(slot_rows) * (D + 2);
-  // the warp's rows: four of the block's 32
-  int vr[4], tok[4];
-  float acc[4][kPer], mm[4], ll[4];
+  int vr[kRows], tok[kRows];
+  JoinRow<D> row[kRows];
   bool any = false;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    vr[x] = blockIdx.y * kJoinRows + warp * 4 + x;
-    const int q_tile = vr[x] / kTileRows, row = vr[x] - q_tile * kTileRows, in = row / p.G;
+  for (int x = 0; x < kRows; ++x) {
+    vr[x] = (kSplit ? int(blockIdx.y) : int(blockIdx.y) * 8 + warp) * kRows + x;
+    const int q_tile = vr[x] / kTileRows, in = (vr[x] - q_tile * kTileRows) / p.G;
     tok[x] = vr[x] < slot_rows && in < tt && it.tok0 + q_tile * tt + in < it.nq ? it.tok0 + q_tile * tt + in : -1;
     any |= tok[x] >= 0;
-    mm[x] = -INFINITY;
-    ll[x] = 0.0f;
-#pragma unroll
-    for (int y = 0; y < kPer; ++y) acc[x][y] = 0.0f;
+    row[x].clear();
   }
   if (!any) return;
-  for (int64_t r = first; r < it.runs; ++r) {
-    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
-    if (lo >= it.item + it.tiles) break;
-    if (hi <= it.item || hi == lo) continue;
-    const float* s = part + (size_t(r) * 2 + (lo > it.item ? 0 : 1)) * stride;
-    float o[4][kPer];
-    float2 ml[4];
+  const int64_t end = it.item + it.tiles;
+  for (int64_t r0 = first + (kSplit ? warp : 0); r0 < it.runs && run_lo(r0) < end;
+       r0 += kJoinBatch * (kSplit ? 8 : 1)) {
+    float o[kJoinBatch][kRows][kPer];
+    float2 ml[kJoinBatch][kRows];
+    bool has[kJoinBatch];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (tok[x] < 0) continue;
-      ml[x] = *reinterpret_cast<const float2*>(s + size_t(slot_rows) * D + 2 * vr[x]);
-      if (D == 128) {
-        const float4 f = *reinterpret_cast<const float4*>(s + size_t(vr[x]) * D + 4 * lane);
-        o[x][0] = f.x;
-        o[x][1] = f.y;
-        o[x][kPer - 2] = f.z;
-        o[x][kPer - 1] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(s + size_t(vr[x]) * D + 2 * lane);
-        o[x][0] = f.x;
-        o[x][1] = f.y;
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const int64_t r = r0 + b * (kSplit ? 8 : 1), lo = run_lo(r), hi = run_lo(r + 1);
+      has[b] = r < it.runs && lo < end && hi > it.item && hi > lo;
+      if (!has[b]) continue;
+      const float* s = part + (size_t(r) * 2 + (lo > it.item ? 0 : 1)) * stride;
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        if (tok[x] < 0) continue;
+        ml[b][x] = *reinterpret_cast<const float2*>(s + size_t(slot_rows) * D + 2 * vr[x]);
+        const float* at = s + size_t(vr[x]) * D + kPer * lane;
+        if (D == 128) {
+          const float4 f = *reinterpret_cast<const float4*>(at);
+          o[b][x][0] = f.x;
+          o[b][x][1] = f.y;
+          o[b][x][kPer - 2] = f.z;
+          o[b][x][kPer - 1] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(at);
+          o[b][x][0] = f.x;
+          o[b][x][1] = f.y;
+        }
       }
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (tok[x] < 0) continue;
-      const float mn = fmaxf(mm[x], ml[x].x);
-      const float base = mn == -INFINITY ? 0.0f : mn;
-      const float f = mm[x] == -INFINITY ? 1.0f : exp2f((mm[x] - base) * c2);
-      // a part without any weight adds nothing; with a NaN among its scores its sum passes on
-      const float w = ml[x].x == -INFINITY ? 1.0f : exp2f((ml[x].x - base) * c2);
-      ll[x] = ll[x] * f + ml[x].y * w;
+    for (int b = 0; b < kJoinBatch; ++b)
 #pragma unroll
-      for (int y = 0; y < kPer; ++y) acc[x][y] = acc[x][y] * f + o[x][y] * w;
-      mm[x] = mn;
+      for (int x = 0; x < kRows; ++x)
+        if (has[b] && tok[x] >= 0) row[x].add(o[b][x], ml[b][x].x, ml[b][x].y, c2);
+  }
+  if (kSplit) {  // warp x < 4 finishes row x, adding the warps' parts in their order
+    __shared__ float s_o[8][kRows][D];
+    __shared__ float2 s_ml[8][kRows];
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) s_o[warp][x][kPer * lane + y] = row[x].acc[y];
+      if (lane == 0) s_ml[warp][x] = make_float2(row[x].m, row[x].l);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+      if (x != warp) {
+        tok[x] = -1;
+        continue;
+      }
+      row[x].clear();
+      for (int w = 0; w < 8; ++w) {
+        float o[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) o[y] = s_o[w][x][kPer * lane + y];
+        row[x].add(o, s_ml[w][x].x, s_ml[w][x].y, c2);
+      }
     }
   }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
+  for (int x = 0; x < kRows; ++x) {
     if (tok[x] < 0) continue;
-    const bool none = mm[x] == -INFINITY && ll[x] == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / ll[x];
+    const bool none = row[x].m == -INFINITY && row[x].l == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / row[x].l;
     const int head = it.hk * p.G + (vr[x] % kTileRows) % p.G;
-    const int64_t row = int64_t(it.q0) + tok[x];
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.o_ts + int64_t(head) * p.o_hs + kPer * lane;
-    uint32_t u[kPer / 2];
+    const int64_t at = int64_t(it.q0) + tok[x];
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at * p.o_ts + int64_t(head) * p.o_hs + kPer * lane;
 #pragma unroll
-    for (int y = 0; y < kPer / 2; ++y)
-      u[y] = none ? 0u : ptx::pack_bf16(acc[x][2 * y] * inv, acc[x][2 * y + 1] * inv);
-    if (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[kPer / 2 - 1]);
-    else *reinterpret_cast<uint32_t*>(dst) = u[0];
+    for (int y = 0; y < kPer; y += 2)
+      *reinterpret_cast<uint32_t*>(dst + y) =
+          none ? 0u : ptx::pack_bf16(row[x].acc[y] * inv, row[x].acc[y + 1] * inv);
     if (lane == 0 && p.lse)
-      p.lse[row * p.Hq + head] = none ? -INFINITY : (mm[x] * c2 + log2f(ll[x])) * kLn2;
+      p.lse[at * p.Hq + head] = none ? -INFINITY : (row[x].m * c2 + log2f(row[x].l)) * kLn2;
   }
 }
 
@@ -1286,18 +1336,25 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
-  // Where an item has few tiles at most (the call's keys, the ids of a row), cutting them to fill the
-  // SMs saves less than the join costs: whole items, one to a CTA.
-  // Gathered items all have the same tiles: one CTA each (and two tiles' time for its start and end) against
-  // runs of all tiles and a join of about five tiles' time.
+  // Equal runs of all K/V tiles fill the SMs whatever the lengths are, and cost a join (about five tiles' time)
+  // and the starts of the items they cut. Whole items, one to a CTA, are taken instead (us, 32 / 8 heads of 128
+  // unless said otherwise):
+  //  - where an item has few tiles at most: one prompt of 600 tokens 16 against 28, of 900 21 against 36, a
+  //    decode step at 900 keys 14 against 22;
+  //  - for one or two items per SM of like sequences, which end about together: 1,500 tokens 38 against 46,
+  //    4 x 300 22 against 28, 1,400 of 64 / 1 heads 47 against 62 (32 x 256, ten per SM: 87 against 68);
+  //  - for long sequences with many items (deepest first, a head's K and V in L2): 32,768 tokens 6.1 against
+  //    6.5 ms;
+  //  - for gathered items, all of the same tiles, where their rounding up to the SMs costs less than the join.
   const int64_t nt = (p.width + kTileKeys - 1) / kTileKeys;
-  const bool whole = GATHER && !p.list && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
-  const bool small = whole || ((GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms && !p.list);
-  const bool direct = !GATHER && (small || p.S > kAttnMaxRunSeqs ||
-                                  (C::TWO && items >= int64_t(kAttnDirectItems) * sms &&
-                                   p.T >= int64_t(kAttnDirectKeys) * p.S));
+  const bool even = GATHER && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
+  const bool small = !p.list && (even || ((GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
+  const bool like = F == kTwo && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
+  const bool deep = C::TWO && items >= int64_t(kAttnDirectItems) * sms && p.T >= int64_t(kAttnDirectKeys) * p.S;
+  const bool direct = !GATHER && (small || like || deep || p.S > kAttnMaxRunSeqs);
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
-  const int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
+  int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
+  if (GATHER && !small && !p.list) grid = int(run_count(items * nt, grid));
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
@@ -1317,7 +1374,10 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || small || grid < 2) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + kJoinRows - 1) / kJoinRows));
+  // many runs to an item: a CTA's warps share its rows; else each has its own
+  const bool split = items * (slot_rows <= 64 ? 4 : 16) <= grid;
+  const int join_rows = split ? 4 : 32;
+  cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + join_rows - 1) / join_rows));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -1325,7 +1385,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p, tt, static_cast<const JoinItem*>(joins),
+  e = cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, p, tt, static_cast<const JoinItem*>(joins),
                          static_cast<const float*>(part), slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

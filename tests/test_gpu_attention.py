@@ -142,6 +142,18 @@ def test_tree_rows_that_see_nothing(family):
     assert (out[0] == 0).all() and torch.isinf(lse[0]).all()
 
 
+@pytest.mark.parametrize("heads,nodes,prefixes", [
+    ((64, 1, 128), [1, 1], [20000, 3000]), ((16, 1, 64), [40, 3], [8000, 200]), ((8, 8, 128), [1], [30000]),
+    ((32, 8, 128), [16, 30, 8], [3000, 1000, 9000]), ((4, 4, 64), [1], [1500]),
+], ids=str)
+def test_rows_cut_into_many_runs(heads, nodes, prefixes):
+    """One item over all CTAs of the GPU: joins of more than a hundred partial results."""
+    extents = [p + n for p, n in zip(prefixes, nodes)]
+    (q, k, v, scale), out, lse, ws = run_tree(nodes, prefixes, extents, None, heads, BF, "auto", seed=77)
+    assert K.kpool_last_device_error(ws) == K.KPOOL_OK
+    A.check(out, lse, A.reference(q, k, v, A.see_tree(nodes, extents, prefixes, None), scale))
+
+
 @pytest.mark.parametrize("heads", [(8, 2, 128, BF), (16, 1, 64, BF), (8, 8, 128, BF)], ids=str)
 def test_decode_long_cache(heads):
     """Few rows over long caches: the key axis is split over CTAs and joined."""
@@ -166,7 +178,7 @@ def test_many_sequences():
     ([500], [500], (128, 1, 128)), ([4000], [4000], (32, 8, 128)), ([70, 500, 3], [900, 500, 1500], (128, 1, 64)),
     ([1] * 40, [3000] * 40, (8, 2, 128)), ([6000, 1, 900], [6000, 7000, 1000], (32, 8, 64)), ([12000], [12000], (32, 8, 128)),
     ([20, 7, 1], [300, 20000, 4000], (24, 4, 64)), ([900, 64, 300], [300, 0, 2000], (8, 2, 128)),
-    ([1] * 9 + [1200], [2] * 9 + [1200], (8, 2, 128)),
+    ([1] * 9 + [1200], [2] * 9 + [1200], (8, 2, 128)), ([1500], [1500], (32, 8, 128)), ([1100], [1100], (8, 8, 128)),
 ], ids=str)
 def test_runs_of_many_segments(ql, kl, heads):
     """Every split of the work (one CTA per row tile; equal runs with several segments, joined or not)
