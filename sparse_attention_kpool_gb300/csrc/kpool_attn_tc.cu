@@ -516,10 +516,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     return;
   }
   if (GATHER) {
+    // (listed rows, mostly none: whole items, so that there is nothing to join)
+    const int64_t total = gather_total(p), unit = p.list ? gather_tiles(p) : 1;
+    const int64_t lo = total / unit * blockIdx.x / gridDim.x * unit;
+    const int64_t hi = total / unit * (blockIdx.x + 1) / gridDim.x * unit;
+    if (p.list && lo == hi) return;
     if (threadIdx.x == 0) {
-      const int64_t total = gather_total(p);
-      misc->lo = total * blockIdx.x / gridDim.x;
-      misc->hi = total * (blockIdx.x + 1) / gridDim.x;
+      misc->lo = lo;
+      misc->hi = hi;
     }
   } else if (!direct) {
     find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, misc);
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const bool more = gather_seg(p, &pos, hi, &sg);
           if (i == 0) {
             const int nt = gather_tiles(p);
-            if (direct) {
+            if (direct || p.list) {
               // whole items: nothing to join
             } else if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, gather_total(p), blockIdx.x,
                                  gridDim.x);
@@ -1372,7 +1376,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
                                                   joins, hdr);
   e = cudaGetLastError();
-  if (e != cudaSuccess || direct || small || grid < 2) return e;
+  if (e != cudaSuccess || direct || small || p.list || grid < 2) return e;
   cudaLaunchConfig_t cfg{};
   // many runs to an item: a CTA's warps share its rows; else each has its own
   const bool split = items * (slot_rows <= 64 ? 4 : 16) <= grid;
