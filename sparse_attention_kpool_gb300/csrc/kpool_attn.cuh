@@ -204,7 +204,7 @@ inline size_t attn_mask_bytes(int64_t R) {
   return size_t(all < (int64_t(128) << 20) ? all : (int64_t(128) << 20));
 }
 inline size_t attn_list_bytes(int64_t R) { return (size_t(R) * 4 + 255) & ~size_t(255); }
-bool attn_dense_wanted(const AttnParams& p);
+bool attn_dense_wanted(const AttnParams& p, int sms);
 cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t* mask, int32_t* list,
                                    cudaStream_t stream);
 

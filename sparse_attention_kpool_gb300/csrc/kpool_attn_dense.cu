@@ -109,13 +109,19 @@ __global__ void __launch_bounds__(256) dense_mask_kernel(const __grid_constant__
 
 }  // namespace
 
-bool attn_dense_wanted(const AttnParams& p) {
-  if (p.row_seq != nullptr || p.width == 0) return false;
-  // A gathered tile of 128 keys takes about 3300 cycles for one row and key head; a dense one about 4200
-  // for 256 / G rows, and a row goes over half its sequence: 0.064 G keys against 26 width.
-  const int64_t keys = p.T / p.S, tiles = int64_t(p.R) * p.Hkv * ((p.width + 127) / 128);
-  if (tiles < 1024 || keys * p.G > int64_t(256) * p.width) return false;
-  return int64_t(p.R) * ((keys + 127) / 128) * 16 <= attn_mask_bytes(p.R) && p.S <= kAttnMaxRunSeqs;
+bool attn_dense_wanted(const AttnParams& p, int sms) {
+  if (p.row_seq != nullptr || p.width == 0 || p.S > kAttnMaxRunSeqs) return false;
+  const int64_t keys = p.T / p.S;  // of a sequence, on average: a row goes over half of them
+  if (int64_t(p.R) * ((keys + 127) / 128) * 16 > int64_t(attn_mask_bytes(p.R))) return false;
+  // Microseconds of either way, from their measured parts: a gathered (row, key head) takes 3 and 1.25 for each
+  // tile of 128 ids; a dense item (256 / G rows) 6 and 2 for each tile of its keys, the kernels around it 25.
+  // Measured dense / gathered: 32 / 8 heads of 128, 3,000 rows x 24 ids 114 / 684, 1,500 x 516 56 / 742,
+  // 16,000 x 512 1,676 / 6,407, 100 x 32 17 / 31; 64 / 1 heads, 600 x 1,004 25 / 63, 2,000 x 128 110 / 63,
+  // 3,000 x 68 182 / 89.
+  const double items = double(p.R) * p.Hkv / sms;
+  const double gathered = 6.0 + items * (3.0 + 1.25 * ((p.width + 127) / 128));
+  const double dense = 25.0 + items * p.G / 256.0 * (6.0 + 2.0 * double(keys) / 256.0);
+  return dense < gathered;
 }
 
 cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t* mask, int32_t* list,
