@@ -194,7 +194,8 @@ inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
 // AttnDense, the runs' join items and the partial results of the persistent form: two per run,
 // [rows][D] fp32 and (m, l) per row.
 inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
-  return 256 + size_t(kAttnMaxRuns) * kAttnJoinBytes + size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
+  return 256 + size_t(kAttnMaxRuns) * kAttnJoinBytes +
+         size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
 }
 
 // The dense form of a selection: whether the host tries it, the bytes of its mask for R rows, and the

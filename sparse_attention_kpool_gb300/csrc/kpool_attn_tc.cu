@@ -1,20 +1,35 @@
-// kpool_attn_tc.cu -- prompt and tree attention on the 5th-generation tensor cores (bf16,
-// head_dim 64 or 128): one pass over K and V with the running maximum and sum of a softmax.
+// kpool_attn_tc.cu -- attention on the 5th-generation tensor cores (bf16, head_dim 64 or
+// 128): one pass over K and V with the running maximum and sum of a softmax.
 //
 // Rows. The G query heads that share a key head and TT = 128 / G tokens fill the 128 rows of
 // an MMA (row = token * G + head of the group), so a K/V tile read once serves all of them,
-// decode steps of one token included. A CTA holds two such row tiles ("two", 2 * TT tokens that
-// share every K/V tile) or, where sequences have fewer rows, one tile whose K/V tiles alternate
-// between the two softmax groups ("one": each group keeps its own accumulator and statistics,
-// added up at the end).
+// decode steps of one token included. Four forms (Form):
+//   kTwo     two such row tiles per CTA, 2 * TT tokens that share every K/V tile;
+//   kOne     one row tile, where sequences have fewer rows: its K/V tiles alternate between
+//            the two softmax groups, each with its own accumulator and statistics, added up at
+//            the end;
+//   kGather  kOne for the heads of one token over the keys that its ids name: four warps
+//            copy them, 16 bytes a lane (cp.async), into the layout that TMA writes. (TMA's
+//            gather of four rows moved 6 bytes a cycle and SM, these copies 27; 2048 rows x
+//            2052 ids of 64 / 1 heads: 1222 against 288 us.)
+//   kDense   kTwo under a mask of bits for all keys (kpool_attn_dense.cu).
 //
-// Roles (12 warps): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread per row; warp 8
-// loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns TMEM); warp 11
-// cleans V tiles (below). Per
-// 128-key tile of a group: S = Q K^T (128 x 128, fp32 in TMEM); its thread reads the row, takes
-// the maximum, writes P = 2^(c s - c m) as bf16 over S in TMEM and adds its fp32 sum; O += P V
-// with P read from TMEM. The tensor core works on one group while the other does its softmax.
-// K and V share one ring of tiles in the order in which the MMAs consume them.
+// Roles (12 warps; kGather 16): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread
+// per row; warp 8 loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns
+// TMEM); warp 11 cleans V tiles (below), warps 12-15 gather. Per 128-key tile of a group:
+// S = Q K^T (128 x 128, fp32 in TMEM); its thread reads the row, takes the maximum, writes
+// P = 2^(c s - c m) as bf16 over S in TMEM and adds its fp32 sum; O += P V with P read from
+// TMEM. K and V share one ring of tiles in the order in which the MMAs consume them.
+//
+// What bounds it. Of an MMA's 64 cycles at full rate, Q K^T alone (both operands from shared
+// memory) takes 93 and P V alone (one from TMEM) 75; alternating they run at 64, so the tensor
+// core could do a pair of tiles in 2048 cycles. A tile's chain, softmax (1260 cycles: 128
+// exponentials at 4 cycles a warp instruction are 512 of them), handing P over (390), P V and
+// the next Q K^T (1200), handing S over (400), is 3250, and with two groups in flight that is
+// the time of a pair. 32,768 tokens of 32 / 8 heads of 128: 5.95 ms = 1.48 PFLOP/s, 86 % of
+// the measured sustained rate of a large product. Decode is bound by HBM: 792 MB of caches in
+// 139 us = 5.7 TB/s, 84 % of the measured copy rate. Short sequences pay 4 to 6 us of start,
+// masks and epilogue per row tile.
 //
 // Running maximum. O is rescaled only when a row's maximum has grown by more than 8 in the
 // exponent: weights then reach at most 2^8, which costs neither bf16 nor fp32 any precision,
@@ -26,12 +41,13 @@
 // matter. A weight of zero does not silence V, though (0 * NaN): in the tiles that some row
 // does not see entirely, warp 11 first overwrites V rows past the last visible key with
 // zeros, replaces every other infinity or NaN by zero and raises a flag; rows that do see such
-// a value add it in the epilogue.
+// a value add it in the epilogue. (kGather writes zeros for ids outside the sequence.)
 //
-// Work. A pass over (sequence, key head, row tile, K/V tile). Many row tiles: one CTA each,
-// the deepest first. Few: a persistent CTA per SM takes an equal run of all K/V tiles of the
-// call (found by every CTA itself from the lengths on the device), unfinished rows go to the
-// workspace as (m, l, O) and a second kernel joins them in order, so results repeat bit for bit.
+// Work. A pass over (sequence, key head, row tile, K/V tile): whole row tiles, one to a CTA,
+// or a persistent CTA per SM with an equal run of all K/V tiles of the call, found by every CTA
+// itself from the lengths on the device; unfinished rows go to the workspace as (m, l, O) and
+// a second kernel joins them in the order of the runs, so results repeat bit for bit. launch()
+// has the rule and both sides' times.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -247,7 +263,9 @@ __device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int til
 
 // Gathered form: every row and key head has the same number of tiles, and positions run over
 // rows, then key heads (the heads of a token lie together in memory).
-__device__ __forceinline__ int gather_tiles(const AttnParams& p) { return max(1, (p.width + kTileKeys - 1) / kTileKeys); }
+__device__ __forceinline__ int gather_tiles(const AttnParams& p) {
+  return max(1, (p.width + kTileKeys - 1) / kTileKeys);
+}
 
 __device__ __forceinline__ int64_t gather_total(const AttnParams& p) {
   const int rows = p.list && p.dense->enabled ? p.dense->listed : p.R;
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   uint64_t* o_free = q_full + 7;
   uint64_t* done = q_full + 8;
   uint64_t* seg_full = q_full + 9;              // [kSegRing]
-  uint64_t* seg_empty = seg_full + kSegRing;    // [kSegRing]: 8 softmax warps, 2 MMA issuers, the cleaning or gathering warps
+  uint64_t* seg_empty = seg_full + kSegRing;    // [kSegRing]: all that read segments
   uint64_t* turn = seg_empty + kSegRing;        // [2]: it is this issuer's turn
   Seg* ring = reinterpret_cast<Seg*>(smem + C::kOffSeg);
   Misc* misc = reinterpret_cast<Misc*>(smem + C::kOffMisc);
@@ -766,7 +784,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const uint64_t b = v_desc + (u % C::kStages) * (C::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
-            ptx::tc_mma_f16_ts(o_acc, s_acc + kPCol + kk * 8, b + kk * (2048 >> 4), idesc_o, (kk > 0 || !first) ? 1u : 0u);
+            ptx::tc_mma_f16_ts(o_acc, s_acc + kPCol + kk * 8, b + kk * (2048 >> 4), idesc_o,
+                               (kk > 0 || !first) ? 1u : 0u);
         };
         for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
           const int n = sg->n, kt0 = sg->kt0;
@@ -1389,7 +1408,8 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, p, tt, static_cast<const JoinItem*>(joins),
+  e = cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, p, tt,
+                         static_cast<const JoinItem*>(joins),
                          static_cast<const float*>(part), slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
