@@ -535,13 +535,23 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
         raise TypeError("out_lse must be float32 [rows, q_heads]")
     if workspace is None:
         workspace = new_attention_workspace(R, num_seqs, hq, hkv, d, dtype, q.device)
-    fields = []
-    for t, n, h in ((q, R, hq), (k, T, hkv), (v, T, hkv), (out, R, hq)):
-        ts, hs, ds = t.stride()
-        if not t.is_cuda or (ds != 1 and d > 1):
-            raise ValueError("q, k, v and out must be CUDA tensors whose last dimension is contiguous")
-        # the stride of a dimension of one element carries no meaning in torch
-        fields += (t.data_ptr(), ts if n > 1 else d, hs if h > 1 else d)
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and workspace.is_cuda):
+        raise ValueError("tensors must be CUDA tensors")
+    qt, qh, qd = q.stride()
+    kt, kh, kd = k.stride()
+    vt, vh, vd = v.stride()
+    ot, oh, od = out.stride()
+    if not qd == kd == vd == od == 1 and d > 1:
+        raise ValueError("the last dimension of q, k, v and out must be contiguous")
+    # the stride of a dimension of one element carries no meaning in torch
+    if R <= 1:
+        qt = ot = d
+    if T <= 1:
+        kt = vt = d
+    if hq == 1:
+        qh = oh = d
+    if hkv == 1:
+        kh = vh = d
     args = []
     for x in arrays:
         if isinstance(x, torch.Tensor):
@@ -557,14 +567,15 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
         if not out_lse.is_cuda or not out_lse.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
         lse = out_lse.data_ptr()
-    if not workspace.is_cuda or not workspace.is_contiguous():
+    if not workspace.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors")
     a = _attention_args
-    a.pack(a.buffer, 0, *fields, hq, hkv, d, code, scale, 0)
+    a.pack(a.buffer, 0, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh,
+           hq, hkv, d, code, scale, 0)
     rq, rk, rv, ro = a.refs
     st = getattr(_lib or load(), name)(
         rq, rk, rv, *args, num_seqs, R, T, a.shape_ref, ro, lse, workspace.data_ptr(), workspace.nbytes,
-        torch._C._cuda_getCurrentRawStream(q.device.index) if stream is None else _stream(stream),
+        torch._C._cuda_getCurrentRawStream(q.get_device()) if stream is None else _stream(stream),
         None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
     if st != KPOOL_OK:
         raise KpoolError(st, name)
