@@ -193,6 +193,41 @@ def test_runs_of_many_segments(ql, kl, heads):
     assert torch.equal(out, again) and torch.equal(lse, alse)
 
 
+@pytest.mark.parametrize("lens", [[1] * 9000, [1] * 8900 + [60, 0, 200]], ids=["ones", "mixed"])
+def test_more_sequences_than_the_runs_take(lens):
+    heads = (2, 1, 64)
+    (q, k, v, scale), out, lse = run_prompt(lens, lens, heads, BF, "auto", seed=91)
+    pick = sorted(set(range(0, sum(lens), 97)) | set(range(max(0, sum(lens) - 40), sum(lens))))
+    see = A.see_prompt(lens, lens)
+    A.check(out[pick], lse[pick], A.reference(q[pick], k, v, [see[r] for r in pick], scale))
+
+
+@pytest.mark.parametrize("family", FAMILIES)
+def test_offsets_past_32_bits(family):
+    """The last tokens of a cache of more than 2^32 bytes; what lies before them is not set."""
+    tokens, heads = 2_300_000, (16, 8, 128)
+    k = torch.empty((tokens, 8, 128), dtype=BF, device="cuda")
+    v = torch.empty((tokens, 8, 128), dtype=BF, device="cuda")
+    assert k.numel() * 2 > 2 ** 32
+    n = 500
+    q, k[-n:], v[-n:] = make(92, 6, n, heads, BF)
+    lens = [tokens - n, n]
+    nodes, prefixes, scale = [0, 6], [0, n - 6], 0.1
+    kw = dict(return_lse=True, score_kernel=FAMILIES[family])
+    cu = i32(A.cu(lens))
+    out, lse = K.kpool_attention_tree(q, k, v, i32(A.cu(nodes)), cu, i32(prefixes), scale, **kw)
+    ref = A.reference(q, k[-n:], v[-n:], A.see_tree([6], [n], [n - 6], None), scale)
+    A.check(out, lse, ref, "tree")
+    out, lse = K.kpool_attention_prompt(q, k, v, i32(A.cu(nodes)), cu, scale, **kw)
+    A.check(out, lse, ref, "prompt")
+    ids = torch.randint(0, n, (6, 70), generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    out, lse = K.kpool_attention_selected(q, k, v, ids.cuda(), cu, scale, row_seq=i32([1] * 6), **kw)
+    A.check(out, lse, A.reference(q, k[-n:], v[-n:], A.see_selected(ids, [0] * 6, [n]), scale), "selected")
+    one = i32([0, tokens])     # and as ids of one long sequence
+    out, lse = K.kpool_attention_selected(q, k, v, (ids + (tokens - n)).cuda(), one, scale, row_seq=i32([0] * 6), **kw)
+    A.check(out, lse, A.reference(q, k[-n:], v[-n:], A.see_selected(ids, [0] * 6, [n]), scale), "long ids")
+
+
 SELECT_HEADS = HEADS + [(32, 8, 128, BF), (64, 1, 128, BF), (20, 1, 64, BF), (24, 2, 128, BF)]
 
 
