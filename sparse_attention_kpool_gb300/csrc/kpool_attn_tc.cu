@@ -159,8 +159,13 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
     }
     const uint64_t y = uint64_t(a) * n + b;
     if (y < m) break;
-    n = uint32_t(y / m);
-    b = uint32_t(y % m);
+    if (y >> 32) {
+      n = uint32_t(y / m);
+      b = uint32_t(y % m);
+    } else {
+      n = uint32_t(y) / m;
+      b = uint32_t(y) % m;
+    }
     const uint32_t x = m;
     m = a;
     a = x;
@@ -314,6 +319,15 @@ __host__ __device__ __forceinline__ int64_t run_count(int64_t total, int64_t cta
   return n < 1 ? 1 : n;
 }
 
+// The positions of the runs: run r of n begins at floor(total r / n), without a 64-bit division per run.
+struct Cuts {
+  int64_t each;        // total / n
+  uint32_t rest, n;    // total % n
+  __device__ __forceinline__ Cuts(int64_t total, uint32_t runs)
+      : each(total / runs), rest(uint32_t(total - each * runs)), n(runs) {}
+  __device__ __forceinline__ int64_t lo(uint32_t r) const { return each * r + rest * r / n; }  // rest * r < n * n
+};
+
 // Every thread of the CTA: this CTA's run of positions [total * i / n, total * (i + 1) / n)
 // and the sequence it starts in. `scratch` holds S 64-bit words of shared memory.
 __device__ __forceinline__ void find_run(const AttnParams& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas,
@@ -326,7 +340,9 @@ __device__ __forceinline__ void find_run(const AttnParams& p, int ttb, int64_t* 
     for (int b = lane; b < p.S; b += 32) sum += scratch[b];
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const int64_t n = run_count(sum, ctas), lo = i < n ? sum * i / n : sum, hi = i < n ? sum * (i + 1) / n : sum;
+    const int64_t n = run_count(sum, ctas);
+    const Cuts cuts(sum, uint32_t(n));
+    const int64_t lo = i < n ? cuts.lo(uint32_t(i)) : sum, hi = i < n ? cuts.lo(uint32_t(i) + 1) : sum;
     int64_t run = 0;
     bool found = false;
     for (int b0 = 0; b0 < p.S && !found; b0 += 32) {
@@ -357,12 +373,14 @@ __device__ __forceinline__ void find_run(const AttnParams& p, int ttb, int64_t* 
 
 // What the join of the rows that the border before run r cuts needs; runs = 0: nothing to join here.
 struct JoinItem {
-  int64_t item, total;   // position of the first tile of the rows' item, positions of the call
+  int64_t item;          // position of the first tile of the rows' item
+  int64_t each;          // Cuts of the call
+  uint32_t rest;
   int32_t tiles;         // K/V tiles of the item
   int32_t runs;
   int32_t q0, nq;        // query rows of the sequence
   int32_t tok0, hk;
-  int32_t pad[6];
+  int32_t pad[5];
 };
 static_assert(sizeof(JoinItem) == kAttnJoinBytes, "join items are laid out in the workspace");
 
@@ -373,9 +391,11 @@ __device__ __forceinline__ void write_join(JoinItem* out, const Seg& s, int64_t 
   JoinItem j{};
   j.item = tile0;
   bool own = s.kt0 > 0;
-  const int64_t pos = total * r / n;
-  for (int b = r - 1; own && b > 0 && total * b / n > tile0; --b) own = total * b / n == pos;
-  j.total = total;
+  const Cuts cuts(total, n);
+  const int64_t pos = cuts.lo(r);
+  for (int b = r - 1; own && b > 0 && cuts.lo(b) > tile0; --b) own = cuts.lo(b) == pos;
+  j.each = cuts.each;
+  j.rest = cuts.rest;
   j.tiles = c;
   j.runs = own ? n : 0;
   j.q0 = s.sq.q0;
@@ -536,8 +556,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   if (GATHER) {
     // (listed rows, mostly none: whole items, so that there is nothing to join)
     const int64_t total = gather_total(p), unit = p.list ? gather_tiles(p) : 1;
-    const int64_t lo = total / unit * blockIdx.x / gridDim.x * unit;
-    const int64_t hi = total / unit * (blockIdx.x + 1) / gridDim.x * unit;
+    const Cuts cuts(total / unit, gridDim.x);
+    const int64_t lo = cuts.lo(blockIdx.x) * unit, hi = cuts.lo(blockIdx.x + 1) * unit;
     if (p.list && lo == hi) return;
     if (threadIdx.x == 0) {
       misc->lo = lo;
@@ -1245,7 +1265,7 @@ __global__ void __launch_bounds__(256)
   if (it.runs == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the runs that hold tiles of the item: from `first` while they begin before its end
-  auto run_lo = [&](int64_t r) { return it.total * r / it.runs; };
+  auto run_lo = [&](int r) { return it.each * r + it.rest * uint32_t(r) / uint32_t(it.runs); };
   int first = blockIdx.x;
   while (first > 0 && run_lo(first) > it.item) --first;
   const float c2 = p.scale * kLog2e;
@@ -1263,14 +1283,15 @@ __global__ void __launch_bounds__(256)
   }
   if (!any) return;
   const int64_t end = it.item + it.tiles;
-  for (int64_t r0 = first + (kSplit ? warp : 0); r0 < it.runs && run_lo(r0) < end;
+  for (int r0 = first + (kSplit ? warp : 0); r0 < it.runs && run_lo(r0) < end;
        r0 += kJoinBatch * (kSplit ? 8 : 1)) {
     float o[kJoinBatch][kRows][kPer];
     float2 ml[kJoinBatch][kRows];
     bool has[kJoinBatch];
 #pragma unroll
     for (int b = 0; b < kJoinBatch; ++b) {
-      const int64_t r = r0 + b * (kSplit ? 8 : 1), lo = run_lo(r), hi = run_lo(r + 1);
+      const int r = r0 + b * (kSplit ? 8 : 1);
+      const int64_t lo = run_lo(r), hi = run_lo(r + 1);
       has[b] = r < it.runs && lo < end && hi > it.item && hi > lo;
       if (!has[b]) continue;
       const float* s = part + (size_t(r) * 2 + (lo > it.item ? 0 : 1)) * stride;
