@@ -28,7 +28,7 @@
 // the next Q K^T (1200), handing S over (400), is 3250, and with two groups in flight that is
 // the time of a pair. 32,768 tokens of 32 / 8 heads of 128: 5.95 ms = 1.48 PFLOP/s, 86 % of
 // the measured sustained rate of a large product. Decode is bound by HBM: 792 MB of caches in
-// 139 us = 5.7 TB/s, 84 % of the measured copy rate. Short sequences pay 4 to 6 us of start,
+// 135 us = 5.9 TB/s, 87 % of the measured copy rate. Short sequences pay 4 to 6 us of start,
 // masks and epilogue per row tile.
 //
 // Running maximum. O is rescaled only when a row's maximum has grown by more than 8 in the
@@ -1228,10 +1228,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 //
 // CTA x adds up, in the order of the runs, the partial results of the rows that the border
 // before run x + 1 cuts (if that run was the first to begin inside them: its producer left the
-// item's data). A warp takes four rows, a lane D / 32 channels. kSplit: the 8 warps of a CTA share
-// four rows and each takes every eighth run (few items, each cut into many runs); else they take
-// 32 rows, most of them cut into two or three runs. What is read is a few MB just written; with kSplit
-// four runs are read at a time, since the latency of one read after the other made 100 us of 154 runs.
+// item's data). A lane holds D / 32 channels of a row. kSplit: the 8 warps of a CTA share four
+// rows and each takes every eighth run, four at a time (few items, each cut into many runs: reading
+// one run after the other made 100 us of 154); else a warp has two rows, most of them cut into
+// two or three runs, and reads two at a time. What is read is a few MB just written; the join adds
+// 9 to 18 us to a call of 100 us and more. (Four rows a warp, one run at a time: 138 against 135 us
+// for 16 decode tokens over caches of up to 32,767 keys, prompts alike.)
 
 template <int D>
 struct JoinRow {
@@ -1259,7 +1261,7 @@ template <int D, bool kSplit>
 __global__ void __launch_bounds__(256)
     attn_join_kernel(const __grid_constant__ AttnParams p, int tt, const JoinItem* joins, const float* part,
                      int slot_rows) {
-  constexpr int kPer = D / 32, kRows = 4, kJoinBatch = kSplit ? 4 : 1;
+  constexpr int kPer = D / 32, kRows = kSplit ? 4 : 2, kJoinBatch = kSplit ? 4 : 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
   const JoinItem it = joins[blockIdx.x + 1];
   if (it.runs == 0) return;
@@ -1420,7 +1422,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   // many runs to an item: a CTA's warps share its rows; else each has its own
   const bool split = items * (slot_rows <= 64 ? 4 : 16) <= grid;
-  const int join_rows = split ? 4 : 32;
+  const int join_rows = split ? 4 : 16;
   cfg.gridDim = dim3(uint32_t(grid - 1), uint32_t((slot_rows + join_rows - 1) / join_rows));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
