@@ -404,6 +404,8 @@ kpool_status kpool_attention_tree(const kpool_heads* q, const kpool_heads* k, co
  *   row_seq    [q_rows] int32 (device): the row's sequence, as for kpool_select_rows; or
  *              NULL when the query rows are the key tokens' own (q_rows = k_tokens,
  *              as for kpool_select): row r is then of the sequence that holds token r.
+ *   options    NULL picks a kernel by the sizes (short lists a warp each, a prompt's rows
+ *              together, else gathered); KPOOL_SCORE_TC keeps to the tcgen05 kernels
  */
 kpool_status kpool_attention_selected(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
                                       const int32_t* token_ids, int32_t width, const int32_t* row_seq,

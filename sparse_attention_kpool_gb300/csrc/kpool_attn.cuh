@@ -205,7 +205,10 @@ inline size_t attn_mask_bytes(int64_t R) {
   return size_t(all < (int64_t(128) << 20) ? all : (int64_t(128) << 20));
 }
 inline size_t attn_list_bytes(int64_t R) { return (size_t(R) * 4 + 255) & ~size_t(255); }
-bool attn_dense_wanted(const AttnParams& p, int sms);
+struct AttnSelectedTimes {  // microseconds, estimated; dense is infinite where it cannot be had
+  double gathered, dense;
+};
+AttnSelectedTimes attn_selected_times(const AttnParams& p, int sms);
 cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t* mask, int32_t* list,
                                    cudaStream_t stream);
 
@@ -214,6 +217,11 @@ cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
 bool attn_gather_supported(const AttnParams& p);
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
+
+// Selected tokens by one warp an item, in registers: what attn_tc_supported takes, any strides. Wanted where it
+// beats the other two ways.
+bool attn_warp_wanted(const AttnParams& p, int sms);
+cudaError_t launch_attn_warp(const AttnParams& p, int sms, char* ws, cudaStream_t stream);
 
 // CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);

@@ -84,6 +84,11 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
   p.scale = shape->scale;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (tc_ok && k_tokens > 0 && p.mode == kAttnSelected && opt.score_kernel == KPOOL_SCORE_AUTO) {
+    int sms = 0;
+    if (!note_cuda_error(device_sm_count(&sms))) return KPOOL_ERR_CUDA;
+    if (attn_warp_wanted(p, sms)) return note_cuda_error(launch_attn_warp(p, sms, ws, stream)) ? KPOOL_OK : KPOOL_ERR_CUDA;
+  }
   const bool tc = tc_ok && k_tokens > 0 && opt.score_kernel != KPOOL_SCORE_SIMT &&
                   (p.mode != kAttnSelected || attn_gather_supported(p));
   const cudaError_t e = tc ? launch_attn_tc(p, ws, stream) : launch_attn_simt(p, dtype, ws, stream);

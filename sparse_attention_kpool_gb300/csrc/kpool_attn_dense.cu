@@ -3,7 +3,7 @@
 // Gathering costs every row its own copy of its keys out of L2. Rows of a prompt share most
 // of theirs: a tile of 64 rows reads each key once for all of them when it goes over all keys of its
 // sequence and masks what a row did not select. That does (keys / selected) times the
-// products and still wins while a sequence is not too long (attn_dense_wanted). The ids
+// products and still wins while a sequence is not too long (attn_selected_times). The ids
 // become bits, 32 keys a word, and the prompt kernel runs with them as its mask.
 //
 // A bit cannot say that a row names a key twice: such rows are listed and the gathering kernel
@@ -13,6 +13,7 @@
 //   mask (a CTA per row)  bits in shared memory, then out; a listed row, a later key or an infinity or NaN
 //                         among the token's values is noted (with none the dense kernel cleans no V tile)
 #include <cuda_runtime.h>
+#include <math.h>
 
 #include "kpool_attn.cuh"
 
@@ -109,19 +110,21 @@ __global__ void __launch_bounds__(256) dense_mask_kernel(const __grid_constant__
 
 }  // namespace
 
-bool attn_dense_wanted(const AttnParams& p, int sms) {
-  if (p.row_seq != nullptr || p.width == 0 || p.S > kAttnMaxRunSeqs) return false;
-  const int64_t keys = p.T / p.S;  // of a sequence, on average: a row goes over half of them
-  if (int64_t(p.R) * ((keys + 127) / 128) * 16 > int64_t(attn_mask_bytes(p.R))) return false;
-  // Microseconds of either way, from their measured parts: a gathered (row, key head) takes 3 and 1.25 for each
-  // tile of 128 ids; a dense item (256 / G rows) 6 and 2 for each tile of its keys, the kernels around it 25.
+AttnSelectedTimes attn_selected_times(const AttnParams& p, int sms) {
+  // From the measured parts of either way: a gathered (row, key head) takes 3 and 1.25 for each
+  // tile of 128 ids (few of them are cut into runs); a dense item (256 / G rows) 6 and 2 for each tile of its
+  // keys, the kernels around it 25.
   // Measured dense / gathered: 32 / 8 heads of 128, 3,000 rows x 24 ids 114 / 684, 1,500 x 516 56 / 742,
   // 16,000 x 512 1,676 / 6,407, 100 x 32 17 / 31; 64 / 1 heads, 600 x 1,004 25 / 63, 2,000 x 128 110 / 63,
   // 3,000 x 68 182 / 89.
-  const double items = double(p.R) * p.Hkv / sms;
-  const double gathered = 6.0 + items * (3.0 + 1.25 * ((p.width + 127) / 128));
-  const double dense = 25.0 + items * p.G / 256.0 * (6.0 + 2.0 * double(keys) / 256.0);
-  return dense < gathered;
+  const double items = double(p.R) * p.Hkv / sms, tiles = double((p.width + 127) / 128);
+  const double all = items * (3.0 + 1.25 * tiles), cut = 1.2 * tiles < 8.0 ? 1.2 * tiles : 8.0;
+  AttnSelectedTimes t{6.0 + (all > cut ? all : cut), INFINITY};
+  if (p.row_seq != nullptr || p.width == 0 || p.S > kAttnMaxRunSeqs) return t;
+  const int64_t keys = p.T / p.S;  // of a sequence, on average: a row goes over half of them
+  if (int64_t(p.R) * ((keys + 127) / 128) * 16 > int64_t(attn_mask_bytes(p.R))) return t;
+  t.dense = 25.0 + items * p.G / 256.0 * (6.0 + 2.0 * double(keys) / 256.0);
+  return t;
 }
 
 cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t* mask, int32_t* list,

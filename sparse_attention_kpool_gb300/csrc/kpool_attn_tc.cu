@@ -1453,7 +1453,8 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
     int sms = 0;
     const cudaError_t q = device_sm_count(&sms);
     if (q != cudaSuccess) return q;
-    if (attn_dense_wanted(p, sms)) {
+    const AttnSelectedTimes times = attn_selected_times(p, sms);
+    if (times.dense < times.gathered) {
       AttnDense* ctl = reinterpret_cast<AttnDense*>(ws + sizeof(WorkspaceHeader));
       char* at = ws + sizeof(WorkspaceHeader) + ((attn_partial_bytes(p.R, p.G, p.D) + 255) & ~size_t(255));
       int32_t* list = reinterpret_cast<int32_t*>(at);
