@@ -28,7 +28,7 @@
 // the next Q K^T (1200), handing S over (400), is 3250, and with two groups in flight that is
 // the time of a pair. 32,768 tokens of 32 / 8 heads of 128: 5.95 ms = 1.48 PFLOP/s, 86 % of
 // the measured sustained rate of a large product. Decode is bound by HBM: 792 MB of caches in
-// 135 us = 5.9 TB/s, 87 % of the measured copy rate. Short sequences pay 4 to 6 us of start,
+// 136 us = 5.8 TB/s, 86 % of the measured copy rate. Short sequences pay 4 to 6 us of start,
 // masks and epilogue per row tile.
 //
 // Running maximum. O is rescaled only when a row's maximum has grown by more than 8 in the
@@ -1232,7 +1232,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 // rows and each takes every eighth run, four at a time (few items, each cut into many runs: reading
 // one run after the other made 100 us of 154); else a warp has two rows, most of them cut into
 // two or three runs, and reads two at a time. What is read is a few MB just written; the join adds
-// 9 to 18 us to a call of 100 us and more. (Four rows a warp, one run at a time: 138 against 135 us
+// 9 to 18 us to a call of 100 us and more. (Four rows a warp, one run at a time: 138 against 136 us
 // for 16 decode tokens over caches of up to 32,767 keys, prompts alike.)
 
 template <int D>
