@@ -186,16 +186,20 @@ constexpr int kAttnLikeKeys = 2600;
 constexpr int kAttnDirectItems = 6;
 constexpr int kAttnDirectKeys = 8192;
 constexpr int kAttnJoinBytes = 64;   // per run: what the join of the rows before it needs
-// Rows of one partial result.
-inline int attn_slot_rows(int64_t R, int32_t G, int tile_rows) {
-  const int64_t rows = (R * G + 3) & ~int64_t(3);  // keeps every partial result 16-byte aligned
-  return int(rows < tile_rows ? rows : tile_rows);
+constexpr int kAttnTileRows = 128;   // MMA rows: row tile t's tokens fill the first 128 / G * G rows from 128 t on
+// Rows of one partial result of a call of R query rows: up to the last row that the form's row tiles (one or two) give
+// a token, so with two of them the gap that a G which does not divide 128 leaves before row 128 is counted.
+inline int attn_slot_rows(int64_t R, int32_t G, int row_tiles) {
+  const int64_t tt = kAttnTileRows / G;
+  int64_t rows = (R < tt ? R : tt) * G;
+  if (row_tiles == 2 && R > tt) rows = kAttnTileRows + (R < 2 * tt ? R - tt : tt) * G;
+  return int((rows + 3) & ~int64_t(3));  // keeps every partial result 16-byte aligned
 }
 // AttnDense, the runs' join items and the partial results of the persistent form: two per run,
 // [rows][D] fp32 and (m, l) per row.
 inline size_t attn_partial_bytes(int64_t R, int32_t G, int32_t D) {
   return 256 + size_t(kAttnMaxRuns) * kAttnJoinBytes +
-         size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 256)) * size_t(D + 2) * sizeof(float);
+         size_t(2 * kAttnMaxRuns) * size_t(attn_slot_rows(R, G, 2)) * size_t(D + 2) * sizeof(float);
 }
 
 // The dense form of a selection: whether the host tries it, the bytes of its mask for R rows, and the

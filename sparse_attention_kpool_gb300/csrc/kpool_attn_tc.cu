@@ -62,7 +62,7 @@ namespace kpool {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kTileRows = 128;
+constexpr int kTileRows = kAttnTileRows;
 constexpr int kPCol = 64;      // a tile's weights, bf16 in 64 columns, replace the upper half of its scores
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -1401,7 +1401,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
   if (GATHER && !small && !p.list) grid = int(run_count(items * nt, grid));
-  const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles * kTileRows);
+  const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles);
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
