@@ -73,6 +73,16 @@ __global__ void wait_selftest_kernel(WorkspaceHeader* hdr, int64_t spin_limit) {
 bool note_cuda_error(cudaError_t e) { return cuda_ok(e); }
 cudaError_t device_sm_count(int* out) { return sm_count(out); }
 
+cudaError_t allow_dynamic_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && ((done->load(std::memory_order_relaxed) >> dev) & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess && dev < kMaxDevices) done->fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
+
 cudaError_t launch_wait_selftest(char* ws, int64_t spin_limit, cudaStream_t stream) {
   wait_selftest_kernel<<<1, 32, 0, stream>>>(reinterpret_cast<WorkspaceHeader*>(ws), spin_limit);
   return cudaGetLastError();

@@ -133,11 +133,10 @@ cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t
   dense_init_kernel<<<1, 256, 0, stream>>>(p, ctl, capacity);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a mask that fits has at most capacity / R bytes a row
+  // A mask that fits has at most capacity / R bytes a row; its rows are the T = R key tokens' own, so that is
+  // at most 4 KB (2^27 bytes at 32,768 rows), which needs no higher limit.
   const int64_t row_bytes = capacity / p.R < (p.T + 127) / 128 * 16 ? capacity / p.R : (p.T + 127) / 128 * 16;
   const int smem = int(row_bytes & ~int64_t(15));
-  e = cudaFuncSetAttribute(dense_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   dense_mask_kernel<<<uint32_t(p.R), 256, smem, stream>>>(p, ctl, mask, list);
   return cudaGetLastError();
 }

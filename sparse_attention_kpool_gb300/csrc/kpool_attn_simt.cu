@@ -285,6 +285,18 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   if (checks && threadIdx.x < 32) attn_check(p, hdr);
 }
 
+template <typename E, int kGroups>
+cudaError_t launch(const AttnParams& p, const dim3& grid, int gt, int tt, WorkspaceHeader* hdr, cudaStream_t stream) {
+  auto bytes = [](int D) { return sizeof(float) * (size_t(kVRows) * D + size_t(kGroups) * group_floats(D)); };
+  auto kernel = attn_simt_kernel<E, kGroups>;
+  static std::atomic<uint64_t> ready{0};
+  const size_t most = bytes(kGroups == 4 ? 128 : 256);
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), most, &ready);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kGroupThreads * kGroups, bytes(p.D), stream>>>(p, gt, tt, hdr);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
@@ -292,19 +304,12 @@ cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, c
   const int gt = p.G < kVRows ? p.G : kVRows;
   const int tt = p.mode == kAttnSelected ? 1 : kVRows / gt;
   const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles(p.R, p.S, tt);
-  const int groups = p.D <= 128 ? 4 : 2;
-  const size_t smem = sizeof(float) * (size_t(kVRows) * p.D + size_t(groups) * group_floats(p.D));
   const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
-  auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kGroupThreads * groups, smem, stream>>>(p, gt, tt, hdr);
-    return cudaGetLastError();
-  };
   if (dtype == KPOOL_BF16)
-    return groups == 4 ? go(attn_simt_kernel<__nv_bfloat16, 4>) : go(attn_simt_kernel<__nv_bfloat16, 2>);
-  return groups == 4 ? go(attn_simt_kernel<float, 4>) : go(attn_simt_kernel<float, 2>);
+    return p.D <= 128 ? launch<__nv_bfloat16, 4>(p, grid, gt, tt, hdr, stream)
+                      : launch<__nv_bfloat16, 2>(p, grid, gt, tt, hdr, stream);
+  return p.D <= 128 ? launch<float, 4>(p, grid, gt, tt, hdr, stream) : launch<float, 2>(p, grid, gt, tt, hdr, stream);
 }
 
 }  // namespace kpool

@@ -52,7 +52,6 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include <atomic>
 #include <utility>
 
 #include "kpool_attn.cuh"
@@ -1406,15 +1405,9 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   auto kernel = attn_tc_kernel<D, F>;
-  static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory limit is set
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), C::kSmem, &ready);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
-  }
   kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
                                                   joins, hdr);
   e = cudaGetLastError();

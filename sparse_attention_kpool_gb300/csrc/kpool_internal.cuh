@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kpool.h"
 
 namespace kpool {
@@ -200,6 +202,12 @@ bool note_cuda_error(cudaError_t e);
 
 // SM count of the current device (looked up once per device).
 cudaError_t device_sm_count(int* out);
+
+// Lets `kernel` be launched with up to `bytes` of dynamic shared memory on the current device. The limit belongs
+// to the kernel, not to a launch or a thread: every call site names the largest size that the kernel is ever
+// launched with, so that no thread lowers it between another's call of this function and its launch. `done` is
+// the kernel's own record of the devices where the limit is set.
+cudaError_t allow_dynamic_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
 
 // Bounded-wait self test.
 cudaError_t launch_wait_selftest(char* ws, int64_t spin_limit, cudaStream_t stream);

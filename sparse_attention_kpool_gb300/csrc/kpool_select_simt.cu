@@ -147,10 +147,10 @@ cudaError_t launch_typed(const void* q, const void* kp, const float* w, const in
   if (warps < 1) warps = 1;
   const size_t smem = per_warp * warps;
   auto kern = select_simt_kernel<Elem, kNeg>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const size_t most = size_t(simt_capacity(4096)) * sizeof(uint64_t);  // a warp's at the largest budget taken
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), most, &ready);
+  if (e != cudaSuccess) return e;
   int64_t blocks = (row_end - row_begin + warps - 1) / warps;
   const int64_t cap_blocks = int64_t(num_sms) * 16;
   if (blocks > cap_blocks) blocks = cap_blocks;
