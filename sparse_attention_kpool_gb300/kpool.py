@@ -4,7 +4,9 @@ Argument marshalling only: every step of the selection runs in the library's
 kernels. Functions carry the C names. Tensors must be CUDA tensors on the
 current device; outputs and workspace are allocated with torch when the caller
 does not pass them (the library itself never allocates). Calls run on torch's
-current CUDA stream unless `stream` is given.
+current CUDA stream unless `stream` is given; what they allocate then is memory
+of that stream, and ordering them with the work that makes the inputs and uses
+the outputs is the caller's.
 
 There is no fallback: if the library is not built, or a call fails, these
 functions raise.
@@ -175,6 +177,37 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _torch_stream(stream):
+    """A stream argument (a torch stream or a handle) as a torch stream."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+
+
+def _new(make, stream, returned=True):
+    """A tensor that a call on `stream` (None: the current one) makes for itself: make() allocates it.
+
+    The allocator hands memory out again in the order of the stream it was allocated on. Memory of the current
+    stream that a call uses on another one would be neither free when the call's kernels begin nor
+    theirs until they end, so it comes from the call's own stream. What is `returned` to a caller
+    is marked as used on the caller's current stream, too."""
+    if stream is None:
+        return make()
+    here, there = torch.cuda.current_stream(), _torch_stream(stream)
+    if here == there:
+        return make()
+    with torch.cuda.stream(there):
+        t = make()
+    if returned:
+        t.record_stream(here)
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    return _new(lambda: torch.empty(shape, dtype=dtype, device=device), stream)
+
+
 def _check_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -213,13 +246,13 @@ def kpool_select_ex(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, cu_seqlen
     R = T if row_range is None else max(0, int(row_range[1]) - int(row_range[0]))
     dev = q.device
     if out_pool_ids is None:
-        out_pool_ids = torch.empty((R, B), dtype=torch.int32, device=dev)
+        out_pool_ids = _empty((R, B), torch.int32, dev, stream)
     if out_token_ids is None:
-        out_token_ids = torch.empty((R, index_topk + kpool), dtype=torch.int32, device=dev)
+        out_token_ids = _empty((R, index_topk + kpool), torch.int32, dev, stream)
     if out_pool_scores is None and return_scores:
-        out_pool_scores = torch.empty((R, B), dtype=torch.float32, device=dev)
+        out_pool_scores = _empty((R, B), torch.float32, dev, stream)
     if workspace is None:
-        workspace = new_workspace(T, S, H, d, dt, kpool, index_topk, dev)
+        workspace = _new(lambda: new_workspace(T, S, H, d, dt, kpool, index_topk, dev), stream, returned=False)
     _check_cuda(q, k, w, cu_seqlens, out_pool_ids, out_token_ids, out_pool_scores, workspace)
     opts, _arr = _options(score_kernel, max_ctas, row_range, stage_events)
     st = load().kpool_select_ex(_ptr(q), _ptr(k), _ptr(w), _ptr(cu_seqlens), S, T, H, d, dt, kpool, index_topk,
@@ -243,9 +276,9 @@ def kpool_pool_keys(k: torch.Tensor, cu_seqlens: torch.Tensor, kpool: int, out=N
     S = cu_seqlens.numel() - 1
     dt = _dtype_code(k)
     if out is None:
-        out = torch.empty((max(T // kpool, 0), d), dtype=k.dtype, device=k.device)
+        out = _empty((max(T // kpool, 0), d), k.dtype, k.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, S, 1, d, dt, kpool, 0, k.device)
+        workspace = _new(lambda: new_workspace(T, S, 1, d, dt, kpool, 0, k.device), stream, returned=False)
     _check_cuda(k, cu_seqlens, out, workspace)
     st = load().kpool_pool_keys(_ptr(k), _ptr(cu_seqlens), S, T, d, dt, kpool, _ptr(out), _ptr(workspace),
                                 workspace.numel(), _stream(stream))
@@ -259,7 +292,7 @@ def kpool_expand(pool_ids: torch.Tensor, cu_seqlens: torch.Tensor, kpool: int, i
     T = pool_ids.shape[0]
     S = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, index_topk + kpool), dtype=torch.int32, device=pool_ids.device)
+        out = _empty((T, index_topk + kpool), torch.int32, pool_ids.device, stream)
     _check_cuda(pool_ids, cu_seqlens, out)
     st = load().kpool_expand(_ptr(pool_ids), _ptr(cu_seqlens), S, T, kpool, index_topk, _ptr(out), _stream(stream))
     if st != KPOOL_OK:
@@ -288,11 +321,11 @@ def kpool_select_static_scratch(q: torch.Tensor, k: torch.Tensor, w: torch.Tenso
     B = index_topk // kpool if kpool > 0 else 0
     dev = q.device
     if out_pool_ids is None:
-        out_pool_ids = torch.empty((T, B), dtype=torch.int32, device=dev)
+        out_pool_ids = _empty((T, B), torch.int32, dev, stream)
     if out_token_ids is None:
-        out_token_ids = torch.empty((T, index_topk + kpool), dtype=torch.int32, device=dev)
+        out_token_ids = _empty((T, index_topk + kpool), torch.int32, dev, stream)
     if out_pool_scores is None and return_scores:
-        out_pool_scores = torch.empty((T, B), dtype=torch.float32, device=dev)
+        out_pool_scores = _empty((T, B), torch.float32, dev, stream)
     _check_cuda(q, k, w, cu_seqlens, out_pool_ids, out_token_ids, out_pool_scores)
     st = load().kpool_select_static_scratch(_ptr(q), _ptr(k), _ptr(w), _ptr(cu_seqlens), S, T, H, d, dt, kpool,
                                             index_topk, float(scale), _ptr(out_pool_ids), _ptr(out_token_ids),
@@ -341,13 +374,13 @@ def kpool_select_rows(q: torch.Tensor, w: torch.Tensor, row_seq: torch.Tensor, r
     B = index_topk // kpool if kpool > 0 else 0
     dev = q.device
     if out_pool_ids is None:
-        out_pool_ids = torch.empty((R, B), dtype=torch.int32, device=dev)
+        out_pool_ids = _empty((R, B), torch.int32, dev, stream)
     if out_token_ids is None:
-        out_token_ids = torch.empty((R, index_topk + kpool), dtype=torch.int32, device=dev)
+        out_token_ids = _empty((R, index_topk + kpool), torch.int32, dev, stream)
     if out_pool_scores is None and return_scores:
-        out_pool_scores = torch.empty((R, B), dtype=torch.float32, device=dev)
+        out_pool_scores = _empty((R, B), torch.float32, dev, stream)
     if workspace is None:
-        workspace = new_rows_workspace(R, total_tokens, S, kpool, index_topk, dev)
+        workspace = _new(lambda: new_rows_workspace(R, total_tokens, S, kpool, index_topk, dev), stream, returned=False)
     _check_cuda(q, w, row_seq, row_pos, pooled_keys, cu_seqlens, out_pool_ids, out_token_ids, out_pool_scores,
                 workspace)
     opts = kpool_options(KPOOL_SCORE_AUTO, max_ctas)
@@ -378,9 +411,9 @@ def kpool_pool_keys_gated(k: torch.Tensor, gate: torch.Tensor, ape: torch.Tensor
             or tuple(ape.shape) != (kpool, d):
         raise TypeError("gate must be float32 [T, d] and ape float32 [kpool, d]")
     if out is None:
-        out = torch.empty((max(T // kpool, 0), d), dtype=k.dtype, device=k.device)
+        out = _empty((max(T // kpool, 0), d), k.dtype, k.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, S, 1, d, dt, kpool, 0, k.device)
+        workspace = _new(lambda: new_workspace(T, S, 1, d, dt, kpool, 0, k.device), stream, returned=False)
     _check_cuda(k, gate, ape, cu_seqlens, out, workspace)
     st = load().kpool_pool_keys_gated(_ptr(k), _ptr(gate), _ptr(ape), _ptr(cu_seqlens), S, T, d, dt, kpool, _ptr(out),
                                       _ptr(workspace), workspace.numel(), _stream(stream))
@@ -404,13 +437,13 @@ def kpool_select_pooled(q: torch.Tensor, pooled_keys: torch.Tensor, w: torch.Ten
     R = T if row_range is None else max(0, int(row_range[1]) - int(row_range[0]))
     dev = q.device
     if out_pool_ids is None:
-        out_pool_ids = torch.empty((R, B), dtype=torch.int32, device=dev)
+        out_pool_ids = _empty((R, B), torch.int32, dev, stream)
     if out_token_ids is None:
-        out_token_ids = torch.empty((R, index_topk + kpool), dtype=torch.int32, device=dev)
+        out_token_ids = _empty((R, index_topk + kpool), torch.int32, dev, stream)
     if out_pool_scores is None and return_scores:
-        out_pool_scores = torch.empty((R, B), dtype=torch.float32, device=dev)
+        out_pool_scores = _empty((R, B), torch.float32, dev, stream)
     if workspace is None:
-        workspace = new_workspace(T, S, H, d, dt, kpool, index_topk, dev)
+        workspace = _new(lambda: new_workspace(T, S, H, d, dt, kpool, index_topk, dev), stream, returned=False)
     _check_cuda(q, pooled_keys, w, cu_seqlens, out_pool_ids, out_token_ids, out_pool_scores, workspace)
     opts = kpool_options(score_kernel, max_ctas)
     if row_range is not None:
@@ -460,11 +493,11 @@ def kpool_index_scores(q: torch.Tensor, k: torch.Tensor, w: torch.Tensor, cu_seq
     R = T if row_range is None else max(0, int(row_range[1]) - int(row_range[0]))
     dev = q.device
     if out is None:
-        out = torch.empty((R, ld), dtype=torch.float32, device=dev)
+        out = _empty((R, ld), torch.float32, dev, stream)
     elif out.dtype != torch.float32 or out.numel() < R * ld or not out.is_contiguous():
         raise TypeError("out must be a contiguous float32 tensor of at least R * ld elements")
     if workspace is None:
-        workspace = new_workspace(T, S, H, d, dt, kpool, 0, dev)
+        workspace = _new(lambda: new_workspace(T, S, H, d, dt, kpool, 0, dev), stream, returned=False)
     _check_cuda(q, k, w, cu_seqlens, out, workspace)
     opts, _arr = _options(score_kernel, max_ctas, row_range, stage_events)
     fn = load().kpool_index_scores_pooled if pooled else load().kpool_index_scores
@@ -525,16 +558,17 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     R, hq, d = qs
     T, hkv, _ = ks
     if out is None:
-        out = torch.empty((R, hq, d), dtype=dtype, device=q.device)
+        out = _empty((R, hq, d), dtype, q.device, stream)
     elif out.shape != qs or out.dtype != dtype:
         raise TypeError("out must have q's shape and dtype")
     if out_lse is None:
         if return_lse:
-            out_lse = torch.empty((R, hq), dtype=torch.float32, device=q.device)
+            out_lse = _empty((R, hq), torch.float32, q.device, stream)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (R, hq):
         raise TypeError("out_lse must be float32 [rows, q_heads]")
     if workspace is None:
-        workspace = new_attention_workspace(R, num_seqs, hq, hkv, d, dtype, q.device)
+        workspace = _new(lambda: new_attention_workspace(R, num_seqs, hq, hkv, d, dtype, q.device), stream,
+                         returned=False)
     if not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and workspace.is_cuda):
         raise ValueError("tensors must be CUDA tensors")
     qt, qh, qd = q.stride()
