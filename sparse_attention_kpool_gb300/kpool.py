@@ -569,8 +569,11 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     if workspace is None:
         workspace = _new(lambda: new_attention_workspace(R, num_seqs, hq, hkv, d, dtype, q.device), stream,
                          returned=False)
-    if not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and workspace.is_cuda):
-        raise ValueError("tensors must be CUDA tensors")
+    # (-1 on the CPU; the library launches on the current device, whatever stream it is given)
+    dev = q.get_device()
+    if dev < 0 or not dev == k.get_device() == v.get_device() == out.get_device() == workspace.get_device() or \
+            dev != torch.cuda.current_device():
+        raise ValueError("tensors must be CUDA tensors on the current device")
     qt, qh, qd = q.stride()
     kt, kh, kd = k.stride()
     vt, vh, vd = v.stride()
@@ -591,15 +594,15 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
         if isinstance(x, torch.Tensor):
             if x.dtype != torch.int32:
                 raise TypeError("cumulative lengths, prefix, mask, token ids and row_seq are int32")
-            if not x.is_cuda or not x.is_contiguous():
-                raise ValueError("tensors must be contiguous CUDA tensors")
+            if x.get_device() != dev or not x.is_contiguous():
+                raise ValueError("tensors must be contiguous CUDA tensors on the current device")
             args.append(x.data_ptr())
         else:
             args.append(x)
     lse = None
     if out_lse is not None:
-        if not out_lse.is_cuda or not out_lse.is_contiguous():
-            raise ValueError("tensors must be contiguous CUDA tensors")
+        if out_lse.get_device() != dev or not out_lse.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors on the current device")
         lse = out_lse.data_ptr()
     if not workspace.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors")
@@ -609,7 +612,7 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     rq, rk, rv, ro = a.refs
     st = getattr(_lib or load(), name)(
         rq, rk, rv, *args, num_seqs, R, T, a.shape_ref, ro, lse, workspace.data_ptr(), workspace.nbytes,
-        torch._C._cuda_getCurrentRawStream(q.get_device()) if stream is None else _stream(stream),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream),
         None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
     if st != KPOOL_OK:
         raise KpoolError(st, name)
