@@ -572,7 +572,7 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
     # (-1 on the CPU; the library launches on the current device, whatever stream it is given)
     dev = q.get_device()
     if dev < 0 or not dev == k.get_device() == v.get_device() == out.get_device() == workspace.get_device() or \
-            dev != torch.cuda.current_device():
+            dev != torch._C._cuda_getDevice():
         raise ValueError("tensors must be CUDA tensors on the current device")
     qt, qh, qd = q.stride()
     kt, kh, kd = k.stride()

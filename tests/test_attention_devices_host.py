@@ -32,7 +32,7 @@ def calls(monkeypatch):
         def __getattr__(self, name):
             return lambda *a: made.append(name) or K.KPOOL_OK
     monkeypatch.setattr(K, "_lib", Library())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
     return made
 

@@ -46,7 +46,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch, "empty", make)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: seen["stream"][-1])
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: "default")
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, *a: handle)
     monkeypatch.setattr(K, "_lib", Library())
