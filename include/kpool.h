@@ -366,7 +366,8 @@ size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const k
  *   cu_q, cu_k  [num_seqs + 1] int32 (device), from 0 to q_rows / k_tokens
  *   out_lse     [q_rows, q_heads] fp32 or NULL
  *   options     NULL, or a score_kernel (KPOOL_SCORE_TC: bf16, head_dim 64 or 128) with
- *               every other field zero
+ *               every other field zero. (With no key token at all the CUDA-core kernel
+ *               writes the empty rows, whatever is asked for.)
  */
 kpool_status kpool_attention_prompt(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
                                     const int32_t* cu_q, const int32_t* cu_k, int32_t num_seqs, int64_t q_rows,
@@ -405,7 +406,8 @@ kpool_status kpool_attention_tree(const kpool_heads* q, const kpool_heads* k, co
  *              NULL when the query rows are the key tokens' own (q_rows = k_tokens,
  *              as for kpool_select): row r is then of the sequence that holds token r.
  *   options    NULL picks a kernel by the sizes (short lists a warp each, a prompt's rows
- *              together, else gathered); KPOOL_SCORE_TC keeps to the tcgen05 kernels
+ *              together, else gathered); KPOOL_SCORE_TC keeps to the tcgen05 kernels, which take
+ *              token strides of k and v below 2^31 elements (else KPOOL_ERR_UNSUPPORTED)
  */
 kpool_status kpool_attention_selected(const kpool_heads* q, const kpool_heads* k, const kpool_heads* v,
                                       const int32_t* token_ids, int32_t width, const int32_t* row_seq,

@@ -217,9 +217,9 @@ cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t
                                    cudaStream_t stream);
 
 // Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens
-// also strides that attn_gather_supported takes.
+// also token strides of k and v that attn_gather_supported takes.
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
-bool attn_gather_supported(const AttnParams& p);
+bool attn_gather_supported(int64_t k_ts, int64_t v_ts);
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
 
 // Selected tokens by one warp an item, in registers: what attn_tc_supported takes, any strides. Wanted where it

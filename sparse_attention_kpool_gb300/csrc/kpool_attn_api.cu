@@ -54,6 +54,9 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
   if (!heads_ok(q, *shape) || !heads_ok(out, *shape)) return KPOOL_ERR_INVALID_ARG;
   // with no key token there is nothing to point at
   if (k_tokens > 0 && (!heads_ok(k, *shape) || !heads_ok(v, *shape))) return KPOOL_ERR_INVALID_ARG;
+  const bool gathers = p.mode == kAttnSelected && k_tokens > 0;
+  if (gathers && opt.score_kernel == KPOOL_SCORE_TC && !attn_gather_supported(k->token_stride, v->token_stride))
+    return KPOOL_ERR_UNSUPPORTED;
   if (!p.cu_k || !aligned(p.cu_k, 4) || !aligned(out_lse, 4)) return KPOOL_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < kpool_attention_workspace_bytes(q_rows, num_seqs, shape))
@@ -90,7 +93,7 @@ kpool_status attention(AttnParams& p, const kpool_heads* q, const kpool_heads* k
     if (attn_warp_wanted(p, sms)) return note_cuda_error(launch_attn_warp(p, sms, ws, stream)) ? KPOOL_OK : KPOOL_ERR_CUDA;
   }
   const bool tc = tc_ok && k_tokens > 0 && opt.score_kernel != KPOOL_SCORE_SIMT &&
-                  (p.mode != kAttnSelected || attn_gather_supported(p));
+                  (!gathers || attn_gather_supported(p.k_ts, p.v_ts));
   const cudaError_t e = tc ? launch_attn_tc(p, ws, stream) : launch_attn_simt(p, dtype, ws, stream);
   return note_cuda_error(e) ? KPOOL_OK : KPOOL_ERR_CUDA;
 }

@@ -1436,8 +1436,8 @@ bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim) {
   return dtype == KPOOL_BF16 && (head_dim == 64 || head_dim == 128);
 }
 
-bool attn_gather_supported(const AttnParams& p) {
-  return p.k_ts < (int64_t(1) << 31) && p.v_ts < (int64_t(1) << 31);  // byte strides in 32 bits
+bool attn_gather_supported(int64_t k_ts, int64_t v_ts) {
+  return k_ts < (int64_t(1) << 31) && v_ts < (int64_t(1) << 31);  // byte strides in 32 bits
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
