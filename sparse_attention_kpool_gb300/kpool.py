@@ -536,8 +536,8 @@ class _AttentionArgs(threading.local):
         self.shape = kpool_attention_shape.from_buffer(self.buffer, 4 * size)
         self.refs = [ctypes.byref(h) for h in self.heads]
         self.shape_ref = ctypes.byref(self.shape)
-        # data, token_stride, head_stride four times; q_heads, kv_heads, head_dim, dtype, scale, reserved
-        self.pack = struct.Struct("=" + "Qqq" * 4 + "iiiifi").pack_into
+        # data, token_stride, head_stride four times; q_heads, kv_heads, head_dim, dtype (reserved stays zero)
+        self.pack = struct.Struct("=" + "Qqq" * 4 + "iiii").pack_into
 
 
 _attention_args = _AttentionArgs()
@@ -608,7 +608,8 @@ def _attention(name, q, k, v, arrays, num_seqs, scale, out, return_lse, out_lse,
         raise ValueError("tensors must be contiguous CUDA tensors")
     a = _attention_args
     a.pack(a.buffer, 0, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh,
-           hq, hkv, d, code, scale, 0)
+           hq, hkv, d, code)
+    a.shape.scale = scale  # (rounded as C does: out of fp32's range it is infinite, and refused)
     rq, rk, rv, ro = a.refs
     st = getattr(_lib or load(), name)(
         rq, rk, rv, *args, num_seqs, R, T, a.shape_ref, ro, lse, workspace.data_ptr(), workspace.nbytes,
