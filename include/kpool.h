@@ -352,8 +352,9 @@ typedef struct {
 } kpool_attention_shape;
 
 /* Workspace size for up to q_rows query rows of up to num_seqs sequences, for any of the three
- * calls; 0 for shapes the calls reject. bf16 at head_dim 64 or 128: partial results of up to 41 MB, and
- * the bits of a prompt's selection (q_rows^2 / 8 bytes, at most 128 MiB; longer prompts do without them). */
+ * calls; 0 for shapes or sizes that they refuse as KPOOL_ERR_INVALID_ARG. bf16 at head_dim 64 or
+ * 128: partial results of up to 41 MB, and the bits of a prompt's selection (q_rows^2 / 8 bytes, at
+ * most 128 MiB; longer prompts do without them). */
 size_t kpool_attention_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_attention_shape* shape);
 
 /*

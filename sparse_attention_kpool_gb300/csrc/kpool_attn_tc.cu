@@ -66,7 +66,9 @@ constexpr int kPCol = 64;      // a tile's weights, bf16 in 64 columns, replace 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
-constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are microseconds
+// 1 s. Legitimate waits are microseconds, and for the cleaning warp's first tile as long as the tiles before it in
+// the segment take (1.7 us each: 14 ms after a million keys).
+constexpr uint64_t kMaxWaitNs = 1000000000ull;
 constexpr int kGatherWarps = 4;
 // Gathered tiles whose validity bits are held: the producer is at most the ring of tiles (8 slots,
 // four K and four V) plus the two K tiles of lead ahead of the softmax.
@@ -1467,7 +1469,14 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
     return p.D == 64 ? launch<64, kGather>(g, ws, stream) : launch<128, kGather>(g, ws, stream);
   }
   if (p.dense) return p.D == 64 ? launch<64, kDense>(p, ws, stream) : launch<128, kDense>(p, ws, stream);
-  // two row tiles per CTA read K and V half as often, but want sequences that fill them
+  // Two row tiles per CTA read K and V half as often, but want sequences that fill them; the lengths are on the
+  // device, so the call's mean decides (one / two row tiles, us, 32 / 8 heads of 128, 32 tokens a row tile):
+  //  - like sequences: 8 x 30 over 8,000 keys 64 / 71, 8 x 33 85 / 72, 8 x 64 90 / 77, 4 x 200 over 6,000 91 / 100;
+  //    prompts 32 x 256 83 / 69, 8 x 1,000 138 / 109, 1 x 2,048 62 / 56, 32,768 tokens 6,860 / 5,916;
+  //    chunks over 30,000 keys, 128 rows 91 / 76, 512 rows 218 / 211; 16 decode tokens 136 / 151;
+  //  - mixed ones lose by it whatever the mean is: 64 decode tokens over 4,000 keys and a chunk of 2,048 rows over
+  //    8,192 316 / 404, of 512 rows 221 / 273; 16 over 8,000 and a prompt of 2,048 129 / 147; 8 trees of 1 to 64
+  //    nodes 98 / 97.
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
   if (p.D == 64) return two ? launch<64, kTwo>(p, ws, stream) : launch<64, kOne>(p, ws, stream);
   return two ? launch<128, kTwo>(p, ws, stream) : launch<128, kOne>(p, ws, stream);
