@@ -418,6 +418,135 @@ kpool_status kpool_attention_selected(const kpool_heads* q, const kpool_heads* k
                                       const kpool_options* options);
 
 /*
+ * Attention over a key/value cache in pages. A pool of num_pages pages of page_size tokens each holds the caches
+ * of all sequences: key j of sequence b is token j % page_size of page
+ * page_table[b * max_pages + j / page_size]. Sequence b holds lengths[b] keys, and its query rows
+ * [cu_q[b], cu_q[b+1]) are the last ones of them: row i of n sees the keys j <= i + lengths[b] - n, as for
+ * kpool_attention_prompt. cu_q NULL: one row per sequence (q_rows = num_seqs), a decode step.
+ *   k, v        [num_pages, page_size, kv_heads, head_dim], with any page, token and head strides
+ *   page_table  [num_seqs, max_pages] int32 (device); entries behind a sequence's last key are not read
+ *   lengths     [num_seqs] int32 (device), 0 to max_pages * page_size (which is below 2^30)
+ * A page may serve several sequences. What a page holds behind a sequence's last key does not reach its rows. A
+ * length out of range gives the sequence's rows 0 and -INFINITY, a page outside the pool leaves the sequence's rows
+ * unspecified (nothing outside the given arrays is read); both record KPOOL_ERR_INVALID_ARG. The workspace is that of
+ * the other attention calls, kpool_attention_workspace_bytes. options: as for kpool_attention_prompt.
+ */
+typedef struct {
+  void* data;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} kpool_pages;
+
+kpool_status kpool_attention_paged(const kpool_heads* q, const kpool_pages* k, const kpool_pages* v,
+                                   const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t page_size,
+                                   const int32_t* lengths, const int32_t* cu_q, int32_t num_seqs, int64_t q_rows,
+                                   const kpool_attention_shape* shape, const kpool_heads* out, float* out_lse,
+                                   void* workspace, size_t workspace_bytes, void* stream,
+                                   const kpool_options* options);
+
+/*
+ * Latent attention: keys and values of all heads come from one latent vector a token, beside a rotated part that
+ * all heads share. Two forms of it, for prompts and for caches.
+ */
+typedef struct {
+  int32_t heads;
+  int32_t key_dim;     /* channels of a key without its rotated part; absorbed: of the latent vector */
+  int32_t rotary_dim;  /* channels of the rotated part */
+  int32_t value_dim;   /* channels of a value; absorbed: key_dim */
+  int32_t dtype;       /* a kpool_dtype: of every tensor */
+  float scale;
+} kpool_latent_shape;
+
+/*
+ * The expanded form, for prompts: every head has keys and values of its own, projected from the latent vectors by
+ * the caller, and the keys of all heads end with the same rotated channels. With [a, b] for a beside b,
+ *     s[j] = scale * q[h] . [k[j, h], k_rotary[j]],  out[h] = sum_J exp(s[j]) v[j, h] / sum_J exp(s[j])
+ * over the keys that kpool_attention_prompt's rows see.
+ *   q          [q_rows, heads, key_dim + rotary_dim]
+ *   k          [k_tokens, heads, key_dim];  v, out  [., heads, value_dim]
+ *   k_rotary   [k_tokens, rotary_dim]: its head_stride is not used, but valid
+ * Each part is a multiple of 16 bytes; key_dim + rotary_dim and value_dim are at most 256. options: as for
+ * kpool_attention_prompt (KPOOL_SCORE_TC: bf16, 128 + 64 channels, values of 128).
+ */
+size_t kpool_latent_prompt_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_latent_shape* shape);
+kpool_status kpool_attention_latent_prompt(const kpool_heads* q, const kpool_heads* k, const kpool_heads* k_rotary,
+                                           const kpool_heads* v, const int32_t* cu_q, const int32_t* cu_k,
+                                           int32_t num_seqs, int64_t q_rows, int64_t k_tokens,
+                                           const kpool_latent_shape* shape, const kpool_heads* out, float* out_lse,
+                                           void* workspace, size_t workspace_bytes, void* stream,
+                                           const kpool_options* options);
+
+/*
+ * The absorbed form, for caches: the caller has multiplied the queries into the latent space, so that the cached
+ * vector c of a token, latent channels first, is its key as a whole and its value in the latent channels:
+ *     s[j] = scale * q[h] . c[j],  out[h] = sum_J exp(s[j]) c[j][0:key_dim] / sum_J exp(s[j])
+ * (the caller projects out to the heads' values). The cache is in pages, as for kpool_attention_paged.
+ *   q          [q_rows, heads, key_dim + rotary_dim];  out  [q_rows, heads, key_dim]
+ *   cache      [num_pages, page_size, key_dim + rotary_dim]; head_stride is not used
+ *   token_ids  NULL with width = KPOOL_WHOLE_CACHE: a row sees all lengths[b] tokens of its sequence; or
+ *              [q_rows, width] int32 (device), as kpool_select / kpool_select_rows leave them: a row sees the tokens
+ *              that are named (ids outside [0, lengths[b]) are not seen, an id that appears twice counts twice)
+ *   row_seq    [q_rows] int32 (device): the row's sequence; NULL: row r is of sequence r (q_rows = num_seqs)
+ * A row whose sequence does not exist gets 0 and -INFINITY (and KPOOL_ERR_INVALID_ARG is recorded). Each part is a
+ * multiple of 16 bytes, key_dim + rotary_dim at most 1,024. options: KPOOL_SCORE_TC takes bf16, 512 + 64 channels.
+ */
+#define KPOOL_WHOLE_CACHE (-1)
+size_t kpool_latent_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_latent_shape* shape);
+kpool_status kpool_attention_latent(const kpool_heads* q, const kpool_pages* cache, const int32_t* page_table,
+                                    int32_t max_pages, int32_t num_pages, int32_t page_size, const int32_t* lengths,
+                                    const int32_t* token_ids, int32_t width, const int32_t* row_seq, int32_t num_seqs,
+                                    int64_t q_rows, const kpool_latent_shape* shape, const kpool_heads* out,
+                                    float* out_lse, void* workspace, size_t workspace_bytes, void* stream,
+                                    const kpool_options* options);
+
+/*
+ * Rotary positions. Channel pair (a, b) number i of a head of the token at position t becomes
+ *     (a cos x - b sin x, b cos x + a sin x) * magnitude,   x = t f[i]
+ * with KPOOL_ROTARY_INVERSE x = -t f[i] (which, with the same magnitude, is the gradient's way back, too). The
+ * rotated channels are [offset, offset + rotary_dim) of each head; pair i is channels i and i + rotary_dim / 2 of
+ * them, or with KPOOL_ROTARY_INTERLEAVED channels 2 i and 2 i + 1. The other channels are copied. Products
+ * and sums are in fp32, rounded once; angles are exact to 2^-24 of a half turn at any position.
+ *   in, out    [tokens, heads, head_dim], any token and head strides (multiples of the element; 16-byte aligned
+ *              ones are faster); out is in itself (same strides), or overlaps no input
+ *   positions  [tokens] int32 (device), any value
+ *   table      [rotary_dim / 2] int64 (device): f[i] in turns a token, a fraction in units of 2^-64
+ * q and k (NULL: none) are two tensors of the same tokens, each with sizes of its own.
+ */
+#define KPOOL_ROTARY_INTERLEAVED 1
+#define KPOOL_ROTARY_INVERSE 2
+
+typedef struct {
+  kpool_heads in;
+  kpool_heads out;
+  int32_t heads;
+  int32_t head_dim;  /* at most 4,096, as heads */
+  int32_t offset;
+  int32_t reserved;  /* must be zero */
+} kpool_rotary_part;
+
+typedef struct {
+  int32_t rotary_dim; /* even */
+  int32_t dtype;      /* a kpool_dtype */
+  int32_t flags;
+  float magnitude;    /* finite */
+} kpool_rotary_shape;
+
+kpool_status kpool_rotary(const kpool_rotary_part* q, const kpool_rotary_part* k, const int32_t* positions,
+                          const int64_t* table, int64_t tokens, const kpool_rotary_shape* shape, void* stream);
+
+/*
+ * A table for kpool_rotary, written to host memory (out: [rotary_dim / 2]): f[i] = base^(-2 i / rotary_dim) radians a
+ * token, stretched for contexts longer than the model was trained on:
+ *     f[i] * (keep + (1 - keep) / factor),  keep = clamp((turns - low) / (high - low), 0, 1),
+ *     turns = original_length * f[i] / 2 pi
+ * (pairs that turn often within the original context stay as they are, slow ones are stretched by factor);
+ * original_length 0 stretches all pairs alike, factor 1 none.
+ */
+kpool_status kpool_rotary_table(int32_t rotary_dim, double base, double factor, double original_length, double low,
+                                double high, int64_t* out);
+
+/*
  * Synchronises `stream`, then reads the device error word the last call on this
  * workspace recorded: KPOOL_OK, KPOOL_ERR_INVALID_ARG (malformed cu_seqlens),
  * KPOOL_ERR_DEVICE_TIMEOUT (a bounded wait ran out), KPOOL_ERR_INTERNAL (a

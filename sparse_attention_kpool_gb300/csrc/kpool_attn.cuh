@@ -40,11 +40,21 @@ struct AttnParams {
   const int32_t* ids;                        // [R, width] (selected)
   const int32_t* row_seq;                    // [R] or null (selected)
   int32_t mask_words, width;
+  // Keys in pages (prompt): key j of sequence b is token j % page_size of page table[b * max_pages + j / page_size];
+  // k and v are then the pages, with these strides between them. cu_q may be null: a row per sequence.
+  const int32_t* table;                      // [S, max_pages] or null
+  const int32_t* lengths;                    // [S] keys of a sequence
+  int32_t max_pages, page_size, num_pages;
+  int64_t k_ps, v_ps;
+  // Keys whose last channels are shared by all heads (prompt): channels [Dn, D) come from here
+  const void* kr;                            // [T, D - Dn] or null
+  int64_t kr_ts;
   const AttnDense* dense;                    // null, or what the dense form of a selection goes by
   const int32_t* list;                       // with dense, gathering: the listed rows
   int32_t S, R;
   int64_t T;
-  int32_t Hq, Hkv, G, D;
+  int32_t Hq, Hkv, G, D;                     // D: channels of q and k
+  int32_t Dn, Dv;                            // channels that k holds itself (D without kr), and of v and out
   float scale;
   AttnMode mode;
 };
@@ -54,18 +64,33 @@ struct AttnParams {
 // false when the sequence's entries are malformed: its rows then get zeros.
 struct AttnSeq {
   int32_t q0, nq;     // first query row and their number
-  int32_t k0, nk;     // first key token and the keys that exist for some row
+  int32_t k0, nk;     // first key token (pages: the sequence itself) and the keys that exist for some row
   int32_t prefix;     // row i sees keys < prefix (+ i + 1 when causal); may be negative (prompt)
   bool ok;
 };
 
+// First query row of sequence b (b <= S).
+__device__ __forceinline__ int attn_q0(const AttnParams& p, int b) { return p.cu_q ? __ldg(p.cu_q + b) : b; }
+
+// Keys that a sequence's pages can hold.
+__device__ __forceinline__ int64_t attn_page_keys(const AttnParams& p) { return int64_t(p.max_pages) * p.page_size; }
+
 __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
   AttnSeq s;
-  s.q0 = __ldg(p.cu_q + b);
-  const int64_t q1 = __ldg(p.cu_q + b + 1);
-  s.k0 = __ldg(p.cu_k + b);
-  const int64_t k1 = __ldg(p.cu_k + b + 1);
-  s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= p.R && s.k0 >= 0 && k1 >= s.k0 && k1 <= p.T;
+  s.q0 = attn_q0(p, b);
+  const int64_t q1 = attn_q0(p, b + 1);
+  int64_t k1;
+  if (p.table) {
+    s.k0 = b;
+    const int n = __ldg(p.lengths + b);
+    k1 = int64_t(b) + n;
+    s.ok = n >= 0 && n <= attn_page_keys(p);
+  } else {
+    s.k0 = __ldg(p.cu_k + b);
+    k1 = __ldg(p.cu_k + b + 1);
+    s.ok = s.k0 >= 0 && k1 >= s.k0 && k1 <= p.T;
+  }
+  s.ok = s.ok && s.q0 >= 0 && q1 >= s.q0 && q1 <= p.R;
   if (!s.ok) {
     // rows inside the call's range still get their zeros
     s.q0 = max(0, min(s.q0, p.R));
@@ -128,7 +153,7 @@ __device__ __forceinline__ int attn_seq_of_tile(const AttnParams& p, int tile, i
   int lo = 0, hi = p.S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu_q + mid) / tt + mid <= tile) lo = mid; else hi = mid - 1;
+    if (attn_q0(p, mid) / tt + mid <= tile) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
@@ -141,9 +166,18 @@ __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader*
   const int lane = threadIdx.x & 31;
   bool bad = false;
   for (int b = lane; b <= p.S; b += 32) {
-    const int k = __ldg(p.cu_k + b);
-    if (b == 0 ? k != 0 : k < __ldg(p.cu_k + b - 1)) bad = true;
-    if (b == p.S && k != p.T) bad = true;
+    int k = 0;
+    if (p.table) {
+      if (b < p.S) {
+        const int n = __ldg(p.lengths + b);
+        if (n < 0 || n > attn_page_keys(p)) bad = true;
+      }
+      if (!p.cu_q) continue;
+    } else {
+      k = __ldg(p.cu_k + b);
+      if (b == 0 ? k != 0 : k < __ldg(p.cu_k + b - 1)) bad = true;
+      if (b == p.S && k != p.T) bad = true;
+    }
     if (p.mode == kAttnSelected) continue;
     const int q = __ldg(p.cu_q + b);
     if (b == 0 ? q != 0 : q < __ldg(p.cu_q + b - 1)) bad = true;
@@ -163,6 +197,14 @@ __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader*
   }
   bad = __any_sync(0xffffffffu, bad);
   if (lane == 0 && bad) record_error(hdr, KPOOL_ERR_INVALID_ARG);
+}
+
+// The page that key j of sequence b lies in; -1 (and *bad) where the table names none of the pool's.
+__device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j, bool* bad) {
+  const int page = __ldg(p.table + int64_t(b) * p.max_pages + j / p.page_size);
+  if (page >= 0 && page < p.num_pages) return page;
+  *bad = true;
+  return -1;
 }
 
 // Key tokens of selected row r: first token and number (0 when the row has no valid sequence).
@@ -219,6 +261,8 @@ cudaError_t launch_attn_dense_mask(const AttnParams& p, AttnDense* ctl, uint32_t
 // Tensor-core kernel: bf16, head_dim 64 or 128, at least one key token; over selected tokens
 // also token strides of k and v that attn_gather_supported takes.
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
+// The same for keys with a shared part: 128 + 64 channels, values of 128.
+bool attn_tc_shared_supported(kpool_dtype dtype, int32_t own, int32_t shared, int32_t value);
 bool attn_gather_supported(int64_t k_ts, int64_t v_ts);
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
 
@@ -227,7 +271,7 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
 bool attn_warp_wanted(const AttnParams& p, int sms);
 cudaError_t launch_attn_warp(const AttnParams& p, int sms, char* ws, cudaStream_t stream);
 
-// CUDA-core kernel: fp32 or bf16, any head_dim <= 256.
+// CUDA-core kernel: fp32 or bf16, any head_dim <= 256 (of keys and of values).
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
 
 }  // namespace kpool

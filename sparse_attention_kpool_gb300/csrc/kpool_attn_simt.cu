@@ -45,19 +45,19 @@ __device__ __forceinline__ void group_sync(int group) {
 }
 
 // Shared memory, in floats: Q, then each group's K and V block; the groups' results overlay the blocks.
-inline __host__ __device__ int group_floats(int D) { return kKeys * (2 * D + 4 + 4 * kPerWarp); }
+inline __host__ __device__ int group_floats(int D, int Dv) { return kKeys * (D + Dv + 4 + 4 * kPerWarp); }
 
 template <typename E, int kGroups>
 __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
     attn_simt_kernel(const __grid_constant__ AttnParams p, int gt, int tt, WorkspaceHeader* hdr) {
   constexpr int kH = kGroups == 4 ? 1 : 2;  // 128-channel parts of a head
   extern __shared__ __align__(16) float smem[];
-  const int D = p.D, ldk = D + 4;
+  const int D = p.D, Dv = p.Dv, ldk = D + 4;
   const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
   float* s_q = smem;                                        // [kVRows][D]
-  float* s_k = s_q + kVRows * D + group * group_floats(D);  // [kKeys][D + 4]
-  float* s_v = s_k + kKeys * ldk;                           // [kKeys][D]
-  float* s_p = s_v + kKeys * D;                             // [4 warps][kKeys][kPerWarp]
+  float* s_k = s_q + kVRows * D + group * group_floats(D, Dv);  // [kKeys][D + 4]
+  float* s_v = s_k + kKeys * ldk;                               // [kKeys][Dv]
+  float* s_p = s_v + kKeys * Dv;                                // [4 warps][kKeys][kPerWarp]
   const int lane = tid & 31, warp = tid >> 5;
   const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
   if (checks && threadIdx.x == 0) attn_clear_error(hdr);
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   } else {
     const int b = attn_seq_of_tile(p, blockIdx.x, tt);
     sq = attn_seq(p, b);
-    i0 = (int(blockIdx.x) - (__ldg(p.cu_q + b) / tt + b)) * tt;
+    i0 = (int(blockIdx.x) - (attn_q0(p, b) / tt + b)) * tt;
     if (i0 < 0 || i0 >= sq.nq) {
       __syncwarp();
       if (checks && threadIdx.x < 32) attn_check(p, hdr);
@@ -93,7 +93,9 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   const E* q = static_cast<const E*>(p.q);
   const E* kk = static_cast<const E*>(p.k) + int64_t(hk) * p.k_hs;
   const E* vv = static_cast<const E*>(p.v) + int64_t(hk) * p.v_hs;
-  const int chunks = D / 4;
+  const E* kr = static_cast<const E*>(p.kr);
+  const int chunks = D / 4, pieces = max(D, Dv) / 4;
+  bool bad_page = false;
   for (int x = threadIdx.x; x < kVRows * chunks; x += kGroupThreads * kGroups) {
     const int r = x / chunks, c = x % chunks, i = i0 + r / gt, g = g0 + r % gt;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -120,28 +122,36 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   __syncthreads();
   for (int j0 = group * kKeys; j0 < end; j0 += kGroups * kKeys) {
     group_sync(group);
-    // two pieces of K and V in flight per thread; piece x is channels 4 (x % chunks).. of key x / chunks
-    for (int x0 = tid; x0 < kKeys * chunks; x0 += 2 * kGroupThreads) {
+    // two pieces of K and V in flight per thread; piece x is channels 4 (x % pieces).. of key x / pieces
+    for (int x0 = tid; x0 < kKeys * pieces; x0 += 2 * kGroupThreads) {
       float4 a[2], b[2];
       int at[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int x = x0 + y * kGroupThreads, jj = x / chunks, c = 4 * (x - jj * chunks);
-        at[y] = x < kKeys * chunks ? jj * 1024 + c : -1;
+        const int x = x0 + y * kGroupThreads, jj = x / pieces, c = 4 * (x - jj * pieces);
+        at[y] = x < kKeys * pieces ? jj * 1024 + c : -1;
         a[y] = b[y] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (at[y] < 0 || j0 + jj >= end) continue;
         const int id = selected ? __ldg(ids + j0 + jj) : j0 + jj;
         if (id < 0 || id >= sq.nk) continue;
+        if (p.table) {  // a page that the pool does not have reads as zeros
+          const int page = attn_page(p, sq.k0, id, &bad_page), in = id % p.page_size;
+          if (page < 0) continue;
+          a[y] = load4(kk + int64_t(page) * p.k_ps + in * p.k_ts + c);
+          b[y] = load4(vv + int64_t(page) * p.v_ps + in * p.v_ts + c);
+          continue;
+        }
         const int64_t t = int64_t(sq.k0) + id;
-        a[y] = load4(kk + t * p.k_ts + c);
-        b[y] = load4(vv + t * p.v_ts + c);
+        if (c < p.Dn) a[y] = load4(kk + t * p.k_ts + c);
+        else if (c < D) a[y] = load4(kr + t * p.kr_ts + (c - p.Dn));
+        if (c < Dv) b[y] = load4(vv + t * p.v_ts + c);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         if (at[y] < 0) continue;
         const int jj = at[y] >> 10, c = at[y] & 1023;
-        store4(s_k + jj * ldk + c, a[y]);
-        store4(s_v + jj * D + c, b[y]);
+        if (c < D) store4(s_k + jj * ldk + c, a[y]);
+        if (c < Dv) store4(s_v + jj * Dv + c, b[y]);
       }
     }
     group_sync(group);
@@ -202,8 +212,8 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
         const int c = h * 128 + lane * 4;
-        if (c >= D) break;
-        const float4 b = load4(s_v + jj * D + c);
+        if (c >= Dv) break;
+        const float4 b = load4(s_v + jj * Dv + c);
 #pragma unroll
         for (int r = 0; r < kPerWarp; ++r) {
           const float x = r == 0 ? w.x : r == 1 ? w.y : r == 2 ? w.z : w.w;
@@ -225,17 +235,17 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
     }
   }
 
-  // the groups' results: [group][kVRows][D] sums, then [group][kVRows] (m, l); group g finishes row g of each warp
+  // the groups' results: [group][kVRows][Dv] sums, then [group][kVRows] (m, l); group g finishes row g of each warp
   __syncthreads();
   float* s_o = smem + kVRows * D;
-  float2* s_ml = reinterpret_cast<float2*>(s_o + kGroups * kVRows * D);
+  float2* s_ml = reinterpret_cast<float2*>(s_o + kGroups * kVRows * Dv);
 #pragma unroll
   for (int r = 0; r < kPerWarp; ++r) {
     const int vr = group * kVRows + warp * kPerWarp + r;
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       const int c = h * 128 + lane * 4;
-      if (c < D) store4(s_o + vr * D + c, o[r][h]);
+      if (c < Dv) store4(s_o + vr * Dv + c, o[r][h]);
     }
     if (lane == 0) s_ml[vr] = make_float2(m[r], l[r]);
   }
@@ -259,8 +269,8 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
         const int c = h * 128 + lane * 4;
-        if (c >= D) break;
-        const float4 f = load4(s_o + (g * kVRows + vr) * D + c);
+        if (c >= Dv) break;
+        const float4 f = load4(s_o + (g * kVRows + vr) * Dv + c);
         o[r][h].x = fmaf(f.x, w, o[r][h].x);
         o[r][h].y = fmaf(f.y, w, o[r][h].y);
         o[r][h].z = fmaf(f.z, w, o[r][h].z);
@@ -274,26 +284,29 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       const int c = h * 128 + lane * 4;
-      if (c >= D) break;
+      if (c >= Dv) break;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (!none) f = make_float4(o[r][h].x * inv, o[r][h].y * inv, o[r][h].z * inv, o[r][h].w * inv);
       store4(out + row * p.o_ts + int64_t(head) * p.o_hs + c, f);
     }
     if (lane == 0 && p.lse) p.lse[row * p.Hq + head] = none ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
   }
+  if (bad_page) record_error(hdr, KPOOL_ERR_INVALID_ARG);
   __syncwarp();
   if (checks && threadIdx.x < 32) attn_check(p, hdr);
 }
 
 template <typename E, int kGroups>
 cudaError_t launch(const AttnParams& p, const dim3& grid, int gt, int tt, WorkspaceHeader* hdr, cudaStream_t stream) {
-  auto bytes = [](int D) { return sizeof(float) * (size_t(kVRows) * D + size_t(kGroups) * group_floats(D)); };
+  auto bytes = [](int D, int Dv) {
+    return sizeof(float) * (size_t(kVRows) * D + size_t(kGroups) * group_floats(D, Dv));
+  };
   auto kernel = attn_simt_kernel<E, kGroups>;
   static std::atomic<uint64_t> ready{0};
-  const size_t most = bytes(kGroups == 4 ? 128 : 256);
+  const size_t most = bytes(256, kGroups == 4 ? 128 : 256);
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), most, &ready);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kGroupThreads * kGroups, bytes(p.D), stream>>>(p, gt, tt, hdr);
+  kernel<<<grid, kGroupThreads * kGroups, bytes(p.D, p.Dv), stream>>>(p, gt, tt, hdr);
   return cudaGetLastError();
 }
 
@@ -307,9 +320,9 @@ cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, c
   const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   if (dtype == KPOOL_BF16)
-    return p.D <= 128 ? launch<__nv_bfloat16, 4>(p, grid, gt, tt, hdr, stream)
+    return p.Dv <= 128 ? launch<__nv_bfloat16, 4>(p, grid, gt, tt, hdr, stream)
                       : launch<__nv_bfloat16, 2>(p, grid, gt, tt, hdr, stream);
-  return p.D <= 128 ? launch<float, 4>(p, grid, gt, tt, hdr, stream) : launch<float, 2>(p, grid, gt, tt, hdr, stream);
+  return p.Dv <= 128 ? launch<float, 4>(p, grid, gt, tt, hdr, stream) : launch<float, 2>(p, grid, gt, tt, hdr, stream);
 }
 
 }  // namespace kpool

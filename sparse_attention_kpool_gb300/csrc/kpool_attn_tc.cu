@@ -13,6 +13,7 @@
 //            gather of four rows moved 6 bytes a cycle and SM, these copies 27; 2048 rows x
 //            2052 ids of 64 / 1 heads: 1222 against 288 us.)
 //   kDense   kTwo under a mask of bits for all keys (kpool_attn_dense.cu).
+//   kPagedOne, kPagedTwo   kOne and kTwo over a cache in pages.
 //
 // Roles (12 warps; kGather 16): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread
 // per row; warp 8 loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns
@@ -76,23 +77,35 @@ constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
 // The forms of the kernel: one or two row tiles of consecutive tokens, one token's heads over gathered keys, or
-// two row tiles under a mask of bits for all keys (the dense form of a selection).
-enum Form { kOne, kTwo, kGather, kDense };
+// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages.
+enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo };
 
-template <int D, Form F>
+// Where a tile of the ring lies, and the parity of its use of that slot.
+struct Place {
+  uint32_t slot, par;
+};
+
+// DK: channels of Q and K, DV: of V and the result. With DK > DV the last DK - DV channels of K come from a tensor
+// of their own without heads, and K and V have rings of their own.
+template <int DK, int DV, Form F>
 struct Cfg {
-  static constexpr bool TWO = F == kTwo || F == kDense;
+  static constexpr bool TWO = F == kTwo || F == kDense || F == kPagedTwo;
+  static constexpr bool PAGED = F == kPagedOne || F == kPagedTwo;
+  static constexpr bool SHARED = DK != DV;
   // The ring holds K(0) .. K(kAhead - 1), then K(j), V(j - kAhead) in turn: the order in which the MMAs use
   // them, K one tile (one-tile form: one per group) ahead.
   static constexpr int kAhead = TWO ? 1 : 2;
   static constexpr int kThreads = F == kGather ? 512 : 384;
-  static constexpr int kTileBytes = kTileKeys * D * 2;   // one K or V tile, one Q tile
+  static constexpr int kTileBytes = kTileKeys * DK * 2;  // one K tile, one Q tile
+  static constexpr int kVBytes = kTileKeys * DV * 2;     // one V tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
-  static constexpr int kBlocks = D / 64;
+  static constexpr int kBlocks = DK / 64, kVBlocks = DV / 64;
   static constexpr int kQTiles = TWO ? 2 : 1;
-  static constexpr int kStages = D == 64 ? 8 : (TWO ? 5 : 6);
+  // rings apart: the first kKSlots slots hold K, the others V; as many as fit beside Q at 192 + 128 channels
+  static constexpr int kKSlots = 2, kVSlots = TWO ? 1 : 2;
+  static constexpr int kStages = SHARED ? kKSlots + kVSlots : DK == 64 ? 8 : (TWO ? 5 : 6);
   static constexpr int kOffRing = kQTiles * kTileBytes;
-  static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffRing + (SHARED ? kKSlots * kTileBytes + kVSlots * kVBytes : kStages * kTileBytes);
   // full[stages] empty[stages] clean[stages] dirty[stages] q_full q_empty s_full[2] p_ready[2] o_final o_free done
   // seg_full[ring] seg_empty[ring] turn[2]
   static constexpr int kNumBars = 4 * kStages + 11 + 2 * kSegRing;
@@ -103,13 +116,28 @@ struct Cfg {
   static_assert(kOffBits % 16 == 0 && kOffSeg % 16 == 0 && kOffStat % 16 == 0, "16-byte accesses");
   static constexpr int kSmem = kOffBits + (F == kGather ? 16 * kBitsRing : 0);
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
-};
 
-// Ring use, within its segment of n tiles, of tile j's K and V.
-template <int kAhead>
-__device__ __forceinline__ uint32_t k_use(int j) { return uint32_t(j + max(0, j - kAhead)); }
-template <int kAhead>
-__device__ __forceinline__ uint32_t v_use(int j, int n) { return uint32_t(min(n, j + kAhead + 1) + j); }
+  // Use number u of the ring (of the K or the V ring where they are apart), and a slot's bytes from the ring's start.
+  __device__ static __forceinline__ Place k_slot(uint32_t u) {
+    if (SHARED) return {u % kKSlots, (u / kKSlots) & 1};
+    return {u % kStages, (u / kStages) & 1};
+  }
+  __device__ static __forceinline__ Place v_slot(uint32_t u) {
+    if (SHARED) return {kKSlots + u % kVSlots, (u / kVSlots) & 1};
+    return k_slot(u);
+  }
+  __device__ static __forceinline__ uint32_t slot_at(uint32_t slot) {
+    if (SHARED && slot >= kKSlots) return kKSlots * kTileBytes + (slot - kKSlots) * kVBytes;
+    return slot * kTileBytes;
+  }
+  // K and V of tile j of a segment of n tiles; `use`: ring uses before the segment, two a tile.
+  __device__ static __forceinline__ Place k_place(uint32_t use, int j) {
+    return k_slot(SHARED ? use / 2 + j : use + uint32_t(j + max(0, j - kAhead)));
+  }
+  __device__ static __forceinline__ Place v_place(uint32_t use, int j, int n) {
+    return v_slot(SHARED ? use / 2 + j : use + uint32_t(min(n, j + kAhead + 1) + j));
+  }
+};
 
 struct Misc {
   int64_t base;       // persistent form: first position of sequence b
@@ -119,6 +147,7 @@ struct Misc {
   int32_t b;
   uint32_t tmem;
   volatile int32_t abort;
+  volatile int32_t bad_page;           // a page of the table that the pool does not have
   volatile int32_t bad_seg[kSegRing];  // 1 + the last segment of this slot with an infinity or NaN in a cleaned V tile
 };
 static_assert(sizeof(Misc) <= 80, "Misc fits its space");
@@ -258,7 +287,7 @@ __device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int til
   const int tile = tiles - 1 - int(blockIdx.x % tiles);
   const int b = attn_seq_of_tile(p, tile, ttb);
   s->sq = attn_seq(p, b);
-  s->tok0 = (tile - (__ldg(p.cu_q + b) / ttb + b)) * ttb;
+  s->tok0 = (tile - (attn_q0(p, b) / ttb + b)) * ttb;
   if (s->tok0 < 0 || s->tok0 >= s->sq.nq) return false;
   s->kt0 = 0;
   s->n = tile_cost(p, s->sq, s->tok0 / ttb, ttb);
@@ -408,6 +437,13 @@ __device__ __forceinline__ void write_join(JoinItem* out, const Seg& s, int64_t 
 
 // ------------------------------------------------------------------------- waits
 
+// Keys that lie in one page wherever a multiple of them begins: the largest power of two up to a tile that divides
+// the page size.
+__host__ __device__ __forceinline__ int piece_rows(int page_size) {
+  const int low = page_size & -page_size;
+  return low < kTileKeys ? low : kTileKeys;
+}
+
 // Bounded wait; also gives up when another role did.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -518,13 +554,14 @@ __device__ __forceinline__ bool bad_bf16(uint32_t x) { return (x & 0x7F80u) == 0
 
 // -------------------------------------------------------------------- the kernel
 
-template <int D, Form F>
-__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
+template <int DK, int DV, Form F>
+__global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p, int tiles,
-                   int direct, float* part, int slot_rows, JoinItem* joins, WorkspaceHeader* hdr) {
-  using C = Cfg<D, F>;
-  constexpr bool TWO = C::TWO, GATHER = F == kGather, DENSE = F == kDense;
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
+                   const __grid_constant__ AttnParams p, int tiles, int direct, float* part, int slot_rows,
+                   JoinItem* joins, WorkspaceHeader* hdr) {
+  using C = Cfg<DK, DV, F>;
+  constexpr bool TWO = C::TWO, GATHER = F == kGather, DENSE = F == kDense, PAGED = C::PAGED;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -591,6 +628,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     }
     ptx::fence_mbar_init();
     misc->abort = 0;
+    misc->bad_page = 0;
     for (int i = 0; i < kSegRing; ++i) misc->bad_seg[i] = 0;
   }
   if (warp == 9) {
@@ -646,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       // Warp w fetches keys [32 w, 32 w + 32) of every tile, 16 bytes a lane, into the swizzled
       // layout that TMA would write. An id outside the sequence reads nothing and leaves zeros,
       // so no weight of zero meets an infinity or NaN.
-      constexpr int kChunks = D / 8;               // 16-byte pieces of a row
+      constexpr int kChunks = DK / 8;              // 16-byte pieces of a row
       constexpr int kRowsPer = 32 / kChunks;       // rows per warp instruction
       const int w = warp - 12, c = lane % kChunks, rsub = lane / kChunks;
       // the lane's place in the warp's first rows; a row's pieces are permuted by its number's low bits
@@ -708,56 +746,91 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
       ptx::cp_async_wait_all();                    // every copy has landed before the CTA exits
-    } else if (warp == 8) {
-      if (lane == 0) {  // -------------------------------------------------- TMA producer
+    } else if (warp == 8) {  // ------------------------------------------------- TMA producer
+      // One lane, or over pages all of them, each with its own pieces of a tile.
+      if (PAGED || lane == 0) {
         SegIter it;
         if (!direct) it.start(p, misc, ttb);
-        uint32_t fills = 0, q_loads = 0;
-        bool ok = true;
+        uint32_t fills[2] = {0, 0}, q_loads = 0;  // of the ring, or of K's and V's
+        bool ok = true, bad_page = false;
         Seg sg{};
-        auto load_kv = [&](const CUtensorMap* tm, int kt) {
-          const int st = fills % C::kStages;
-          if (fills >= C::kStages && !wait_bar(empty + st, (fills / C::kStages - 1) & 1, misc)) return false;
-          uint8_t* dst = smem + C::kOffRing + st * C::kTileBytes;
-          ptx::mbar_arrive_expect_tx(full + st, C::kTileBytes);
-          ++fills;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          const bool r = wait_bar(bar, parity, misc);
+          return PAGED ? bool(__all_sync(0xffffffffu, r)) : r;
+        };
+        auto load_kv = [&](bool is_k, int kt) {
+          uint32_t& f = fills[C::SHARED && !is_k];
+          const Place at = is_k ? C::k_slot(f) : C::v_slot(f);
+          const uint32_t st = at.slot, depth = !C::SHARED ? C::kStages : is_k ? C::kKSlots : C::kVSlots;
+          if (f >= depth && !wait(empty + st, at.par ^ 1)) return false;
+          ++f;
+          uint8_t* dst = smem + C::kOffRing + C::slot_at(st);
+          const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+          if (PAGED) {
+            // Pieces of `rows` keys lie in one page each; the keys past the last one that a row sees are not loaded.
+            const int rows = piece_rows(p.page_size), key0 = kt * kTileKeys;
+            const int pieces = min(kTileKeys / rows, (sg.end - key0 + rows - 1) / rows);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, uint32_t(pieces * rows * 128 * C::kVBlocks));
+            __syncwarp();
+            for (int x = lane; x < pieces; x += 32) {
+              const int j = key0 + x * rows, page = attn_page(p, sg.sq.k0, j, &bad_page);
 #pragma unroll
-          for (int h = 0; h < C::kBlocks; ++h)
-            ptx::tma_load_3d(dst + h * C::kHalf, tm, full + st, 64 * h, sg.hk, sg.sq.k0 + kt * kTileKeys);
-          if (tm == &tm_v && !no_cleaning && tile_masked(&sg, kt)) ptx::mbar_arrive(dirty + st);
+              for (int h = 0; h < C::kVBlocks; ++h)  // (page -1: zeros)
+                ptx::tma_load_4d(dst + h * C::kHalf + x * rows * 128, tm, full + st, 64 * h, sg.hk, j % p.page_size, page);
+            }
+          } else {
+            ptx::mbar_arrive_expect_tx(full + st, is_k ? C::kTileBytes : C::kVBytes);
+#pragma unroll
+            for (int h = 0; h < C::kVBlocks; ++h)
+              ptx::tma_load_3d(dst + h * C::kHalf, tm, full + st, 64 * h, sg.hk, sg.sq.k0 + kt * kTileKeys);
+            if (C::SHARED && is_k) {
+#pragma unroll
+              for (int h = C::kVBlocks; h < C::kBlocks; ++h)
+                ptx::tma_load_3d(dst + h * C::kHalf, &tm_r, full + st, 64 * (h - C::kVBlocks), 0,
+                                 sg.sq.k0 + kt * kTileKeys);
+            }
+          }
+          if (!is_k && !no_cleaning && tile_masked(&sg, kt) && lane == 0) ptx::mbar_arrive(dirty + st);
           return true;
         };
         for (int i = 0;; ++i) {
           const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
-          if (i == 0 && !direct) {
+          if (i == 0 && !direct && lane == 0) {
             if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
             else joins[blockIdx.x].runs = 0;
           }
           if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
-          if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
-          ring[i % kSegRing] = sg;
-          ptx::mbar_arrive(seg_full + i % kSegRing);
+          if (i >= kSegRing && !wait(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1)) break;
+          if (lane == 0) {
+            ring[i % kSegRing] = sg;
+            ptx::mbar_arrive(seg_full + i % kSegRing);
+          }
           if (!more) break;
           if (sg.n == 0) continue;
-          if (q_loads > 0 && !wait_bar(q_empty, (q_loads - 1) & 1, misc)) break;
-          ptx::mbar_arrive_expect_tx(q_full, C::kQTiles * C::kBlocks * uint32_t(tt * p.G) * 128);
+          if (q_loads > 0 && !wait(q_empty, (q_loads - 1) & 1)) break;
           ++q_loads;
-          for (int g = 0; g < C::kQTiles; ++g)
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(q_full, C::kQTiles * C::kBlocks * uint32_t(tt * p.G) * 128);
+            for (int g = 0; g < C::kQTiles; ++g)
 #pragma unroll
-            for (int h = 0; h < C::kBlocks; ++h)
-              ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
-                               sg.sq.q0 + sg.tok0 + g * tt);
+              for (int h = 0; h < C::kBlocks; ++h)
+                ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
+                                 sg.sq.q0 + sg.tok0 + g * tt);
+          }
           for (int j = 0; ok && j < sg.n + C::kAhead; ++j) {
-            if (j < sg.n) ok = load_kv(&tm_k, sg.kt0 + j);
-            if (ok && j >= C::kAhead) ok = load_kv(&tm_v, sg.kt0 + j - C::kAhead);
+            if (j < sg.n) ok = load_kv(true, sg.kt0 + j);
+            if (ok && j >= C::kAhead) ok = load_kv(false, sg.kt0 + j - C::kAhead);
           }
           if (!ok) break;
         }
+        if (PAGED && bad_page) misc->bad_page = 1;
         // every copy armed above lands before the CTA exits
-        for (uint32_t s2 = 0; s2 < uint32_t(C::kStages) && s2 < fills; ++s2) {
-          const uint32_t uses = (fills - 1 - s2) / C::kStages;
-          ptx::mbar_wait_bounded(full + s2, uses & 1, int64_t(1) << 40, kMaxWaitNs);
-        }
+        auto land = [&](uint32_t first, uint32_t depth, uint32_t f) {
+          for (uint32_t s2 = 0; s2 < depth && s2 < f; ++s2)
+            ptx::mbar_wait_bounded(full + first + s2, ((f - 1 - s2) / depth) & 1, int64_t(1) << 40, kMaxWaitNs);
+        };
+        land(0, C::SHARED ? C::kKSlots : C::kStages, fills[0]);
+        if (C::SHARED) land(C::kKSlots, C::kVSlots, fills[1]);
         if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
       }
     } else if (warp == 9 || warp == 10) {
@@ -770,14 +843,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         const uint64_t k_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + C::kOffRing));
         const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + C::kOffRing), C::kHalf);
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kTileRows, kTileKeys);
-        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32_bn(kTileRows, D);
-        const uint32_t s_acc = tmem + g * kTileKeys, o_acc = tmem + 256 + g * D;
+        constexpr uint32_t idesc_o = ptx::idesc_bf16_f32_bn(kTileRows, DV);
+        const uint32_t s_acc = tmem + g * kTileKeys, o_acc = tmem + 256 + g * DV;
         uint32_t use = 0, q_uses = 0, p_uses = 0, turns = 0;  // ring uses before this segment, Q tiles, P tiles
         uint32_t clean_par = 0;                    // bit per ring slot
         bool ok = true;
         const Seg* sg;
-        auto landed = [&](uint32_t u) {
-          const bool r = wait_bar(full + u % C::kStages, (u / C::kStages) & 1, misc);
+        auto landed = [&](Place u) {
+          const bool r = wait_bar(full + u.slot, u.par, misc);
           if (GATHER) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
           return r;
         };
@@ -790,19 +863,19 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           ++turns;
           return r;
         };
-        auto qk = [&](uint32_t u, bool pass) {
-          const uint64_t b = k_desc + (u % C::kStages) * (C::kTileBytes >> 4);
+        auto qk = [&](Place u, bool pass) {
+          const uint64_t b = k_desc + (C::slot_at(u.slot) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
+          for (int kk = 0; kk < DK / 16; ++kk) {
             // handed on a little early: the other's first product follows without a gap
-            if (kk == D / 32 && pass) ptx::mbar_arrive(turn + (g ^ 1));
+            if (kk == DK / 32 && pass) ptx::mbar_arrive(turn + (g ^ 1));
             const uint32_t step = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
             ptx::tc_mma_f16(s_acc, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
           }
           ptx::tc_commit(s_full + g);
         };
-        auto pv = [&](uint32_t u, bool first) {
-          const uint64_t b = v_desc + (u % C::kStages) * (C::kTileBytes >> 4);
+        auto pv = [&](Place u, bool first) {
+          const uint64_t b = v_desc + (C::slot_at(u.slot) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
             ptx::tc_mma_f16_ts(o_acc, s_acc + kPCol + kk * 8, b + kk * (2048 >> 4), idesc_o,
@@ -816,20 +889,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
             const int n0 = TWO && g == 0 ? sg->n0 : n;
             auto mine = [&](int j) { return TWO ? j < n0 : (j & 1) == g; };
             const int last = TWO ? n0 - 1 : n - 1 - ((n - 1 - g) & 1);  // the group's last tile (< 0: none)
-            auto score = [&](int j, uint32_t u, bool pass) {
+            auto score = [&](int j, Place u, bool pass) {
               if (mine(j)) {
                 qk(u, pass);
                 if (j == last) ptx::tc_commit(q_empty);
-                ptx::tc_commit(empty + u % C::kStages);
+                ptx::tc_commit(empty + u.slot);
               } else {
-                ptx::mbar_arrive(empty + u % C::kStages);
+                ptx::mbar_arrive(empty + u.slot);
                 if (pass) ptx::mbar_arrive(turn + (g ^ 1));
               }
             };
             if (!(ok = wait_bar(q_full, q_uses & 1, misc))) break;
             if (last < 0) ptx::mbar_arrive(q_empty);
             for (int j = 0; j < min(n, C::kAhead); ++j) {
-              const uint32_t u = use + k_use<C::kAhead>(j);
+              const Place u = C::k_place(use, j);
               if (!(ok = landed(u))) break;
               ptx::tc_fence_after();
               score(j, u, false);
@@ -839,10 +912,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
             ++q_uses;
             for (int j = 0; j < n; ++j) {
               const int jk = j + C::kAhead;
-              const uint32_t uk = use + k_use<C::kAhead>(jk), uv = use + v_use<C::kAhead>(j, n);
+              const Place uk = C::k_place(use, jk), uv = C::v_place(use, j, n);
               if (jk < n && !(ok = landed(uk))) break;
               if (!(ok = landed(uv))) break;
-              const uint32_t slot = uv % C::kStages;
+              const uint32_t slot = uv.slot;
               const bool masked = !no_cleaning && tile_masked(sg, kt0 + j);
               if (mine(j)) {
                 if (masked && !(ok = wait_bar(clean + slot, (clean_par >> slot) & 1, misc))) break;
@@ -885,20 +958,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       for (int i = 0; ok && (sg = segment(i)) != nullptr && sg->n >= 0; ++i) {
         const int n = sg->n, kt0 = sg->kt0;
         for (int j = no_cleaning ? n : max(0, sg->all / kTileKeys - kt0); j < n; ++j) {
-          const uint32_t u = use + v_use<C::kAhead>(j, n);
-          const uint32_t slot = u % C::kStages;
+          const Place u = C::v_place(use, j, n);
+          const uint32_t slot = u.slot;
           // The producer says when it has begun to fill the slot with this tile: the slot's
           // full barrier is then in this tile's phase, not one of the same parity before.
           ok = __all_sync(0xffffffffu, wait_bar(dirty + slot, (dirty_par >> slot) & 1, misc) &&
-                                           wait_bar(full + slot, (u / C::kStages) & 1, misc));
+                                           wait_bar(full + slot, u.par, misc));
           dirty_par ^= 1u << slot;
           if (!ok) break;
-          uint8_t* v = smem + C::kOffRing + slot * C::kTileBytes;
+          uint8_t* v = smem + C::kOffRing + C::slot_at(slot);
           // Keys before `seen` are seen by every row and stay as they are; keys from `live` on by none.
           const int base = (kt0 + j) * kTileKeys, live = sg->end - base, seen = max(0, sg->all - base);
           bool bad = false;
           // 16 bytes per lane; block h holds columns [64 h, 64 h + 64) of all keys, 128 bytes a key
-          for (int h = 0; h < C::kBlocks; ++h) {
+          for (int h = 0; h < C::kVBlocks; ++h) {
             uint4* block = reinterpret_cast<uint4*>(v + h * C::kHalf);
             const int first = seen * 8, checked = min(live, kTileKeys) * 8;
             // eight pieces at a time are read and tested together; they are all but always as they should be
@@ -952,7 +1025,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     const int row = threadIdx.x & 127;       // row of the tile
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + g * kTileKeys;
-    const uint32_t o_col = tmem + lane_base + 256 + g * D;
+    const uint32_t o_col = tmem + lane_base + 256 + g * DV;
     const int tok_in = row / p.G, head_in = row - tok_in * p.G;
     const float c2 = p.scale * kLog2e;
     uint32_t s_uses = 0, finals = 0, tile = 0;
@@ -1037,7 +1110,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
             l2[0] = ptx::fma_f32x2(l2[0], ff, 0);
             l2[1] = ptx::fma_f32x2(l2[1], ff, 0);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < DV / 16; ++c) {
               uint32_t o[16];
               ptx::tc_ld_32x32b_x16(o_col + 16 * c, o);
               ptx::tc_wait_ld();
@@ -1113,15 +1186,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           out_at[r] = __shfl_sync(0xffffffffu, own, (lane & 28) + r);
-          if (out_at[r] >= 0) out_at[r] += (TWO ? 0 : g * (D / 2)) + 8 * (lane & 3);
+          if (out_at[r] >= 0) out_at[r] += (TWO ? 0 : g * (DV / 2)) + 8 * (lane & 3);
         }
       }
       const int prow = TWO ? g * kTileRows + row : row;
-      float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slot_rows) * (D + 2);
+      float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slot_rows) * (DV + 2);
       // columns of this thread: all (two), or the group's half (one)
-      constexpr int kCols = TWO ? D : D / 2;
+      constexpr int kCols = TWO ? DV : DV / 2;
       const int col0 = TWO ? 0 : g * kCols;
-      const uint32_t oa = tmem + lane_base + 256 + (TWO ? g * D : 0) + col0, ob = tmem + lane_base + 256 + D + col0;
+      const uint32_t oa = tmem + lane_base + 256 + (TWO ? g * DV : 0) + col0, ob = tmem + lane_base + 256 + DV + col0;
 #pragma unroll 1
       for (int c = 0; live && c < kCols / 32; ++c) {
         uint32_t o[32];
@@ -1153,7 +1226,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + int64_t(sg->hk) * p.v_hs + col0 + 32 * c;
           for (int j = j0; j < j1; ++j) {
             if (!attn_sees(p, sg->sq, i, j)) continue;
-            const uint32_t* e = reinterpret_cast<const uint32_t*>(v + (int64_t(sg->sq.k0) + j) * p.v_ts);
+            int64_t at = (int64_t(sg->sq.k0) + j) * p.v_ts;
+            if (PAGED) {
+              bool none_such = false;
+              const int page = attn_page(p, sg->sq.k0, j, &none_such);
+              if (none_such) continue;
+              at = int64_t(page) * p.v_ps + (j % p.page_size) * p.v_ts;
+            }
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(v + at);
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const uint32_t u = __ldg(e + x);
@@ -1188,7 +1268,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int to = (prow & ~3) + r;
-              if (to < slot_rows) *reinterpret_cast<uint4*>(dst + size_t(to) * D + 16 * h) = u[r];
+              if (to < slot_rows) *reinterpret_cast<uint4*>(dst + size_t(to) * DV + 16 * h) = u[r];
             }
           }
         }
@@ -1198,8 +1278,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           if (valid && p.lse)
             p.lse[grow_row * p.Hq + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
         } else if (prow < slot_rows) {
-          pslot[size_t(slot_rows) * D + 2 * prow] = m;
-          pslot[size_t(slot_rows) * D + 2 * prow + 1] = l;
+          pslot[size_t(slot_rows) * DV + 2 * prow] = m;
+          pslot[size_t(slot_rows) * DV + 2 * prow + 1] = l;
         }
       }
       if (n_all > 0) {
@@ -1218,6 +1298,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   __syncwarp();
   __syncthreads();
   if (threadIdx.x == 0 && misc->abort) record_error(hdr, KPOOL_ERR_DEVICE_TIMEOUT);
+  if (PAGED && threadIdx.x == 0 && misc->bad_page) record_error(hdr, KPOOL_ERR_INVALID_ARG);
   if (warp == 9) {
     __syncwarp();
     ptx::tc_fence_after();
@@ -1364,22 +1445,31 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D, Form F>
+template <int DK, int DV, Form F>
 cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
-  using C = Cfg<D, F>;
+  using C = Cfg<DK, DV, F>;
   constexpr bool GATHER = F == kGather;
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int tt = GATHER ? 1 : kTileRows / p.G, ttb = C::kQTiles * tt;
-  CUtensorMap tq, tk, tv;
-  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), D, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
+  CUtensorMap tq, tk, tv, tr;
+  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), DK, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
     return cudaErrorInvalidValue;
-  if (GATHER) {
-    tk = tv = tq;  // (not used: keys and values come by plain copies)
-  } else if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), D, p.k_ts, p.k_hs, kTileKeys, 1) ||
-             !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), D, p.v_ts, p.v_hs, kTileKeys, 1)) {
-    return cudaErrorInvalidValue;
+  tk = tv = tr = tq;  // (gathered: not used, keys and values come by plain copies)
+  if (C::PAGED) {
+    const uint32_t rows = uint32_t(piece_rows(p.page_size));
+    if (!make_tmap_bf16_pages(&tk, p.k, uint64_t(p.num_pages), uint64_t(p.page_size), uint64_t(p.Hkv), DK, p.k_ps, p.k_ts,
+                              p.k_hs, rows) ||
+        !make_tmap_bf16_pages(&tv, p.v, uint64_t(p.num_pages), uint64_t(p.page_size), uint64_t(p.Hkv), DV, p.v_ps, p.v_ts,
+                              p.v_hs, rows))
+      return cudaErrorInvalidValue;
+  } else if (!GATHER) {
+    if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), DV, p.k_ts, p.k_hs, kTileKeys, 1) ||
+        !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), DV, p.v_ts, p.v_hs, kTileKeys, 1))
+      return cudaErrorInvalidValue;
+    if (C::SHARED && !make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, kTileKeys, 1))
+      return cudaErrorInvalidValue;
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
@@ -1406,11 +1496,11 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
-  auto kernel = attn_tc_kernel<D, F>;
+  auto kernel = attn_tc_kernel<DK, DV, F>;
   static std::atomic<uint64_t> ready{0};
   e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), C::kSmem, &ready);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
+  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, tr, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
                                                   joins, hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || small || p.list || grid < 2) return e;
@@ -1426,7 +1516,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<D, true> : attn_join_kernel<D, false>, p, tt,
+  e = cudaLaunchKernelEx(&cfg, split ? attn_join_kernel<DV, true> : attn_join_kernel<DV, false>, p, tt,
                          static_cast<const JoinItem*>(joins),
                          static_cast<const float*>(part), slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1436,6 +1526,10 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
 
 bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim) {
   return dtype == KPOOL_BF16 && (head_dim == 64 || head_dim == 128);
+}
+
+bool attn_tc_shared_supported(kpool_dtype dtype, int32_t own, int32_t shared, int32_t value) {
+  return dtype == KPOOL_BF16 && own == 128 && shared == 64 && value == 128;
 }
 
 bool attn_gather_supported(int64_t k_ts, int64_t v_ts) {
@@ -1466,9 +1560,9 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
       g.dense = ctl;
       g.list = list;
     }
-    return p.D == 64 ? launch<64, kGather>(g, ws, stream) : launch<128, kGather>(g, ws, stream);
+    return p.D == 64 ? launch<64, 64, kGather>(g, ws, stream) : launch<128, 128, kGather>(g, ws, stream);
   }
-  if (p.dense) return p.D == 64 ? launch<64, kDense>(p, ws, stream) : launch<128, kDense>(p, ws, stream);
+  if (p.dense) return p.D == 64 ? launch<64, 64, kDense>(p, ws, stream) : launch<128, 128, kDense>(p, ws, stream);
   // Two row tiles per CTA read K and V half as often, but want sequences that fill them; the lengths are on the
   // device, so the call's mean decides (one / two row tiles, us, 32 / 8 heads of 128, 32 tokens a row tile):
   //  - like sequences: 8 x 30 over 8,000 keys 64 / 71, 8 x 33 85 / 72, 8 x 64 90 / 77, 4 x 200 over 6,000 91 / 100;
@@ -1478,8 +1572,13 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
   //    8,192 316 / 404, of 512 rows 221 / 273; 16 over 8,000 and a prompt of 2,048 129 / 147; 8 trees of 1 to 64
   //    nodes 98 / 97.
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
-  if (p.D == 64) return two ? launch<64, kTwo>(p, ws, stream) : launch<64, kOne>(p, ws, stream);
-  return two ? launch<128, kTwo>(p, ws, stream) : launch<128, kOne>(p, ws, stream);
+  if (p.kr) return two ? launch<192, 128, kTwo>(p, ws, stream) : launch<192, 128, kOne>(p, ws, stream);
+  if (p.table) {
+    if (p.D == 64) return two ? launch<64, 64, kPagedTwo>(p, ws, stream) : launch<64, 64, kPagedOne>(p, ws, stream);
+    return two ? launch<128, 128, kPagedTwo>(p, ws, stream) : launch<128, 128, kPagedOne>(p, ws, stream);
+  }
+  if (p.D == 64) return two ? launch<64, 64, kTwo>(p, ws, stream) : launch<64, 64, kOne>(p, ws, stream);
+  return two ? launch<128, 128, kTwo>(p, ws, stream) : launch<128, 128, kOne>(p, ws, stream);
 }
 
 }  // namespace kpool

@@ -197,6 +197,12 @@ bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint
 bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t dim,
                           int64_t token_stride, int64_t head_stride, uint32_t box_tokens, uint32_t box_heads);
 
+// TMA descriptor of a [pages, page_size, heads, dim] bf16 tensor, strides as above, read in boxes of 64 channels of
+// box_tokens tokens of one head and page.
+bool make_tmap_bf16_pages(CUtensorMap* map, const void* base, uint64_t pages, uint64_t page_size, uint64_t heads,
+                          uint64_t dim, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                          uint32_t box_tokens);
+
 // Remembers a failing CUDA call of this thread for kpool_last_cuda_error; true on success.
 bool note_cuda_error(cudaError_t e);
 

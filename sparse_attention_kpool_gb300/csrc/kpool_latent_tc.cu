@@ -1,0 +1,812 @@
+// kpool_latent_tc.cu -- attention over latent vectors on the 5th-generation tensor cores: bf16, 512 + 64
+// channels (the latent, then its rotated part), over a cache in pages, whole or by token ids.
+//
+// Rows. The heads of one query row share every token, and a token is key and value at once: a tile
+// of 64 tokens is copied once into shared memory and feeds both products. Up to 64 heads a CTA:
+//   S [64 heads x 64 tokens] = Q C^T         36 steps of 16 channels, Q and C from shared memory;
+//   O^T [512 channels x heads] += C^T P^T    four blocks of 128 channels, C as the A operand.
+// The second product is transposed because 64 heads x 512 fp32 channels would fill tensor memory with rows
+// to spare in its lanes only; as 4 x (128 lanes x heads columns) they take 256 of 512 columns, beside two
+// buffers of scores. More than 64 heads are split evenly over CTAs side by side that walk
+// the same tokens at the same time, so that the second reads what the first brought into L2.
+//
+// Roles (10 warps): warps 0-3 softmax, four threads to a head's 64 scores (the layout in which a 16-row
+// accumulator is read); warps 4-7 copy tokens, 16 bytes a lane (cp.async), whole rows of 1,152 bytes wherever
+// the page table puts them; warp 8 issues the MMAs and owns tensor memory; warp 9 hands out segments and loads Q.
+// The scores of tile j + 1 are issued before the second product of tile j, which waits for its softmax.
+//
+// What bounds it. A tile is 74 KB, at the measured copy rate and 152 SMs 3,100 cycles. The tensor core
+// reads operands from shared memory at about 90 bytes a cycle: 36 x 4 KB and 16 x 6 KB are 2,700 cycles at 64 heads
+// (1,600 + 800 at 16). Two tiles in shared memory are what fits beside 64 heads of Q.
+//
+// Masked places: tokens that are not seen are written as zeros (no infinity meets a weight of zero) and
+// score -inf. P is rounded to bf16 (half a step is 2^-8 of a weight) because the second product takes
+// bf16; the row sum adds the weights before that rounding, in fp32. O is rescaled only when a maximum has
+// grown by more than 8 in the exponent, as in kpool_attn_tc.cu.
+//
+// Work. A run per CTA (per group of CTAs, above 64 heads) of about equally many tiles, found by every CTA itself
+// from the lengths on the device; unfinished rows go to the workspace as (m, l, O) and a second kernel joins
+// them in the order of the runs, so results repeat bit for bit.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "kpool_latent.cuh"
+#include "kpool_ptx.cuh"
+
+namespace kpool {
+namespace {
+
+constexpr int kLatent = 512, kRotary = 64, kDim = kLatent + kRotary;
+constexpr int kKeys = 64;                    // tokens of a tile
+constexpr int kHeads = 64;                   // MMA rows of the first product
+constexpr int kBlock = kKeys * 128;          // bytes of 64 channels of a tile, of 64 heads of Q
+constexpr int kBlocks = kDim / 64;
+constexpr int kTileBytes = kBlocks * kBlock;
+constexpr int kStages = 2;
+constexpr int kThreads = 320;
+constexpr int kSegRing = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;                // growth of the maximum (in powers of two) that O is not rescaled for
+constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are microseconds
+
+// Shared memory: Q, the tiles, P, then
+constexpr int kOffTiles = kTileBytes;
+constexpr int kOffP = kOffTiles + kStages * kTileBytes;
+constexpr int kOffFactor = kOffP + kBlock;               // [64] fp32: factors of O's columns
+constexpr int kOffSeg = kOffFactor + kHeads * 4;
+constexpr int kOffBits = kOffSeg + 48 * kSegRing;        // [kStages] x 64 bits: tokens of a tile that are seen
+constexpr int kOffBar = kOffBits + 8 * kStages;
+// full[2] empty[2] q_full q_empty s_full[2] p_ready p_empty o_final o_free done seg_full[4] seg_empty[4]
+constexpr int kNumBars = 2 * kStages + 9 + 2 * kSegRing;
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+constexpr int kSmem = kOffMisc + 64;
+static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
+static_assert(kOffSeg % 16 == 0 && kOffBits % 8 == 0 && kOffBar % 8 == 0 && kOffMisc % 8 == 0, "aligned accesses");
+
+struct Misc {
+  int64_t base;      // first position of row r
+  int64_t lo, hi;    // positions of this run
+  int64_t total;
+  int32_t runs;      // runs that have tiles
+  int32_t row;
+  uint32_t tmem;
+  volatile int32_t abort;
+  volatile int32_t bad_page;
+};
+static_assert(sizeof(Misc) <= 64, "Misc fits its space");
+
+struct Seg {
+  int32_t row, seq, keys;  // query row, its sequence and the keys that one holds
+  int32_t end;             // places to walk
+  int32_t kt0, n;          // first tile here and their number (0: the row sees nothing; -1: the work is done)
+  int8_t whole;            // no other run has tiles of this row
+  int8_t slot;             // partial slot of the CTA: 0 when an earlier run began the row, else 1
+};
+static_assert(sizeof(Seg) <= 48, "Seg fits its space");
+
+// Beginning and finishing a row (Q, first product, epilogue) takes about as long as this many tiles; it is counted
+// when runs are cut, as positions before the row's first tile.
+constexpr int kRowCost = 2;
+// A run has at least this many positions.
+constexpr int kMinRun = 3;
+constexpr int kMaxRuns = 152;
+constexpr int kMaxRunRows = 8192;   // rows whose lengths a CTA adds up itself (whole rows above)
+
+__device__ __forceinline__ int row_tiles(const LatentParams& p, int r) {
+  int b;
+  return max(1, (latent_places(p, latent_seq(p, r, &b)) + kKeys - 1) / kKeys);
+}
+// Over ids every row has the tiles of the list, whatever its sequence holds.
+__device__ __forceinline__ int id_tiles(const LatentParams& p) { return max(1, (p.width + kKeys - 1) / kKeys); }
+
+__host__ __device__ __forceinline__ int64_t run_count(int64_t total, int64_t runs) {
+  const int64_t n = total / kMinRun < runs ? total / kMinRun : runs;
+  return n < 1 ? 1 : n;
+}
+
+// The positions of the runs: run r of n begins at floor(total r / n).
+struct Cuts {
+  int64_t each;
+  uint32_t rest, n;
+  __device__ __forceinline__ Cuts(int64_t total, uint32_t runs)
+      : each(total / runs), rest(uint32_t(total - each * runs)), n(runs) {}
+  __device__ __forceinline__ int64_t lo(uint32_t r) const { return each * r + rest * r / n; }  // rest * r < n * n
+};
+
+// Every thread of the CTA: the positions of run i of up to `runs`, and the row that it begins in. `scratch` holds R
+// 64-bit words (without ids).
+__device__ __forceinline__ void find_run(const LatentParams& p, int64_t* scratch, int i, int runs, Misc* m) {
+  if (latent_listed(p)) {
+    if (threadIdx.x == 0) {
+      const int per = id_tiles(p) + kRowCost;
+      m->total = int64_t(p.R) * per;
+      m->runs = int(run_count(m->total, runs));
+      const Cuts cuts(m->total, uint32_t(m->runs));
+      m->lo = i < m->runs ? cuts.lo(i) : m->total;
+      m->hi = i < m->runs ? cuts.lo(i + 1) : m->total;
+      m->row = int(m->lo / per);
+      m->base = int64_t(m->row) * per;
+    }
+    __syncthreads();
+    return;
+  }
+  for (int r = threadIdx.x; r < p.R; r += kThreads) scratch[r] = row_tiles(p, r) + kRowCost;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t sum = 0;
+    for (int r = lane; r < p.R; r += 32) sum += scratch[r];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const int64_t n = run_count(sum, runs);
+    const Cuts cuts(sum, uint32_t(n));
+    const int64_t lo = i < n ? cuts.lo(i) : sum, hi = i < n ? cuts.lo(i + 1) : sum;
+    int64_t run = 0;
+    bool found = false;
+    for (int r0 = 0; r0 < p.R && !found; r0 += 32) {
+      const int64_t own = r0 + lane < p.R ? scratch[r0 + lane] : 0;
+      int64_t inc = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      const bool mine = lo < run + inc && lo >= run + inc - own;
+      if (mine) {
+        m->row = r0 + lane;
+        m->base = run + inc - own;
+      }
+      found = __any_sync(0xffffffffu, mine);
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      m->lo = lo;
+      m->hi = found ? hi : lo;
+      m->total = sum;
+      m->runs = int(n);
+    }
+  }
+  __syncthreads();
+}
+
+// Rows of a partial result of `per` heads: their 16-byte words stay aligned.
+__host__ __device__ __forceinline__ int part_rows(int per) { return (per + 15) & ~15; }
+
+// What the join of the row that the border before a run cuts needs; runs = 0: nothing to join here.
+struct JoinItem {
+  int64_t item;       // position of the row's first tile
+  int64_t each;       // Cuts of the call
+  uint32_t rest;
+  int32_t tiles;
+  int32_t runs;
+  int32_t row;
+};
+static_assert(sizeof(JoinItem) == 32, "join items are laid out in the workspace");
+
+// The segments of a run: whole rows, `step` apart, or the rows of its positions.
+struct SegIter {
+  int64_t pos, hi, item;   // item: first position of the present row
+  int row, c;              // c: its tiles
+  __device__ __forceinline__ void start(const LatentParams& p, const Misc* m) {
+    pos = m->lo;
+    hi = m->hi;
+    row = m->row;
+    item = m->base;
+    c = pos < hi ? tiles(p) : 0;
+  }
+  __device__ __forceinline__ int tiles(const LatentParams& p) const { return latent_listed(p) ? id_tiles(p) : row_tiles(p, row); }
+  __device__ __forceinline__ bool next(const LatentParams& p, Seg* s) {
+    if (pos >= hi) return false;
+    if (pos == item + kRowCost + c) {
+      item = pos;
+      ++row;
+      c = tiles(p);
+    }
+    const int64_t tile0 = item + kRowCost;
+    if (hi <= tile0) return false;  // (only as the run's last row)
+    s->row = row;
+    s->kt0 = int(max(pos - tile0, int64_t(0)));
+    s->n = int(min(int64_t(c), hi - tile0)) - s->kt0;
+    s->whole = s->n == c;
+    s->slot = s->kt0 > 0 ? 0 : 1;
+    pos = tile0 + s->kt0 + s->n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (int i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (m->abort) return false;
+    if ((i & 63) == 0 && ptx::globaltimer_ns() - t0 > kMaxWaitNs) {
+      m->abort = 1;
+      return false;
+    }
+  }
+}
+
+// Barrier of the softmax warps that tells all of them whether one of them says so.
+__device__ __forceinline__ bool group_or(bool flag) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(flag ? 1u : 0u)
+      : "memory");
+  return out != 0;
+}
+
+// per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ LatentParams p, int per,
+                     int groups, int direct, float* part, JoinItem* joins, WorkspaceHeader* hdr) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;   // [2]
+  uint64_t* p_ready = q_full + 4;
+  uint64_t* p_empty = q_full + 5;
+  uint64_t* o_final = q_full + 6;
+  uint64_t* o_free = q_full + 7;
+  uint64_t* done = q_full + 8;
+  uint64_t* seg_full = q_full + 9;             // [kSegRing]
+  uint64_t* seg_empty = seg_full + kSegRing;   // [kSegRing]
+  auto seg_at = [&](int i) { return reinterpret_cast<Seg*>(smem + kOffSeg + 48 * (i % kSegRing)); };
+  float* factor = reinterpret_cast<float*>(smem + kOffFactor);
+  Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = blockIdx.x / groups, group = blockIdx.x - run * groups, runs = gridDim.x / groups;
+  const int head0 = group * per, heads = min(per, p.H - head0), cols = (heads + 15) & ~15;
+  const int slots = part_rows(per);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
+  if (blockIdx.x == 0 && threadIdx.x == 0) hdr->error = KPOOL_OK;
+  if (!direct) {
+    find_run(p, reinterpret_cast<int64_t*>(smem), run, runs, misc);
+    ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(full + i, 33 * 4);
+      ptx::mbar_init(empty + i, 1);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(s_full + 1, 1);
+    ptx::mbar_init(p_ready, 4);
+    ptx::mbar_init(p_empty, 1);
+    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(o_free, 4);
+    ptx::mbar_init(done, 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      ptx::mbar_init(seg_full + i, 1);
+      ptx::mbar_init(seg_empty + i, 9);
+    }
+    ptx::fence_mbar_init();
+    misc->abort = 0;
+    misc->bad_page = 0;
+  }
+  if (warp == 8) {
+    ptx::tmem_alloc(&misc->tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  auto segment = [&](int i) -> const Seg* {
+    return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? seg_at(i) : nullptr;
+  };
+
+  if (warp == 9) {  // ----------------------------------------------------- segments and Q
+    if (lane == 0) {
+      SegIter it;
+      if (!direct) it.start(p, misc);
+      uint32_t q_loads = 0;
+      Seg s{};
+      for (int i = 0;; ++i) {
+        bool more;
+        if (direct) {
+          s.row = run + i * runs;
+          more = s.row < p.R;
+          if (more) {
+            s.kt0 = 0;
+            s.n = latent_listed(p) ? id_tiles(p) : row_tiles(p, s.row);
+            s.whole = 1;
+            s.slot = 0;
+          }
+        } else {
+          more = it.next(p, &s);
+        }
+        if (i == 0 && !direct && group == 0) {
+          // The join of a cut row is left to the first run that begins inside it.
+          JoinItem j{};
+          if (more && s.kt0 > 0) {
+            const Cuts cuts(misc->total, uint32_t(misc->runs));
+            j.item = it.item + kRowCost;
+            bool own = true;
+            const int64_t pos = cuts.lo(run);
+            for (int b = run - 1; own && b > 0 && cuts.lo(b) > j.item; --b) own = cuts.lo(b) == pos;
+            j.each = cuts.each;
+            j.rest = cuts.rest;
+            j.tiles = it.c;
+            j.runs = own ? misc->runs : 0;
+            j.row = s.row;
+          }
+          joins[run] = j;
+        }
+        if (more) {
+          s.keys = latent_seq(p, s.row, &s.seq);
+          s.end = latent_places(p, s.keys);
+          if (s.end == 0) s.n = 0;
+        } else {
+          s.n = -1;
+        }
+        if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
+        *seg_at(i) = s;
+        ptx::mbar_arrive(seg_full + i % kSegRing);
+        if (!more) break;
+        if (s.n == 0) continue;
+        if (q_loads > 0 && !wait_bar(q_empty, (q_loads - 1) & 1, misc)) break;
+        ptx::mbar_arrive_expect_tx(q_full, kTileBytes);
+        ++q_loads;
+#pragma unroll
+        for (int h = 0; h < kBlocks; ++h)
+          ptx::tma_load_3d(smem + h * kBlock, &tm_q, q_full, 64 * h, head0, s.row);
+      }
+      if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
+    }
+    __syncwarp();
+    if (blockIdx.x == 0) latent_check(p, hdr);
+  } else if (warp == 8) {  // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t q_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem));
+      const uint64_t c_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffTiles));
+      const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + kOffTiles), kBlock);
+      const uint64_t p_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffP));
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kHeads, kKeys);
+      const uint32_t idesc_o = ptx::idesc_bf16_f32_am(128, cols);
+      uint32_t tile = 0, q_uses = 0;  // tiles before this segment; segments with tiles
+      bool ok = true;
+      const Seg* s;
+      auto landed = [&](uint32_t u) {
+        const bool r = wait_bar(full + u % kStages, (u / kStages) & 1, misc);
+        ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
+        return r;
+      };
+      auto score = [&](uint32_t u) {
+        const uint64_t b = c_desc + (u % kStages) * (kTileBytes >> 4);
+        const uint32_t acc = tmem + 256 + 64 * (u & 1);
+#pragma unroll
+        for (int kk = 0; kk < kDim / 16; ++kk) {
+          const uint32_t step = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
+          ptx::tc_mma_f16(acc, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        ptx::tc_commit(s_full + (u & 1));
+      };
+      for (int i = 0; ok && (s = segment(i)) != nullptr && s->n >= 0; ++i) {
+        const int n = s->n;
+        if (n > 0) {
+          if (!(ok = wait_bar(q_full, q_uses & 1, misc) && landed(tile))) break;
+          ptx::tc_fence_after();
+          score(tile);
+          for (int j = 0; j < n; ++j) {
+            const uint32_t u = tile + j;
+            if (j + 1 < n) {
+              if (!(ok = landed(u + 1))) break;
+              ptx::tc_fence_after();
+              score(u + 1);
+            }
+            if (j == max(n - 2, 0)) ptx::tc_commit(q_empty);  // the segment's last scores are issued
+            if (!(ok = wait_bar(p_ready, u & 1, misc))) break;
+            if (j == 0 && q_uses > 0 && !(ok = wait_bar(o_free, (q_uses - 1) & 1, misc))) break;
+            ptx::tc_fence_after();
+            const uint64_t a = v_desc + (u % kStages) * (kTileBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < kLatent / 128; ++c)
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                ptx::tc_mma_f16(tmem + 64 * c, a + ((2 * c * kBlock + kk * 2048) >> 4), p_desc + (kk * 32 >> 4), idesc_o,
+                                (kk > 0 || j > 0) ? 1u : 0u);
+            ptx::tc_commit(empty + u % kStages);
+            ptx::tc_commit(p_empty);
+          }
+          if (!ok) break;
+          ptx::tc_commit(o_final);
+          tile += n;
+          ++q_uses;
+        }
+        ptx::mbar_arrive(seg_empty + i % kSegRing);
+      }
+      ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
+      ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
+    }
+  } else if (warp >= 4) {  // ------------------------------------------------ copying warps
+    // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each.
+    const int w = warp - 4, c = lane & 7, sub = lane >> 3;
+    const char* base = static_cast<const char*>(p.cache) + c * 16;
+    const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * 16 + sub) * 128;
+    uint32_t u = 0;
+    bool ok = true, bad = false;
+    const Seg* s;
+    for (int i = 0;; ++i) {
+      s = segment(i);
+      if (!__all_sync(0xffffffffu, s != nullptr) || s->n < 0) break;
+      const int n = s->n;
+      auto token = [&](int j) {
+        const int place = (s->kt0 + j) * kKeys + w * 16 + lane;
+        return lane < 16 && place < s->end ? latent_token(p, s->row, s->seq, s->keys, place, &bad) : int64_t(-1);
+      };
+      int64_t next = n > 0 ? token(0) : -1;
+      for (int j = 0; j < n; ++j, ++u) {
+        const int64_t at = next;
+        const uint32_t st = u % kStages;
+        if (u >= kStages) ok = __all_sync(0xffffffffu, wait_bar(empty + st, (u / kStages - 1) & 1, misc));
+        if (!ok) break;
+        __syncwarp();
+        const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
+        if (lane == 0) reinterpret_cast<uint16_t*>(smem + kOffBits)[4 * st + w] = uint16_t(bits);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t t = __shfl_sync(0xffffffffu, at, 4 * q + sub);
+          const char* from = base + (t >= 0 ? t : 0) * 2;
+          const uint32_t bytes = t >= 0 ? 16u : 0u;
+          // the row's number modulo eight permutes its 16-byte pieces
+          const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ (((q & 1) * 4 + sub) & 7)) << 4);
+#pragma unroll
+          for (int h = 0; h < kBlocks; ++h) ptx::cp_async_16(dst + h * kBlock, from + h * 128, bytes);
+        }
+        ptx::cp_async_arrive(full + st);
+        if (lane == 0) ptx::mbar_arrive(full + st);
+        if (j + 1 < n) next = token(j + 1);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
+    }
+    if (bad) misc->bad_page = 1;
+    ptx::cp_async_wait_all();  // every copy has landed before the CTA exits
+  } else {  // ---------------------------------------------------------------- softmax
+    // Lane 4 g + t has the heads 16 warp + g and 8 further, tokens 8 x + 2 t and the next of every eight.
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    const float c2 = p.scale * kLog2e;
+    const int row0 = warp * 16 + g;
+    uint8_t* p_row = smem + kOffP + row0 * 128 + t * 4;
+    uint32_t u = 0, finals = 0;
+    bool ok = true;
+    for (int is = 0;; ++is) {
+      const Seg* sg = segment(is);
+      if (group_or(sg == nullptr) || sg->n < 0) break;
+      const int n = sg->n;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < n; ++j, ++u) {
+        ok = wait_bar(s_full + (u & 1), (u >> 1) & 1, misc);
+        if (group_or(!ok)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        uint32_t s[32];
+        ptx::tc_ld_16x256b_x8(tmem + lanes + 256 + 64 * (u & 1), s);
+        const uint64_t bits = *reinterpret_cast<const volatile uint64_t*>(smem + kOffBits + 8 * (u % kStages));
+        ptx::tc_wait_ld();
+        ptx::tc_reg_fence(s);
+        if (bits != ~uint64_t(0)) {
+          const uint64_t mine = bits >> (2 * t);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (!((mine >> (8 * x + y)) & 1)) s[4 * x + y] = s[4 * x + 2 + y] = 0xFF800000u;  // -inf
+        }
+        float mt[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mt[h] = __uint_as_float(s[2 * h]);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            mt[h] = fmaxf(fmaxf(mt[h], __uint_as_float(s[4 * x + 2 * h])), __uint_as_float(s[4 * x + 2 * h + 1]));
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
+          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+        }
+        bool grow[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) grow[h] = mt[h] > m[h] && (mt[h] - m[h]) * c2 > kLazy;
+        const bool rescale = group_or(grow[0] || grow[1]);
+        // the second product of the tile before is done: O is at rest and P may be written
+        if (u > 0) ok = wait_bar(p_empty, (u - 1) & 1, misc);
+        if (rescale) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = grow[h] ? ptx::exp2_approx((m[h] - mt[h]) * c2) : 1.0f;
+            if (grow[h]) m[h] = mt[h];
+            l[h] *= f;
+            if (t == 0) factor[row0 + 8 * h] = f;
+          }
+          if (j > 0) {
+            if (group_or(!ok)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4 * cols / 16; ++x) {
+              const int c = x / (cols / 16), col = (x - c * (cols / 16)) * 16;
+              const uint32_t at = tmem + lanes + 64 * c + col;
+              uint32_t o[16];
+              ptx::tc_ld_32x32b_x16(at, o);
+              ptx::tc_wait_ld();
+              ptx::tc_reg_fence(o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * factor[col + y]);
+              ptx::tc_st_32x32b_x16(at, o);
+            }
+            ptx::tc_wait_st();
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          misc->abort = 1;
+          ok = false;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float nb = m[h] == -INFINITY ? 0.0f : -m[h] * c2;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb));
+            const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb));
+            l[h] += a + b;
+            *reinterpret_cast<uint32_t*>(p_row + h * 1024 + ((x ^ g) << 4)) = ptx::pack_bf16(a, b);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_ready);
+      }
+      if (group_or(!ok)) break;
+      // ------------------------------------------------------------------------ epilogue
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      }
+      float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slots) * (kLatent + 2);
+      if (t == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int head = row0 + 8 * h;
+          const bool none = m[h] == -INFINITY && l[h] == 0.0f;  // (a NaN score leaves l NaN: not empty)
+          factor[head] = none ? 0.0f : 1.0f / l[h];
+          if (head >= heads) continue;
+          if (sg->whole) {
+            if (p.lse)
+              p.lse[int64_t(sg->row) * p.H + head0 + head] = none ? -INFINITY : (m[h] * c2 + log2f(l[h])) * kLn2;
+          } else {
+            *reinterpret_cast<float2*>(pslot + size_t(slots) * kLatent + 2 * head) = make_float2(m[h], l[h]);
+          }
+        }
+      }
+      if (n > 0) ok = wait_bar(o_final, finals & 1, misc);
+      if (group_or(!ok)) break;  // (and the factors are written)
+      ptx::tc_fence_after();
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(sg->row) * p.o_ts + int64_t(head0) * p.o_hs;
+#pragma unroll 1
+      for (int x = 0; x < 4 * cols / 16; ++x) {
+        const int c = x / (cols / 16), col = (x - c * (cols / 16)) * 16;
+        uint32_t o[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = 0;
+        if (n > 0) {
+          ptx::tc_ld_32x32b_x16(tmem + lanes + 64 * c + col, o);
+          ptx::tc_wait_ld();
+          ptx::tc_reg_fence(o);
+        }
+        const int ch = 128 * c + 32 * warp + lane;
+        if (sg->whole) {
+          // neighbouring lanes exchange halves of two heads: each then writes two channels of one head
+#pragma unroll
+          for (int y = 0; y < 16; y += 2) {
+            const float a = __uint_as_float(o[y]) * factor[col + y], b = __uint_as_float(o[y + 1]) * factor[col + y + 1];
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            const int head = col + y + odd;
+            const bool zero = factor[head] == 0.0f;  // (no weight at all, or an infinite sum: zeros either way)
+            const uint32_t v = zero ? 0u : odd ? ptx::pack_bf16(got, b) : ptx::pack_bf16(a, got);
+            if (head < heads) *reinterpret_cast<uint32_t*>(out + head * p.o_hs + (ch & ~1)) = v;
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 16; ++y)
+            if (col + y < heads) pslot[size_t(col + y) * kLatent + ch] = __uint_as_float(o[y]);
+        }
+      }
+      if (n > 0) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(o_free);
+        ++finals;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(seg_empty + is % kSegRing);
+      // (the factors are read by all before the next row writes them: its first tile has a barrier in between)
+    }
+    ptx::tc_fence_before();
+  }
+  // ------------------------------------------------------------------------------ teardown
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && misc->abort) record_error(hdr, KPOOL_ERR_DEVICE_TIMEOUT);
+  if (threadIdx.x == 0 && misc->bad_page) record_error(hdr, KPOOL_ERR_INVALID_ARG);
+  if (warp == 8) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------- join
+//
+// CTA x adds up, in the order of the runs, the partial results of the row that the border before run x + 1 cuts
+// (if that run was the first to begin inside it). kShare warps have one head, each every kShare-th run; a lane
+// holds 16 of the 512 channels.
+template <int kShare>
+__global__ void __launch_bounds__(256)
+    latent_join_kernel(const __grid_constant__ LatentParams p, int per, int groups, const JoinItem* joins,
+                       const float* part) {
+  constexpr int kPer = kLatent / 32, kHeadsCta = 8 / kShare;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
+  const JoinItem it = joins[blockIdx.x + 1];
+  if (it.runs == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int in_cta = warp / kShare, share = warp % kShare;
+  const int head = int(blockIdx.y) * kHeadsCta + in_cta;   // of the call
+  const int group = head / per, h = head - group * per;
+  const bool live = head < p.H;
+  auto run_lo = [&](int r) { return it.each * r + it.rest * uint32_t(r) / uint32_t(it.runs); };
+  int first = blockIdx.x;
+  while (first > 0 && run_lo(first) > it.item) --first;
+  const float c2 = p.scale * kLog2e;
+  const int64_t end = it.item + it.tiles;
+  float acc[kPer], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) acc[y] = 0.0f;
+  // adds a part (o, pm, pl); one without any weight adds nothing, with a NaN among its scores its sum passes on
+  auto add = [&](const float (&o)[kPer], float pm, float pl) {
+    const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
+    const float f = m == -INFINITY ? 1.0f : exp2f((m - base) * c2);
+    const float w = pm == -INFINITY ? 1.0f : exp2f((pm - base) * c2);
+    l = l * f + pl * w;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[y] = acc[y] * f + o[y] * w;
+    m = mn;
+  };
+  const int slots = part_rows(per);
+  const size_t stride = size_t(slots) * (kLatent + 2);
+  for (int r = first + share; live && r < it.runs && run_lo(r) < end; r += kShare) {
+    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
+    if (!(hi > it.item && hi > lo)) continue;
+    const float* s = part + ((size_t(r) * groups + group) * 2 + (lo > it.item ? 0 : 1)) * stride;
+    const float2 ml = *reinterpret_cast<const float2*>(s + size_t(slots) * kLatent + 2 * h);
+    float o[kPer];
+#pragma unroll
+    for (int y = 0; y < kPer; y += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(s + size_t(h) * kLatent + 32 * y + 4 * lane);
+      o[y] = f.x;
+      o[y + 1] = f.y;
+      o[y + 2] = f.z;
+      o[y + 3] = f.w;
+    }
+    add(o, ml.x, ml.y);
+  }
+  if (kShare > 1) {  // the first warp adds the others' parts in their order
+    __shared__ float s_o[8][kLatent];
+    __shared__ float2 s_ml[8];
+#pragma unroll
+    for (int y = 0; y < kPer; y += 4)
+      *reinterpret_cast<float4*>(&s_o[warp][32 * y + 4 * lane]) = make_float4(acc[y], acc[y + 1], acc[y + 2], acc[y + 3]);
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (share != 0) return;
+    for (int x = 1; x < kShare; ++x) {
+      float o[kPer];
+#pragma unroll
+      for (int y = 0; y < kPer; y += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&s_o[warp + x][32 * y + 4 * lane]);
+        o[y] = f.x;
+        o[y + 1] = f.y;
+        o[y + 2] = f.z;
+        o[y + 3] = f.w;
+      }
+      add(o, s_ml[warp + x].x, s_ml[warp + x].y);
+    }
+  }
+  if (!live) return;
+  const bool none = m == -INFINITY && l == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / l;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(it.row) * p.o_ts + head * p.o_hs;
+#pragma unroll
+  for (int y = 0; y < kPer; y += 4) {
+    uint2 v = make_uint2(0, 0);
+    if (!none)
+      v = make_uint2(ptx::pack_bf16(acc[y] * inv, acc[y + 1] * inv), ptx::pack_bf16(acc[y + 2] * inv, acc[y + 3] * inv));
+    *reinterpret_cast<uint2*>(out + 32 * y + 4 * lane) = v;
+  }
+  if (lane == 0 && p.lse) p.lse[int64_t(it.row) * p.H + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+}
+
+// Heads split evenly over CTAs of at most 64, whole sixteens where there are several.
+int head_groups(int32_t heads) { return (heads + kHeads - 1) / kHeads; }
+int heads_per(int32_t heads) {
+  const int groups = head_groups(heads), each = (heads + groups - 1) / groups;
+  return groups == 1 ? heads : (each + 15) & ~15;
+}
+
+}  // namespace
+
+bool latent_tc_supported(kpool_dtype dtype, int32_t latent, int32_t rotary) {
+  return dtype == KPOOL_BF16 && latent == kLatent && rotary == kRotary;
+}
+
+size_t latent_tc_bytes(int32_t heads) {
+  const int groups = head_groups(heads);
+  const size_t runs = groups > kMaxRuns ? 1 : kMaxRuns / groups;
+  return align256(sizeof(JoinItem) * kMaxRuns) +
+         runs * groups * 2 * size_t(part_rows(heads_per(heads))) * (kLatent + 2) * sizeof(float);
+}
+
+cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int per = heads_per(p.H), groups = head_groups(p.H);
+  CUtensorMap tq;
+  if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.H), kDim, p.q_ts, p.q_hs, 1, kHeads))
+    return cudaErrorInvalidValue;
+  if (sms > kMaxRuns) sms = kMaxRuns;
+  int runs = groups > sms ? 1 : sms / groups;
+  // Equal runs of tiles fill the SMs and cost a join (about four tiles' time). Lists of ids are all alike: whole
+  // rows are taken where their rounding up to the runs costs less than that.
+  const bool listed = latent_listed(p);
+  const int64_t nt = listed ? (p.width + kKeys - 1) / kKeys : 0;
+  const bool even = listed && (nt + kRowCost) * ((p.R + runs - 1) / runs) <= p.R * (nt + kRowCost) / runs + 4;
+  const bool direct = even || (!listed && p.R > kMaxRunRows);
+  if (direct && runs > p.R) runs = p.R;
+  if (!direct && listed) runs = int(run_count(int64_t(p.R) * (nt + kRowCost), runs));
+  JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader));
+  float* part = reinterpret_cast<float*>(ws + sizeof(WorkspaceHeader) + align256(sizeof(JoinItem) * kMaxRuns));
+  WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
+  static std::atomic<uint64_t> ready{0};
+  e = allow_dynamic_smem(reinterpret_cast<const void*>(latent_tc_kernel), kSmem, &ready);
+  if (e != cudaSuccess) return e;
+  latent_tc_kernel<<<runs * groups, kThreads, kSmem, stream>>>(tq, p, per, groups, direct ? 1 : 0, part, joins, hdr);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || direct || runs < 2) return e;
+  cudaLaunchConfig_t cfg{};
+  // many runs to a row: a CTA's warps share its heads; else each has its own
+  const bool share = int64_t(p.R) * 4 <= runs;
+  cfg.gridDim = dim3(uint32_t(runs - 1), uint32_t(share ? p.H : (p.H + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<8> : latent_join_kernel<1>, p, per, groups,
+                         static_cast<const JoinItem*>(joins), static_cast<const float*>(part));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kpool

@@ -55,4 +55,18 @@ bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_pages(CUtensorMap* map, const void* base, uint64_t pages, uint64_t page_size, uint64_t heads,
+                          uint64_t dim, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                          uint32_t box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {dim, heads, page_size, pages};
+  const cuuint64_t strides[3] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2, cuuint64_t(page_stride) * 2};
+  const cuuint32_t box[4] = {64, 1, box_tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kpool

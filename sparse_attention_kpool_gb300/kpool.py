@@ -45,7 +45,12 @@ EXPORTED = (
     "kpool_pool_keys_gated", "kpool_select_pooled", "kpool_static_scratch_last_device_error",
     "kpool_balanced_row_split", "kpool_index_scores", "kpool_index_scores_pooled",
     "kpool_attention_workspace_bytes", "kpool_attention_prompt", "kpool_attention_tree", "kpool_attention_selected",
+    "kpool_attention_paged", "kpool_latent_prompt_workspace_bytes", "kpool_attention_latent_prompt",
+    "kpool_latent_workspace_bytes", "kpool_attention_latent", "kpool_rotary", "kpool_rotary_table",
 )
+KPOOL_WHOLE_CACHE = -1
+KPOOL_ROTARY_INTERLEAVED = 1
+KPOOL_ROTARY_INVERSE = 2
 KPOOL_STATIC_SCRATCH_BYTES = 48 << 20
 
 
@@ -72,6 +77,26 @@ class kpool_heads(ctypes.Structure):
 class kpool_attention_shape(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class kpool_pages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class kpool_latent_shape(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("key_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class kpool_rotary_part(ctypes.Structure):
+    _fields_ = [("in_", kpool_heads), ("out", kpool_heads), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("offset", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class kpool_rotary_shape(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -145,6 +170,24 @@ def load() -> ctypes.CDLL:
         lib.kpool_attention_tree.restype = i32
         lib.kpool_attention_selected.argtypes = [HP, HP, HP, P, i32, P, P] + tail
         lib.kpool_attention_selected.restype = i32
+        PP, LP = ctypes.POINTER(kpool_pages), ctypes.POINTER(kpool_latent_shape)
+        tail = [HP, P, P, sz, P, OP]
+        lib.kpool_attention_paged.argtypes = [HP, PP, PP, P, i32, i32, i32, P, P, i32, i64, SP] + tail
+        lib.kpool_attention_paged.restype = i32
+        lib.kpool_latent_prompt_workspace_bytes.argtypes = [i64, i32, LP]
+        lib.kpool_latent_prompt_workspace_bytes.restype = sz
+        lib.kpool_attention_latent_prompt.argtypes = [HP, HP, HP, HP, P, P, i32, i64, i64, LP] + tail
+        lib.kpool_attention_latent_prompt.restype = i32
+        lib.kpool_latent_workspace_bytes.argtypes = [i64, i32, LP]
+        lib.kpool_latent_workspace_bytes.restype = sz
+        lib.kpool_attention_latent.argtypes = [HP, PP, P, i32, i32, i32, P, P, i32, P, i32, i64, LP] + tail
+        lib.kpool_attention_latent.restype = i32
+        RP = ctypes.POINTER(kpool_rotary_part)
+        lib.kpool_rotary.argtypes = [RP, RP, P, P, i64, ctypes.POINTER(kpool_rotary_shape), P]
+        lib.kpool_rotary.restype = i32
+        f64 = ctypes.c_double
+        lib.kpool_rotary_table.argtypes = [i32, f64, f64, f64, f64, f64, P]
+        lib.kpool_rotary_table.restype = i32
         _lib = lib
         return lib
 
@@ -661,6 +704,313 @@ def kpool_attention_selected(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         raise ValueError("row_seq needs one element per row")
     return _attention("kpool_attention_selected", q, k, v, (token_ids, token_ids.shape[1], row_seq, cu_k),
                       cu_k.numel() - 1, scale, out, return_lse, out_lse, workspace, stream, score_kernel)
+
+
+class _ServingArgs(threading.local):
+    """A thread's argument structures of the calls below, filled anew by every call."""
+
+    def __init__(self):
+        heads, pages = ctypes.sizeof(kpool_heads), ctypes.sizeof(kpool_pages)
+        parts = [kpool_heads] * 4 + [kpool_pages] * 2 + [kpool_rotary_part] * 2 + [kpool_attention_shape,
+                                                                                    kpool_latent_shape,
+                                                                                    kpool_rotary_shape]
+        at = [0]
+        for t in parts:
+            at.append(at[-1] + ctypes.sizeof(t))
+        self.buffer = bytearray(at[-1])
+        made = [t.from_buffer(self.buffer, a) for t, a in zip(parts, at)]
+        refs = [ctypes.byref(x) for x in made]
+        self.heads, self.pages, self.parts = refs[:4], refs[4:6], refs[6:8]
+        self.attention, self.latent, self.rotary = refs[8:]
+        self.latent_shape, self.attention_shape, self.rotary_shape = made[9], made[8], made[10]
+        self.heads_at = at[:4]
+        self.pages_at, self.part_at = at[4:6], at[6:8]
+        self.attention_at, self.latent_at, self.rotary_at = at[8:11]
+        self.pack_heads = struct.Struct("=Qqq").pack_into
+        self.pack_pages = struct.Struct("=Qqqq").pack_into
+        self.pack_part = struct.Struct("=QqqQqqiiii").pack_into
+        self.pack_shape = struct.Struct("=iiii").pack_into       # kpool_attention_shape without scale
+        self.pack_latent = struct.Struct("=iiiii").pack_into     # kpool_latent_shape without scale
+        self.pack_rotary = struct.Struct("=iii").pack_into       # kpool_rotary_shape without magnitude
+        assert heads == 24 and pages == 32
+
+
+_serving_args = _ServingArgs()
+
+
+def _current_device(*tensors) -> int:
+    """The device of all of them, which has to be the current one (the library launches there)."""
+    dev = tensors[0].get_device()  # -1 on the CPU
+    for t in tensors:
+        if t.get_device() != dev:
+            dev = -1
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be CUDA tensors on the current device")
+    return dev
+
+
+def _array(t, dev, dtype=torch.int32):
+    """Pointer of an index array (None: none)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"page tables, lengths, cumulative lengths, token ids, row_seq and positions are {dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors on the current device")
+    return t.data_ptr()
+
+
+def _strides(t):
+    """(token stride, head stride) of a [tokens, heads, dim] tensor; a dimension of one element has none of its own."""
+    n, h, d = t.shape
+    a, b, c = t.stride()
+    if c != 1 and d > 1:
+        raise ValueError("the last dimension of a tensor must be contiguous")
+    if h == 1:
+        b = d
+    return (d if n <= 1 else a), b
+
+
+def _page_strides(t):
+    """(page, token, head stride) of a [pages, page_size, heads, dim] tensor."""
+    n, size, h, d = t.shape
+    a, b, c, e = t.stride()
+    if e != 1 and d > 1:
+        raise ValueError("the last dimension of a tensor must be contiguous")
+    return (d if n <= 1 else a), (d if size == 1 else b), (d if h == 1 else c)
+
+
+def _results(q_rows, heads, dim, q, out, return_lse, out_lse, stream):
+    """out [rows, heads, dim] and out_lse [rows, heads] or None, made here or the caller's."""
+    if out is None:
+        out = _empty((q_rows, heads, dim), q.dtype, q.device, stream)
+    elif out.shape != (q_rows, heads, dim) or out.dtype != q.dtype:
+        raise TypeError("out must have q's dtype and a row of values for every query row and head")
+    if out_lse is None:
+        if return_lse:
+            out_lse = _empty((q_rows, heads), torch.float32, q.device, stream)
+    elif out_lse.dtype != torch.float32 or out_lse.shape != (q_rows, heads):
+        raise TypeError("out_lse must be float32 [rows, q_heads]")
+    return out, out_lse
+
+
+def _finish(name, call, args, out, out_lse, workspace, stream, dev, score_kernel):
+    """The arguments that all attention calls end with, and the call's status."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors on the current device")
+    a = _serving_args
+    ot, oh = _strides(out)
+    a.pack_heads(a.buffer, a.heads_at[3], out.data_ptr(), ot, oh)
+    st = call(*args, a.heads[3], _array(out_lse, dev, torch.float32), workspace.data_ptr(), workspace.nbytes,
+              torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream),
+              None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
+    if st != KPOOL_OK:
+        raise KpoolError(st, name)
+    return out, out_lse
+
+
+def kpool_attention_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                          lengths: torch.Tensor, scale: float, cu_q=None, out=None, return_lse: bool = False,
+                          out_lse=None, workspace=None, stream=None, score_kernel: int = KPOOL_SCORE_AUTO):
+    """Attention over a key/value cache in pages: q [R,Hq,D], k and v [pages, page_size, Hkv, D] (bf16 or fp32, any
+    page, token and head strides), page_table [S, max_pages] and lengths [S] int32. Sequence b's query rows (cu_q
+    [S+1] int32; None: row b alone, a decode step) are the last ones of its lengths[b] keys. Returns (out, lse)
+    as kpool_attention_prompt does; the workspace is new_attention_workspace's."""
+    if q.dim() != 3 or k.dim() != 4 or v.shape != k.shape or q.shape[2] != k.shape[3]:
+        raise ValueError("q is [rows, q_heads, head_dim]; k and v are [pages, page_size, kv_heads, head_dim] alike")
+    dtype = q.dtype
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError("k and v must match q's dtype")
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
+    R, hq, d = q.shape
+    pages, size, hkv, _ = k.shape
+    S = lengths.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != S or (R != S if cu_q is None else cu_q.numel() != S + 1):
+        raise ValueError("page_table is [sequences, pages], lengths [sequences], cu_q [sequences + 1] (or a row each)")
+    out, out_lse = _results(R, hq, d, q, out, return_lse, out_lse, stream)
+    if workspace is None:
+        workspace = _new(lambda: new_attention_workspace(R, S, hq, hkv, d, dtype, q.device), stream, returned=False)
+    dev = _current_device(q, k, v, out)
+    a = _serving_args
+    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
+    a.pack_pages(a.buffer, a.pages_at[0], k.data_ptr(), *_page_strides(k))
+    a.pack_pages(a.buffer, a.pages_at[1], v.data_ptr(), *_page_strides(v))
+    a.pack_shape(a.buffer, a.attention_at, hq, hkv, d, code)
+    a.attention_shape.scale = scale  # (rounded as C does: out of fp32's range it is infinite, and refused)
+    return _finish("kpool_attention_paged", (_lib or load()).kpool_attention_paged,
+                   (a.heads[0], *a.pages, _array(page_table, dev), page_table.shape[1], pages, size,
+                    _array(lengths, dev), _array(cu_q, dev), S, R, a.attention), out, out_lse, workspace, stream, dev,
+                   score_kernel)
+
+
+def _latent_shape(heads, key_dim, rotary_dim, value_dim, dtype, scale=1.0):
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"latent attention takes bfloat16 or float32, got {dtype}")
+    return kpool_latent_shape(heads, key_dim, rotary_dim, value_dim, code, scale)
+
+
+def new_latent_prompt_workspace(q_rows: int, num_seqs: int, heads: int, key_dim: int, rotary_dim: int,
+                                value_dim: int, dtype, device=None) -> torch.Tensor:
+    """Workspace of kpool_attention_latent_prompt with up to these sizes (dtype: the torch dtype of q)."""
+    n = int(load().kpool_latent_prompt_workspace_bytes(q_rows, num_seqs, ctypes.byref(
+        _latent_shape(heads, key_dim, rotary_dim, value_dim, dtype))))
+    if n == 0:
+        raise KpoolError(KPOOL_ERR_INVALID_ARG, "kpool_latent_prompt_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def new_latent_workspace(q_rows: int, num_seqs: int, heads: int, latent_dim: int, rotary_dim: int, dtype,
+                         device=None) -> torch.Tensor:
+    """Workspace of kpool_attention_latent with up to these sizes (dtype: the torch dtype of q)."""
+    n = int(load().kpool_latent_workspace_bytes(q_rows, num_seqs, ctypes.byref(
+        _latent_shape(heads, latent_dim, rotary_dim, latent_dim, dtype))))
+    if n == 0:
+        raise KpoolError(KPOOL_ERR_INVALID_ARG, "kpool_latent_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def kpool_attention_latent_prompt(q: torch.Tensor, k: torch.Tensor, k_rotary: torch.Tensor, v: torch.Tensor,
+                                  cu_q: torch.Tensor, cu_k: torch.Tensor, scale: float, out=None,
+                                  return_lse: bool = False, out_lse=None, workspace=None, stream=None,
+                                  score_kernel: int = KPOOL_SCORE_AUTO):
+    """Latent attention expanded, for prompts: q [R,H,Dn+Dr], k [T,H,Dn], k_rotary [T,Dr] (the end of every head's
+    key), v [T,H,Dv], with any token and head strides; rows and keys as for kpool_attention_prompt. Returns
+    (out [R,H,Dv], lse [R,H] fp32 or None)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or k_rotary.dim() != 2:
+        raise ValueError("q, k, v are [tokens, heads, channels], k_rotary [tokens, channels]")
+    R, h, dk = q.shape
+    T, _, dn = k.shape
+    dr, dv = k_rotary.shape[1], v.shape[2]
+    if k.shape[1] != h or v.shape[:2] != k.shape[:2] or k_rotary.shape[0] != T or dk != dn + dr:
+        raise ValueError("k, v and q have the same heads, k, v and k_rotary the same tokens; q has k's and k_rotary's "
+                         "channels")
+    if cu_q.numel() != cu_k.numel():
+        raise ValueError("cu_q and cu_k must have the same length")
+    dtype = q.dtype
+    if not k.dtype == v.dtype == k_rotary.dtype == dtype:
+        raise TypeError("k, k_rotary and v must match q's dtype")
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
+    S = cu_k.numel() - 1
+    out, out_lse = _results(R, h, dv, q, out, return_lse, out_lse, stream)
+    if workspace is None:
+        workspace = _new(lambda: new_latent_prompt_workspace(R, S, h, dn, dr, dv, dtype, q.device), stream,
+                         returned=False)
+    dev = _current_device(q, k, k_rotary, v, out)
+    rt, rd = k_rotary.stride()
+    if rd != 1 and dr > 1:
+        raise ValueError("the last dimension of a tensor must be contiguous")
+    a = _serving_args
+    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
+    a.pack_heads(a.buffer, a.heads_at[1], k.data_ptr(), *_strides(k))
+    a.pack_heads(a.buffer, a.heads_at[2], v.data_ptr(), *_strides(v))
+    rotary = kpool_heads(k_rotary.data_ptr(), rt if T > 1 else dr, dr)
+    a.pack_latent(a.buffer, a.latent_at, h, dn, dr, dv, code)
+    a.latent_shape.scale = scale
+    return _finish("kpool_attention_latent_prompt", (_lib or load()).kpool_attention_latent_prompt,
+                   (a.heads[0], a.heads[1], rotary, a.heads[2], _array(cu_q, dev), _array(cu_k, dev), S, R, T,
+                    a.latent), out, out_lse, workspace, stream, dev, score_kernel)
+
+
+def kpool_attention_latent(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                           latent_dim: int, scale: float, token_ids=None, row_seq=None, out=None,
+                           return_lse: bool = False, out_lse=None, workspace=None, stream=None,
+                           score_kernel: int = KPOOL_SCORE_AUTO):
+    """Latent attention absorbed, for caches: q [R,H,L+P] in the latent space, cache [pages, page_size, L+P] whose
+    first L = latent_dim channels are the value too, page_table [S, max_pages] and lengths [S] int32. Row r, of
+    sequence row_seq[r] ([R] int32; None: sequence r), sees its whole cache, or the tokens that token_ids
+    [R, width] int32 names, as kpool_select_rows returns them. Returns (out [R,H,L], lse [R,H] fp32 or None)."""
+    if q.dim() != 3 or cache.dim() != 3 or q.shape[2] != cache.shape[2] or not 0 < latent_dim < q.shape[2]:
+        raise ValueError("q is [rows, heads, channels], cache [pages, page_size, channels] with more than latent_dim")
+    dtype = q.dtype
+    if cache.dtype != dtype:
+        raise TypeError("cache must match q's dtype")
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q and cache must be bfloat16 or float32, got {dtype}")
+    R, h, dim = q.shape
+    pages, size, _ = cache.shape
+    S = lengths.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != S or (R != S if row_seq is None else row_seq.numel() != R):
+        raise ValueError("page_table is [sequences, pages], lengths [sequences], row_seq [rows] (or a row each)")
+    width = KPOOL_WHOLE_CACHE
+    if token_ids is not None:
+        if token_ids.dim() != 2 or token_ids.shape[0] != R:
+            raise ValueError("token_ids is [rows, width]")
+        width = token_ids.shape[1]
+    out, out_lse = _results(R, h, latent_dim, q, out, return_lse, out_lse, stream)
+    if workspace is None:
+        workspace = _new(lambda: new_latent_workspace(R, S, h, latent_dim, dim - latent_dim, dtype, q.device), stream,
+                         returned=False)
+    dev = _current_device(q, cache, out)
+    ps, ts, cd = cache.stride()
+    if cd != 1 and dim > 1:
+        raise ValueError("the last dimension of a tensor must be contiguous")
+    a = _serving_args
+    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
+    a.pack_pages(a.buffer, a.pages_at[0], cache.data_ptr(), ps if pages > 1 else dim, ts if size > 1 else dim, dim)
+    a.pack_latent(a.buffer, a.latent_at, h, latent_dim, dim - latent_dim, latent_dim, code)
+    a.latent_shape.scale = scale
+    return _finish("kpool_attention_latent", (_lib or load()).kpool_attention_latent,
+                   (a.heads[0], a.pages[0], _array(page_table, dev), page_table.shape[1], pages, size,
+                    _array(lengths, dev), _array(token_ids, dev), width, _array(row_seq, dev), S, R, a.latent), out,
+                   out_lse, workspace, stream, dev, score_kernel)
+
+
+def new_rotary_table(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: float = 0.0,
+                     low: float = 1.0, high: float = 32.0, device=None) -> torch.Tensor:
+    """Frequencies for kpool_rotary (see kpool_rotary_table in kpool.h): [rotary_dim // 2] int64 on the device."""
+    table = torch.empty(max(0, rotary_dim // 2), dtype=torch.int64)
+    st = load().kpool_rotary_table(rotary_dim, base, factor, original_length, low, high, table.data_ptr())
+    if st != KPOOL_OK:
+        raise KpoolError(st, "kpool_rotary_table")
+    return table.to(device or torch.device("cuda"))
+
+
+def kpool_rotary(q: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, k=None, q_offset: int = 0,
+                 k_offset: int = 0, interleaved: bool = False, inverse: bool = False, magnitude: float = 1.0,
+                 out_q=None, out_k=None, stream=None):
+    """Rotary positions: q [T,Hq,Dq] and k [T,Hk,Dk] (or None; bf16 or fp32, any token and head strides), positions
+    [T] int32, table [rotary_dim / 2] int64 (new_rotary_table). The channels [offset, offset + rotary_dim) of each
+    head are rotated, in halves or in neighbouring pairs, the others copied. out_q and out_k may be q and k
+    themselves. With inverse the rotation goes the other way (with the same magnitude: the gradient).
+    Returns (out_q, out_k)."""
+    dtype, n = q.dtype, q.shape[0] if q.dim() == 3 else -1
+    code = _ATTENTION_DTYPES.get(dtype)
+    if code is None or (k is not None and k.dtype != dtype):
+        raise TypeError("q and k must be bfloat16 or float32 alike")
+    if n < 0 or (k is not None and (k.dim() != 3 or k.shape[0] != n)) or positions.numel() != n:
+        raise ValueError("q and k are [tokens, heads, channels], positions [tokens]")
+    a = _serving_args
+    found, dev = [], _current_device(q)
+    for i, (x, out, offset) in enumerate(((q, out_q, q_offset), (k, out_k, k_offset))):
+        if x is None:
+            if out is not None:
+                raise ValueError("out_k without k")
+            found.append(None)
+            continue
+        if out is None:
+            out = _empty(x.shape, dtype, x.device, stream)
+        elif out.shape != x.shape or out.dtype != dtype:
+            raise TypeError("out_q and out_k must have the shape and dtype of q and k")
+        if x.get_device() != dev or out.get_device() != dev:
+            raise ValueError("tensors must be CUDA tensors on the current device")
+        a.pack_part(a.buffer, a.part_at[i], x.data_ptr(), *_strides(x), out.data_ptr(), *_strides(out), x.shape[1],
+                    x.shape[2], offset, 0)
+        found.append(out)
+    a.pack_rotary(a.buffer, a.rotary_at, 2 * table.numel(), code,
+                  (KPOOL_ROTARY_INTERLEAVED if interleaved else 0) | (KPOOL_ROTARY_INVERSE if inverse else 0))
+    a.rotary_shape.magnitude = magnitude
+    st = (_lib or load()).kpool_rotary(a.parts[0], None if k is None else a.parts[1], _array(positions, dev),
+                                       _array(table, dev, torch.int64), n, a.rotary,
+                                       torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st != KPOOL_OK:
+        raise KpoolError(st, "kpool_rotary")
+    return tuple(found)
 
 
 def kpool_balanced_row_split(cu_seqlens, kpool: int, parts: int, row_weight: int = 0) -> list:
