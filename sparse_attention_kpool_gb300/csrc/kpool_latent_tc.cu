@@ -44,7 +44,8 @@ constexpr int kBlock = kKeys * 128;          // bytes of 64 channels of a tile, 
 constexpr int kBlocks = kDim / 64;
 constexpr int kTileBytes = kBlocks * kBlock;
 constexpr int kStages = 2;
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
+constexpr int kSoftWarps = 8;
 constexpr int kSegRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -54,14 +55,14 @@ constexpr uint64_t kMaxWaitNs = 1000000000ull;  // 1 s; legitimate waits are mic
 // Shared memory: Q, the tiles, P, then
 constexpr int kOffTiles = kTileBytes;
 constexpr int kOffP = kOffTiles + kStages * kTileBytes;
-constexpr int kOffFactor = kOffP + kBlock;               // [64] fp32: factors of O's columns
-constexpr int kOffSeg = kOffFactor + kHeads * 4;
+constexpr int kOffMax = kOffP + kBlock;                  // [2][2][64] fp32: maxima of a tile's halves; sums at the end
+constexpr int kOffSeg = kOffMax + 4 * kHeads * 4;
 constexpr int kOffBits = kOffSeg + 48 * kSegRing;        // [kStages] x 64 bits: tokens of a tile that are seen
 constexpr int kOffBar = kOffBits + 8 * kStages;
 // full[2] empty[2] q_full q_empty s_full[2] p_ready p_empty o_final o_free done seg_full[4] seg_empty[4]
 constexpr int kNumBars = 2 * kStages + 9 + 2 * kSegRing;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-constexpr int kSmem = kOffMisc + 64;
+constexpr int kSmem = kOffMisc + 72;
 static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
 static_assert(kOffSeg % 16 == 0 && kOffBits % 8 == 0 && kOffBar % 8 == 0 && kOffMisc % 8 == 0, "aligned accesses");
 
@@ -74,8 +75,9 @@ struct Misc {
   uint32_t tmem;
   volatile int32_t abort;
   volatile int32_t bad_page;
+  volatile int32_t dead[3];  // a softmax warp gave up at an even or odd tile, or between segments
 };
-static_assert(sizeof(Misc) <= 64, "Misc fits its space");
+static_assert(sizeof(Misc) <= 72, "Misc fits its space");
 
 struct Seg {
   int32_t row, seq, keys;  // query row, its sequence and the keys that one holds
@@ -229,18 +231,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m
   }
 }
 
-// Barrier of the softmax warps that tells all of them whether one of them says so.
-__device__ __forceinline__ bool group_or(bool flag) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.or.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(out)
-      : "r"(flag ? 1u : 0u)
-      : "memory");
-  return out != 0;
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("barrier.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 }
 
 // per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
@@ -261,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_full = q_full + 9;             // [kSegRing]
   uint64_t* seg_empty = seg_full + kSegRing;   // [kSegRing]
   auto seg_at = [&](int i) { return reinterpret_cast<Seg*>(smem + kOffSeg + 48 * (i % kSegRing)); };
-  float* factor = reinterpret_cast<float*>(smem + kOffFactor);
+  float* maxima = reinterpret_cast<float*>(smem + kOffMax);
   Misc* misc = reinterpret_cast<Misc*>(smem + kOffMisc);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform)
   const int run = blockIdx.x / groups, group = blockIdx.x - run * groups, runs = gridDim.x / groups;
   const int head0 = group * per, heads = min(per, p.H - head0), cols = (heads + 15) & ~15;
   const int slots = part_rows(per);
@@ -276,27 +268,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(full + i, 33 * 4);
+      ptx::mbar_init(full + i, 4);
       ptx::mbar_init(empty + i, 1);
     }
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(s_full + 1, 1);
-    ptx::mbar_init(p_ready, 4);
     ptx::mbar_init(p_empty, 1);
+    ptx::mbar_init(p_ready, kSoftWarps);
     ptx::mbar_init(o_final, 1);
-    ptx::mbar_init(o_free, 4);
+    ptx::mbar_init(o_free, kSoftWarps);
     ptx::mbar_init(done, 1);
     for (int i = 0; i < kSegRing; ++i) {
       ptx::mbar_init(seg_full + i, 1);
-      ptx::mbar_init(seg_empty + i, 9);
+      ptx::mbar_init(seg_empty + i, kSoftWarps + 5);
     }
     ptx::fence_mbar_init();
     misc->abort = 0;
     misc->bad_page = 0;
+    misc->dead[0] = misc->dead[1] = misc->dead[2] = 0;
   }
-  if (warp == 8) {
+  if (warp == 12) {
     ptx::tmem_alloc(&misc->tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -308,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? seg_at(i) : nullptr;
   };
 
-  if (warp == 9) {  // ----------------------------------------------------- segments and Q
+  if (warp == 13) {  // ---------------------------------------------------- segments and Q
     if (lane == 0) {
       SegIter it;
       if (!direct) it.start(p, misc);
@@ -368,77 +361,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (blockIdx.x == 0) latent_check(p, hdr);
-  } else if (warp == 8) {  // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint64_t q_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem));
-      const uint64_t c_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffTiles));
-      const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + kOffTiles), kBlock);
-      const uint64_t p_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffP));
-      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kHeads, kKeys);
-      const uint32_t idesc_o = ptx::idesc_bf16_f32_am(128, cols);
-      uint32_t tile = 0, q_uses = 0;  // tiles before this segment; segments with tiles
-      bool ok = true;
-      const Seg* s;
-      auto landed = [&](uint32_t u) {
-        const bool r = wait_bar(full + u % kStages, (u / kStages) & 1, misc);
-        ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
-        return r;
-      };
-      auto score = [&](uint32_t u) {
-        const uint64_t b = c_desc + (u % kStages) * (kTileBytes >> 4);
-        const uint32_t acc = tmem + 256 + 64 * (u & 1);
+  } else if (warp == 12) {  // ----------------------------------------------- MMA issuer
+    // The warp stays together, its values are the same in all lanes, and one lane issues: 33 cycles an instruction of
+    // the first product, 48 for code that only lane 0 runs (its operands pass through registers of the lane).
+    const uint64_t q_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem));
+    const uint64_t c_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffTiles));
+    const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + kOffTiles), kBlock);
+    const uint64_t p_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + kOffP));
+    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kHeads, kKeys);
+    const uint32_t idesc_o = ptx::idesc_bf16_f32_am(128, cols);
+    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+    uint32_t u = 0, q_uses = 0;  // tiles, segments with tiles
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return bool(__all_sync(0xffffffffu, wait_bar(bar, parity, misc)));
+    };
+    for (int i = 0; ok; ++i) {
+      const Seg* s = segment(i);
+      if (!__all_sync(0xffffffffu, s != nullptr)) break;
+      const int n = __shfl_sync(0xffffffffu, s->n, 0);
+      if (n < 0) break;
+      if (n > 0 && !(ok = wait(q_full, q_uses & 1))) break;
+      int scored = 0;  // tiles of the segment whose scores are issued
+      auto score = [&](uint32_t v) {
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint64_t b = c_desc + v % kStages * (kTileBytes >> 4);
+          const uint32_t to = acc + 256 + 64 * (v & 1);
 #pragma unroll
-        for (int kk = 0; kk < kDim / 16; ++kk) {
-          const uint32_t step = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
-          ptx::tc_mma_f16(acc, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        ptx::tc_commit(s_full + (u & 1));
-      };
-      for (int i = 0; ok && (s = segment(i)) != nullptr && s->n >= 0; ++i) {
-        const int n = s->n;
-        if (n > 0) {
-          if (!(ok = wait_bar(q_full, q_uses & 1, misc) && landed(tile))) break;
-          ptx::tc_fence_after();
-          score(tile);
-          for (int j = 0; j < n; ++j) {
-            const uint32_t u = tile + j;
-            if (j + 1 < n) {
-              if (!(ok = landed(u + 1))) break;
-              ptx::tc_fence_after();
-              score(u + 1);
-            }
-            if (j == max(n - 2, 0)) ptx::tc_commit(q_empty);  // the segment's last scores are issued
-            if (!(ok = wait_bar(p_ready, u & 1, misc))) break;
-            if (j == 0 && q_uses > 0 && !(ok = wait_bar(o_free, (q_uses - 1) & 1, misc))) break;
-            ptx::tc_fence_after();
-            const uint64_t a = v_desc + (u % kStages) * (kTileBytes >> 4);
-#pragma unroll
-            for (int c = 0; c < kLatent / 128; ++c)
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                ptx::tc_mma_f16(tmem + 64 * c, a + ((2 * c * kBlock + kk * 2048) >> 4), p_desc + (kk * 32 >> 4), idesc_o,
-                                (kk > 0 || j > 0) ? 1u : 0u);
-            ptx::tc_commit(empty + u % kStages);
-            ptx::tc_commit(p_empty);
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint32_t step = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
+            ptx::tc_mma_f16(to, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
           }
-          if (!ok) break;
-          ptx::tc_commit(o_final);
-          tile += n;
-          ++q_uses;
+          ptx::tc_commit(s_full + (v & 1));
+          if (scored == n - 1) ptx::tc_commit(q_empty);
         }
-        ptx::mbar_arrive(seg_empty + i % kSegRing);
+        __syncwarp();
+        ++scored;
+      };
+      for (int j = 0; j < n; ++j, ++u) {
+        const uint32_t st = u % kStages;
+        if (scored == j) {
+          if (!(ok = wait(full + st, (u / kStages) & 1))) break;
+          score(u);
+        }
+        // While the weights are made, the next scores if their tile is there by then: the second product frees
+        // the slot of the tile after, so it does not wait for the next one to land.
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (!__all_sync(0xffffffffu, ptx::mbar_test(p_ready, u & 1))) {
+          if (scored == j + 1 && scored < n &&
+              __all_sync(0xffffffffu, ptx::mbar_test(full + (u + 1) % kStages, ((u + 1) / kStages) & 1)))
+            score(u + 1);
+          if (__any_sync(0xffffffffu, misc->abort || ptx::globaltimer_ns() - t0 > kMaxWaitNs)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) {
+          misc->abort = 1;
+          break;
+        }
+        if (j == 0 && q_uses > 0 && !(ok = wait(o_free, (q_uses - 1) & 1))) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint64_t a = v_desc + st * (kTileBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < kLatent / 128; ++c)
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              ptx::tc_mma_f16(acc + 64 * c, a + ((2 * c * kBlock + kk * 2048) >> 4), p_desc + (kk * 32 >> 4), idesc_o,
+                              (kk > 0 || j > 0) ? 1u : 0u);
+          ptx::tc_commit(empty + st);
+          ptx::tc_commit(p_empty);
+          if (j == n - 1) ptx::tc_commit(o_final);
+        }
+        __syncwarp();
       }
-      ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
-      ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
+      if (!ok) break;
+      if (n > 0) ++q_uses;
+      if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
     }
-  } else if (warp >= 4) {  // ------------------------------------------------ copying warps
+    if (ptx::elect_one()) ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
+    ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
+  } else if (warp >= kSoftWarps) {  // --------------------------------------- copying warps
     // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each.
-    const int w = warp - 4, c = lane & 7, sub = lane >> 3;
+    const int w = warp - kSoftWarps, c = lane & 7, sub = lane >> 3;
     const char* base = static_cast<const char*>(p.cache) + c * 16;
     const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * 16 + sub) * 128;
     uint32_t u = 0;
     bool ok = true, bad = false;
     const Seg* s;
+    // Copies are waited for here, where they are also made known to the tensor core: a fence in the issuing warp
+    // would wait for the products in flight.
+    auto land = [&](uint32_t v) {
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full + v % kStages);
+    };
     for (int i = 0;; ++i) {
       s = segment(i);
       if (!__all_sync(0xffffffffu, s != nullptr) || s->n < 0) break;
@@ -466,9 +485,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < kBlocks; ++h) ptx::cp_async_16(dst + h * kBlock, from + h * 128, bytes);
         }
-        ptx::cp_async_arrive(full + st);
-        if (lane == 0) ptx::mbar_arrive(full + st);
+        ptx::cp_async_commit();
         if (j + 1 < n) next = token(j + 1);
+        if (j + 1 < n && u + 1 < kStages) continue;  // (the first tiles: the next slot is free)
+        if (j > 0 && u < kStages) {
+          ptx::cp_async_wait<1>();
+          land(u - 1);
+        }
+        ptx::cp_async_wait<0>();
+        land(u);
       }
       if (!ok) break;
       __syncwarp();
@@ -477,134 +502,154 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) misc->bad_page = 1;
     ptx::cp_async_wait_all();  // every copy has landed before the CTA exits
   } else {  // ---------------------------------------------------------------- softmax
-    // Lane 4 g + t has the heads 16 warp + g and 8 further, tokens 8 x + 2 t and the next of every eight.
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    // Warps w and w + 4 share the heads [16 w, 16 w + 16), a half of a tile's tokens each: lane 4 g + t has the heads
+    // 16 w + g and 8 further, tokens 8 x + 2 t and the next of every eight. Every warp keeps the maxima of all 64 heads
+    // (lane i: heads i and i + 32) and finds by itself, from the halves' maxima of the tile, which of them grow.
+    const int half = warp >> 2, g = lane >> 2, t = lane & 3;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const float c2 = p.scale * kLog2e;
-    const int row0 = warp * 16 + g;
+    const int row0 = (warp & 3) * 16 + g;
+    const bool live = (warp & 3) * 16 < cols;  // (other heads' weights are not read)
     uint8_t* p_row = smem + kOffP + row0 * 128 + t * 4;
     uint32_t u = 0, finals = 0;
     bool ok = true;
+    // value of heads i, i + 32 (in lane i) for the lane's own two heads
+    auto own = [&](const float (&x)[2], int h) {
+      const float lo = __shfl_sync(0xffffffffu, x[0], (row0 + 8 * h) & 31), hi = __shfl_sync(0xffffffffu, x[1], (row0 + 8 * h) & 31);
+      return row0 + 8 * h < 32 ? lo : hi;
+    };
     for (int is = 0;; ++is) {
       const Seg* sg = segment(is);
-      if (group_or(sg == nullptr) || sg->n < 0) break;
+      // (all warps leave together: whoever gives up says so before a barrier, and all read it behind it)
+      if (!__all_sync(0xffffffffu, sg != nullptr)) misc->dead[2] = 1;
+      soft_sync();
+      if (misc->dead[2]) break;
       const int n = sg->n;
+      if (n < 0) break;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       for (int j = 0; j < n; ++j, ++u) {
-        ok = wait_bar(s_full + (u & 1), (u >> 1) & 1, misc);
-        if (group_or(!ok)) {
+        if (!__all_sync(0xffffffffu, wait_bar(s_full + (u & 1), (u >> 1) & 1, misc))) misc->dead[u & 1] = 1;
+        ptx::tc_fence_after();
+        uint32_t s[16];
+        ptx::tc_ld_16x256b_x4(tmem + 256 + 64 * (u & 1) + lanes + 32 * half, s);
+        const uint32_t bits = *reinterpret_cast<const volatile uint32_t*>(smem + kOffBits + 8 * (u % kStages) + 4 * half);
+        ptx::tc_wait_ld();
+        ptx::tc_reg_fence(s);
+        if (bits != 0xffffffffu) {
+          const uint32_t mine = bits >> (2 * t);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (!((mine >> (8 * x + y)) & 1u)) s[4 * x + y] = s[4 * x + 2 + y] = 0xFF800000u;  // -inf
+        }
+        float* mx = maxima + (u & 1) * 2 * kHeads;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mt = __uint_as_float(s[2 * h]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mt = fmaxf(fmaxf(mt, __uint_as_float(s[4 * x + 2 * h])), __uint_as_float(s[4 * x + 2 * h + 1]));
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+          if (t == 0) mx[half * kHeads + row0 + 8 * h] = mt;
+        }
+        // the second product of the tile before is done: O is at rest, and P may be written
+        if (u > 0 && !__all_sync(0xffffffffu, wait_bar(p_empty, (u - 1) & 1, misc))) misc->dead[u & 1] = 1;
+        soft_sync();
+        if (misc->dead[u & 1]) {
           ok = false;
           break;
         }
-        ptx::tc_fence_after();
-        uint32_t s[32];
-        ptx::tc_ld_16x256b_x8(tmem + lanes + 256 + 64 * (u & 1), s);
-        const uint64_t bits = *reinterpret_cast<const volatile uint64_t*>(smem + kOffBits + 8 * (u % kStages));
-        ptx::tc_wait_ld();
-        ptx::tc_reg_fence(s);
-        if (bits != ~uint64_t(0)) {
-          const uint64_t mine = bits >> (2 * t);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              if (!((mine >> (8 * x + y)) & 1)) s[4 * x + y] = s[4 * x + 2 + y] = 0xFF800000u;  // -inf
-        }
-        float mt[2];
+        bool grow[2];
+        float top[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mt[h] = __uint_as_float(s[2 * h]);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            mt[h] = fmaxf(fmaxf(mt[h], __uint_as_float(s[4 * x + 2 * h])), __uint_as_float(s[4 * x + 2 * h + 1]));
-          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
-          mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+          top[h] = fmaxf(mx[lane + 32 * h], mx[kHeads + lane + 32 * h]);
+          grow[h] = top[h] > m[h] && (top[h] - m[h]) * c2 > kLazy;
         }
-        bool grow[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) grow[h] = mt[h] > m[h] && (mt[h] - m[h]) * c2 > kLazy;
-        const bool rescale = group_or(grow[0] || grow[1]);
-        // the second product of the tile before is done: O is at rest and P may be written
-        if (u > 0) ok = wait_bar(p_empty, (u - 1) & 1, misc);
-        if (rescale) {
+        if (__any_sync(0xffffffffu, grow[0] || grow[1])) {  // (the same in every warp)
+          float f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = grow[h] ? ptx::exp2_approx((m[h] - mt[h]) * c2) : 1.0f;
-            if (grow[h]) m[h] = mt[h];
-            l[h] *= f;
-            if (t == 0) factor[row0 + 8 * h] = f;
+            f[h] = grow[h] ? ptx::exp2_approx((m[h] - top[h]) * c2) : 1.0f;
+            if (grow[h]) m[h] = top[h];
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) l[h] *= own(f, h);
           if (j > 0) {
-            if (group_or(!ok)) {
-              ok = false;
-              break;
-            }
             ptx::tc_fence_after();
+            const int per_block = cols / 16;
 #pragma unroll 1
-            for (int x = 0; x < 4 * cols / 16; ++x) {
-              const int c = x / (cols / 16), col = (x - c * (cols / 16)) * 16;
+            for (int x = 0; x < 2 * per_block; ++x) {
+              const int c = 2 * half + x / per_block, col = (x % per_block) * 16;
               const uint32_t at = tmem + lanes + 64 * c + col;
               uint32_t o[16];
               ptx::tc_ld_32x32b_x16(at, o);
               ptx::tc_wait_ld();
               ptx::tc_reg_fence(o);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * factor[col + y]);
+              for (int y = 0; y < 16; ++y)
+                o[y] = __float_as_uint(__uint_as_float(o[y]) *
+                                       __shfl_sync(0xffffffffu, col < 32 ? f[0] : f[1], (col & 31) + y));
               ptx::tc_st_32x32b_x16(at, o);
             }
             ptx::tc_wait_st();
           }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-          misc->abort = 1;
-          ok = false;
-        }
+        if (live) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float nb = m[h] == -INFINITY ? 0.0f : -m[h] * c2;
+          for (int h = 0; h < 2; ++h) {
+            const float mine = own(m, h), nb = mine == -INFINITY ? 0.0f : -mine * c2;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb));
-            const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb));
-            l[h] += a + b;
-            *reinterpret_cast<uint32_t*>(p_row + h * 1024 + ((x ^ g) << 4)) = ptx::pack_bf16(a, b);
+            for (int x = 0; x < 4; ++x) {
+              const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb));
+              const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb));
+              l[h] += a + b;
+              *reinterpret_cast<uint32_t*>(p_row + h * 1024 + (((4 * half + x) ^ g) << 4)) = ptx::pack_bf16(a, b);
+            }
           }
+          ptx::fence_proxy_async_smem();
         }
-        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_ready);
       }
-      if (group_or(!ok)) break;
+      if (!ok) break;
       // ------------------------------------------------------------------------ epilogue
+      // The sums of both halves, in shared memory like the maxima (whose last readers are behind a barrier).
+      float* sums = maxima + (u & 1) * 2 * kHeads;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (t == 0) sums[half * kHeads + row0 + 8 * h] = l[h];
       }
+      if (n > 0 && !__all_sync(0xffffffffu, wait_bar(o_final, finals & 1, misc))) misc->dead[u & 1] = 1;
+      soft_sync();
+      if (misc->dead[u & 1]) break;
+      ptx::tc_fence_after();
       float* pslot = part + (size_t(blockIdx.x) * 2 + sg->slot) * size_t(slots) * (kLatent + 2);
-      if (t == 0) {
+      float inv[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int head = row0 + 8 * h;
-          const bool none = m[h] == -INFINITY && l[h] == 0.0f;  // (a NaN score leaves l NaN: not empty)
-          factor[head] = none ? 0.0f : 1.0f / l[h];
-          if (head >= heads) continue;
-          if (sg->whole) {
-            if (p.lse)
-              p.lse[int64_t(sg->row) * p.H + head0 + head] = none ? -INFINITY : (m[h] * c2 + log2f(l[h])) * kLn2;
-          } else {
-            *reinterpret_cast<float2*>(pslot + size_t(slots) * kLatent + 2 * head) = make_float2(m[h], l[h]);
-          }
+      for (int h = 0; h < 2; ++h) {
+        const int head = lane + 32 * h;
+        const float sum = sums[head] + sums[kHeads + head];
+        const bool none = m[h] == -INFINITY && sum == 0.0f;  // (a NaN score leaves the sum NaN: not empty)
+        inv[h] = none ? 0.0f : 1.0f / sum;
+        if (warp != 0 || head >= heads) continue;
+        if (sg->whole) {
+          if (p.lse)
+            p.lse[int64_t(sg->row) * p.H + head0 + head] = none ? -INFINITY : (m[h] * c2 + log2f(sum)) * kLn2;
+        } else {
+          *reinterpret_cast<float2*>(pslot + size_t(slots) * kLatent + 2 * head) = make_float2(m[h], sum);
         }
       }
-      if (n > 0) ok = wait_bar(o_final, finals & 1, misc);
-      if (group_or(!ok)) break;  // (and the factors are written)
-      ptx::tc_fence_after();
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(sg->row) * p.o_ts + int64_t(head0) * p.o_hs;
+      const int per_block = cols / 16;
 #pragma unroll 1
-      for (int x = 0; x < 4 * cols / 16; ++x) {
-        const int c = x / (cols / 16), col = (x - c * (cols / 16)) * 16;
+      for (int x = 0; x < 2 * per_block; ++x) {
+        const int c = 2 * half + x / per_block, col = (x % per_block) * 16;
         uint32_t o[16];
 #pragma unroll
         for (int y = 0; y < 16; ++y) o[y] = 0;
@@ -613,18 +658,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_wait_ld();
           ptx::tc_reg_fence(o);
         }
-        const int ch = 128 * c + 32 * warp + lane;
+        const int ch = 128 * c + 32 * (warp & 3) + lane;
         if (sg->whole) {
           // neighbouring lanes exchange halves of two heads: each then writes two channels of one head
 #pragma unroll
           for (int y = 0; y < 16; y += 2) {
-            const float a = __uint_as_float(o[y]) * factor[col + y], b = __uint_as_float(o[y + 1]) * factor[col + y + 1];
+            const float fa = __shfl_sync(0xffffffffu, col < 32 ? inv[0] : inv[1], (col & 31) + y);
+            const float fb = __shfl_sync(0xffffffffu, col < 32 ? inv[0] : inv[1], (col & 31) + y + 1);
+            // (no weight at all: zeros, whatever the products hold)
+            const float a = fa == 0.0f ? 0.0f : __uint_as_float(o[y]) * fa;
+            const float b = fb == 0.0f ? 0.0f : __uint_as_float(o[y + 1]) * fb;
             const bool odd = lane & 1;
             const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
             const int head = col + y + odd;
-            const bool zero = factor[head] == 0.0f;  // (no weight at all, or an infinite sum: zeros either way)
-            const uint32_t v = zero ? 0u : odd ? ptx::pack_bf16(got, b) : ptx::pack_bf16(a, got);
-            if (head < heads) *reinterpret_cast<uint32_t*>(out + head * p.o_hs + (ch & ~1)) = v;
+            if (head < heads)
+              *reinterpret_cast<uint32_t*>(out + head * p.o_hs + (ch & ~1)) =
+                  odd ? ptx::pack_bf16(got, b) : ptx::pack_bf16(a, got);
           }
         } else {
 #pragma unroll
@@ -640,7 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(seg_empty + is % kSegRing);
-      // (the factors are read by all before the next row writes them: its first tile has a barrier in between)
     }
     ptx::tc_fence_before();
   }
@@ -649,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && misc->abort) record_error(hdr, KPOOL_ERR_DEVICE_TIMEOUT);
   if (threadIdx.x == 0 && misc->bad_page) record_error(hdr, KPOOL_ERR_INVALID_ARG);
-  if (warp == 8) {
+  if (warp == 12) {
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
