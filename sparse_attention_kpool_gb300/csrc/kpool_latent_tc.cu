@@ -10,10 +10,11 @@
 // buffers of scores. More than 64 heads are split evenly over CTAs side by side that walk
 // the same tokens at the same time, so that the second reads what the first brought into L2.
 //
-// Roles (10 warps): warps 0-3 softmax, four threads to a head's 64 scores (the layout in which a 16-row
-// accumulator is read); warps 4-7 copy tokens, 16 bytes a lane (cp.async), whole rows of 1,152 bytes wherever
-// the page table puts them; warp 8 issues the MMAs and owns tensor memory; warp 9 hands out segments and loads Q.
-// The scores of tile j + 1 are issued before the second product of tile j, which waits for its softmax.
+// Roles (18 warps): warps 0-7 softmax, eight threads to a head's 64 scores (the layout in which a 16-row
+// accumulator is read); warps 8-15 copy tokens, by TMA where a whole tile lies in few pages, else 16 bytes a lane
+// (cp.async), rows of 1,152 bytes wherever the ids and the page table put them; warp 16 issues the MMAs and owns
+// tensor memory; warp 17 hands out segments and loads Q. The scores of tile j + 1 are issued while the softmax of
+// tile j runs if that tile has landed by then, else behind the second product of tile j.
 //
 // What bounds it. A tile is 74 KB, at the measured copy rate and 152 SMs 3,100 cycles. The tensor core
 // reads operands from shared memory at about 90 bytes a cycle: 36 x 4 KB and 16 x 6 KB are 2,700 cycles at 64 heads
@@ -44,8 +45,10 @@ constexpr int kBlock = kKeys * 128;          // bytes of 64 channels of a tile, 
 constexpr int kBlocks = kDim / 64;
 constexpr int kTileBytes = kBlocks * kBlock;
 constexpr int kStages = 2;
-constexpr int kThreads = 448;
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 8, kCopyWarps = 4, kMmaWarp = kSoftWarps + kCopyWarps, kSegWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kSegWarp + 1);
+constexpr int kCopyRows = kKeys / kCopyWarps;  // tokens of a tile that a warp copies
+constexpr int kBoxRows = 16;                 // smallest boxes that TMA is taken for
 constexpr int kSegRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -235,10 +238,11 @@ __device__ __forceinline__ void soft_sync() {
   asm volatile("barrier.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 }
 
-// per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
+// box_rows: tokens of a TMA copy of the cache, 0 for none; per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ LatentParams p, int per,
-                     int groups, int direct, float* part, JoinItem* joins, WorkspaceHeader* hdr) {
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
+                     const __grid_constant__ LatentParams p, int box_rows, int per, int groups, int direct, float* part,
+                     JoinItem* joins, WorkspaceHeader* hdr) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int run = blockIdx.x / groups, group = blockIdx.x - run * groups, runs = gridDim.x / groups;
   const int head0 = group * per, heads = min(per, p.H - head0), cols = (heads + 15) & ~15;
   const int slots = part_rows(per);
+  const int pieces = box_rows > 0 ? kKeys / box_rows : 0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
   if (blockIdx.x == 0 && threadIdx.x == 0) hdr->error = KPOOL_OK;
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(full + i, 4);
+      ptx::mbar_init(full + i, kCopyWarps);
       ptx::mbar_init(empty + i, 1);
     }
     ptx::mbar_init(q_full, 1);
@@ -282,14 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(done, 1);
     for (int i = 0; i < kSegRing; ++i) {
       ptx::mbar_init(seg_full + i, 1);
-      ptx::mbar_init(seg_empty + i, kSoftWarps + 5);
+      ptx::mbar_init(seg_empty + i, kSoftWarps + kCopyWarps + 1);
     }
     ptx::fence_mbar_init();
     misc->abort = 0;
     misc->bad_page = 0;
     misc->dead[0] = misc->dead[1] = misc->dead[2] = 0;
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(&misc->tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return wait_bar(seg_full + i % kSegRing, (i / kSegRing) & 1, misc) ? seg_at(i) : nullptr;
   };
 
-  if (warp == 13) {  // ---------------------------------------------------- segments and Q
+  if (warp == kSegWarp) {  // ---------------------------------------------------- segments and Q
     if (lane == 0) {
       SegIter it;
       if (!direct) it.start(p, misc);
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (blockIdx.x == 0) latent_check(p, hdr);
-  } else if (warp == 12) {  // ----------------------------------------------- MMA issuer
+  } else if (warp == kMmaWarp) {  // ----------------------------------------------- MMA issuer
     // The warp stays together, its values are the same in all lanes, and one lane issues: 33 cycles an instruction of
     // the first product, 48 for code that only lane 0 runs (its operands pass through registers of the lane).
     const uint64_t q_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem));
@@ -444,12 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ptx::elect_one()) ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
     ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
   } else if (warp >= kSoftWarps) {  // --------------------------------------- copying warps
-    // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each.
+    // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each. Whole
+    // tiles of a cache in pages of 16 tokens and more come by TMA instead, a box in four from each warp. Where a tile's tokens
+    // lie is looked up while the tile before is on its way: ids two tiles ahead, pages one.
     const int w = warp - kSoftWarps, c = lane & 7, sub = lane >> 3;
+    const int box = lane < 9 ? kCopyWarps * lane + w : kCopyWarps * 9;  // of 9 to 36 in a tile
     const char* base = static_cast<const char*>(p.cache) + c * 16;
-    const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * 16 + sub) * 128;
-    uint32_t u = 0;
-    bool ok = true, bad = false;
+    const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * kCopyRows + sub) * 128;
+    uint32_t u = 0, by_tma_at[kStages] = {};  // 1 + the last tile of a slot where TMA brought it
+    bool ok = true, bad = false, held = false;  // held: the tile before has been copied, but not waited for
     const Seg* s;
     // Copies are waited for here, where they are also made known to the tensor core: a fence in the issuing warp
     // would wait for the products in flight.
@@ -461,37 +469,91 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0;; ++i) {
       s = segment(i);
       if (!__all_sync(0xffffffffu, s != nullptr) || s->n < 0) break;
-      const int n = s->n;
-      auto token = [&](int j) {
-        const int place = (s->kt0 + j) * kKeys + w * 16 + lane;
-        return lane < 16 && place < s->end ? latent_token(p, s->row, s->seq, s->keys, place, &bad) : int64_t(-1);
+      const int n = s->n, keys = s->keys, end = s->end, kt0 = s->kt0;
+      const int32_t* table = p.table + int64_t(s->seq) * p.max_pages;
+      const int32_t* ids = p.ids + int64_t(s->row) * p.width;
+      auto by_tma = [&](int j) { return box_rows > 0 && (kt0 + j + 1) * kKeys <= end; };
+      // The token (of the sequence) that the lane looks up for tile j: lanes 0-15 the warp's rows of a copied tile,
+      // lanes 0-8 the first token of the piece of their TMA box; -1: none.
+      auto id_of = [&](int j) {
+        const int first = (kt0 + j) * kKeys;
+        if (j >= n) return -1;
+        if (by_tma(j)) return box < pieces * kBlocks ? first + box / kBlocks * box_rows : -1;
+        const int place = first + w * kCopyRows + lane;
+        if (lane >= kCopyRows || place >= end) return -1;
+        return latent_listed(p) ? ptx::ldg_ordered(ids + place) : place;
       };
-      int64_t next = n > 0 ? token(0) : -1;
+      int id1 = id_of(0), page = -1, in_page = 0, id = -1;
+      auto look_up = [&]() {  // the page of the id that was read before; the next id
+        id = id1 >= 0 && id1 < keys ? id1 : -1;
+        const int at = id / p.page_size;
+        in_page = id - at * p.page_size;
+        page = id >= 0 ? ptx::ldg_ordered(table + at) : -1;
+      };
+      if (n > 0) {
+        look_up();
+        id1 = id_of(1);
+      }
       for (int j = 0; j < n; ++j, ++u) {
-        const int64_t at = next;
         const uint32_t st = u % kStages;
+        const bool tma = by_tma(j);
+        if (id >= 0 && (page < 0 || page >= p.num_pages)) {
+          bad = true;
+          page = -1;
+        }
+        const uint32_t bits = tma ? 0xffffu : __ballot_sync(0xffffffffu, page >= 0);
+        // everything but the copies themselves comes before the slot is free
+        const char* from[kCopyRows / 4];
+        uint32_t bytes[kCopyRows / 4];
+        {
+          const int64_t at = page >= 0 ? int64_t(page) * p.c_ps + int64_t(in_page) * p.c_ts : -1;
+#pragma unroll
+          for (int q = 0; q < kCopyRows / 4; ++q) {
+            const int64_t t = __shfl_sync(0xffffffffu, at, 4 * q + sub);
+            from[q] = base + (t >= 0 ? t : 0) * 2;
+            bytes[q] = t >= 0 ? 16u : 0u;
+            asm volatile("" : "+l"(from[q]), "+r"(bytes[q]));
+          }
+        }
         if (u >= kStages) ok = __all_sync(0xffffffffu, wait_bar(empty + st, (u / kStages - 1) & 1, misc));
         if (!ok) break;
         __syncwarp();
-        const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
         if (lane == 0) reinterpret_cast<uint16_t*>(smem + kOffBits)[4 * st + w] = uint16_t(bits);
+        if (tma) {
+          const int boxes = (pieces * kBlocks - w + kCopyWarps - 1) / kCopyWarps;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, uint32_t(boxes * box_rows * 128));
+          __syncwarp();
+          if (lane < boxes) {
+            const int piece = box / kBlocks, h = box - piece * kBlocks;
+            ptx::tma_load_4d(smem + kOffTiles + st * kTileBytes + h * kBlock + piece * box_rows * 128, &tm_c, full + st, 64 * h,
+                             0, in_page, page);  // (page -1: zeros)
+          }
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t t = __shfl_sync(0xffffffffu, at, 4 * q + sub);
-          const char* from = base + (t >= 0 ? t : 0) * 2;
-          const uint32_t bytes = t >= 0 ? 16u : 0u;
-          // the row's number modulo eight permutes its 16-byte pieces
-          const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ (((q & 1) * 4 + sub) & 7)) << 4);
+          for (int q = 0; q < kCopyRows / 4; ++q) {
+            // the row's number modulo eight permutes its 16-byte pieces
+            const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ ((q * 4 + sub) & 7)) << 4);
 #pragma unroll
-          for (int h = 0; h < kBlocks; ++h) ptx::cp_async_16(dst + h * kBlock, from + h * 128, bytes);
+            for (int h = 0; h < kBlocks; ++h) ptx::cp_async_16(dst + h * kBlock, from[q] + h * 128, bytes[q]);
+          }
+          ptx::cp_async_commit();
         }
-        ptx::cp_async_commit();
-        if (j + 1 < n) next = token(j + 1);
-        if (j + 1 < n && u + 1 < kStages) continue;  // (the first tiles: the next slot is free)
-        if (j > 0 && u < kStages) {
-          ptx::cp_async_wait<1>();
+        if (j + 1 < n) {
+          look_up();
+          id1 = id_of(j + 2);
+        }
+        by_tma_at[st] = tma ? u + 1 : 0;
+        if (!tma && j + 1 < n && u + 1 < kStages) {  // (the first tiles: the next slot is free)
+          held = true;
+          continue;
+        }
+        if (held) {
+          if (tma) ptx::cp_async_wait<0>();
+          else ptx::cp_async_wait<1>();
           land(u - 1);
+          held = false;
         }
+        if (tma) continue;
         ptx::cp_async_wait<0>();
         land(u);
       }
@@ -500,7 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
     }
     if (bad) misc->bad_page = 1;
-    ptx::cp_async_wait_all();  // every copy has landed before the CTA exits
+    // every copy has landed before the CTA exits
+    ptx::cp_async_wait_all();
+#pragma unroll
+    for (int st = 0; st < kStages; ++st)
+      if (by_tma_at[st])
+        ptx::mbar_wait_bounded(full + st, ((by_tma_at[st] - 1) / kStages) & 1, int64_t(1) << 40, kMaxWaitNs);
   } else {  // ---------------------------------------------------------------- softmax
     // Warps w and w + 4 share the heads [16 w, 16 w + 16), a half of a tile's tokens each: lane 4 g + t has the heads
     // 16 w + g and 8 further, tokens 8 x + 2 t and the next of every eight. Every warp keeps the maxima of all 64 heads
@@ -527,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = sg->n;
       if (n < 0) break;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float nb[2] = {0.f, 0.f};  // what the lane's own heads' exponents begin with: minus their maxima
       for (int j = 0; j < n; ++j, ++u) {
         if (!__all_sync(0xffffffffu, wait_bar(s_full + (u & 1), (u >> 1) & 1, misc))) misc->dead[u & 1] = 1;
         ptx::tc_fence_after();
@@ -576,7 +644,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (grow[h]) m[h] = top[h];
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) l[h] *= own(f, h);
+          for (int h = 0; h < 2; ++h) {
+            l[h] *= own(f, h);
+            const float mine = own(m, h);
+            nb[h] = mine == -INFINITY ? 0.0f : -mine * c2;
+          }
           if (j > 0) {
             ptx::tc_fence_after();
             const int per_block = cols / 16;
@@ -600,11 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float mine = own(m, h), nb = mine == -INFINITY ? 0.0f : -mine * c2;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb));
-              const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb));
+              const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb[h]));
+              const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb[h]));
               l[h] += a + b;
               *reinterpret_cast<uint32_t*>(p_row + h * 1024 + (((4 * half + x) ^ g) << 4)) = ptx::pack_bf16(a, b);
             }
@@ -697,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && misc->abort) record_error(hdr, KPOOL_ERR_DEVICE_TIMEOUT);
   if (threadIdx.x == 0 && misc->bad_page) record_error(hdr, KPOOL_ERR_INVALID_ARG);
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -822,6 +893,14 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   CUtensorMap tq;
   if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.H), kDim, p.q_ts, p.q_hs, 1, kHeads))
     return cudaErrorInvalidValue;
+  // Whole caches by TMA where the pieces that lie in one page wherever they begin, the largest power of two that divides
+  // the page size, have at least 16 tokens.
+  const int low = p.page_size & -p.page_size, box = low < kKeys ? low : kKeys;
+  const int box_rows = latent_listed(p) || box < kBoxRows ? 0 : box;
+  CUtensorMap tc = tq;
+  if (box_rows > 0 && !make_tmap_bf16_pages(&tc, p.cache, uint64_t(p.num_pages), uint64_t(p.page_size), 1, kDim, p.c_ps, p.c_ts,
+                                            kDim, uint32_t(box_rows)))
+    return cudaErrorInvalidValue;
   if (sms > kMaxRuns) sms = kMaxRuns;
   int runs = groups > sms ? 1 : sms / groups;
   // Equal runs of tiles fill the SMs and cost a join (about four tiles' time). Lists of ids are all alike: whole
@@ -838,7 +917,7 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   static std::atomic<uint64_t> ready{0};
   e = allow_dynamic_smem(reinterpret_cast<const void*>(latent_tc_kernel), kSmem, &ready);
   if (e != cudaSuccess) return e;
-  latent_tc_kernel<<<runs * groups, kThreads, kSmem, stream>>>(tq, p, per, groups, direct ? 1 : 0, part, joins, hdr);
+  latent_tc_kernel<<<runs * groups, kThreads, kSmem, stream>>>(tq, tc, p, box_rows, per, groups, direct ? 1 : 0, part, joins, hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || runs < 2) return e;
   cudaLaunchConfig_t cfg{};
