@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kpool_internal.cuh"
 
 namespace kpool {
@@ -40,24 +42,35 @@ struct AttnParams {
   const int32_t* ids;                        // [R, width] (selected)
   const int32_t* row_seq;                    // [R] or null (selected)
   int32_t mask_words, width;
-  // Keys in pages (prompt): key j of sequence b is token j % page_size of page table[b * max_pages + j / page_size];
-  // k and v are then the pages, with these strides between them. cu_q may be null: a row per sequence.
-  const int32_t* table;                      // [S, max_pages] or null
-  const int32_t* lengths;                    // [S] keys of a sequence
-  int32_t max_pages, page_size, num_pages;
-  int64_t k_ps, v_ps;
-  // Keys whose last channels are shared by all heads (prompt): channels [Dn, D) come from here
-  const void* kr;                            // [T, D - Dn] or null
-  int64_t kr_ts;
   const AttnDense* dense;                    // null, or what the dense form of a selection goes by
   const int32_t* list;                       // with dense, gathering: the listed rows
   int32_t S, R;
   int64_t T;
-  int32_t Hq, Hkv, G, D;                     // D: channels of q and k
-  int32_t Dn, Dv;                            // channels that k holds itself (D without kr), and of v and out
+  int32_t Hq, Hkv, G, D;
   float scale;
   AttnMode mode;
 };
+
+// Keys in pages (prompt): key j of sequence b is token j % page_size of page table[b * max_pages + j / page_size]; k and
+// v are the pages, with these strides between them. cu_q may be null: a row per sequence.
+struct AttnPagedParams : AttnParams {
+  const int32_t* table;                      // [S, max_pages]
+  const int32_t* lengths;                    // [S] keys of a sequence
+  int32_t max_pages, page_size, num_pages;
+  int64_t k_ps, v_ps;
+};
+
+// Keys whose last channels are shared by all heads (prompt): D = Dn + those of kr, and values of Dv channels.
+struct AttnSharedParams : AttnParams {
+  const void* kr;                            // [T, D - Dn]
+  int64_t kr_ts;
+  int32_t Dn, Dv;
+};
+
+template <class P>
+constexpr bool kPagedKeys = std::is_same<P, AttnPagedParams>::value;
+template <class P>
+constexpr bool kSharedKeys = std::is_same<P, AttnSharedParams>::value;
 
 // Query rows, keys and committed prefix of one sequence, clipped so that nothing
 // read through them leaves the call's arrays whatever the arrays hold. `ok` is
@@ -70,17 +83,25 @@ struct AttnSeq {
 };
 
 // First query row of sequence b (b <= S).
-__device__ __forceinline__ int attn_q0(const AttnParams& p, int b) { return p.cu_q ? __ldg(p.cu_q + b) : b; }
+template <class P>
+__device__ __forceinline__ int attn_q0(const P& p, int b) {
+  if constexpr (kPagedKeys<P>)
+    if (p.cu_q == nullptr) return b;
+  return __ldg(p.cu_q + b);
+}
 
 // Keys that a sequence's pages can hold.
-__device__ __forceinline__ int64_t attn_page_keys(const AttnParams& p) { return int64_t(p.max_pages) * p.page_size; }
+__device__ __forceinline__ int64_t attn_page_keys(const AttnPagedParams& p) {
+  return int64_t(p.max_pages) * p.page_size;
+}
 
-__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
+template <class P>
+__device__ __forceinline__ AttnSeq attn_seq(const P& p, int b) {
   AttnSeq s;
   s.q0 = attn_q0(p, b);
   const int64_t q1 = attn_q0(p, b + 1);
   int64_t k1;
-  if (p.table) {
+  if constexpr (kPagedKeys<P>) {
     s.k0 = b;
     const int n = __ldg(p.lengths + b);
     k1 = int64_t(b) + n;
@@ -149,7 +170,8 @@ __device__ __forceinline__ int attn_keys_end(const AttnParams& p, const AttnSeq&
 // sequence without any scan or planning kernel; numbers without a tile are skipped.
 inline int64_t attn_tiles(int64_t R, int64_t S, int64_t tt) { return R / tt + S; }
 
-__device__ __forceinline__ int attn_seq_of_tile(const AttnParams& p, int tile, int tt) {
+template <class P>
+__device__ __forceinline__ int attn_seq_of_tile(const P& p, int tile, int tt) {
   int lo = 0, hi = p.S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -162,12 +184,13 @@ __device__ __forceinline__ int attn_seq_of_tile(const AttnParams& p, int tile, i
 // checks the device arrays of the whole call (beside the work, which relies on none of it).
 __device__ __forceinline__ void attn_clear_error(WorkspaceHeader* hdr) { hdr->error = KPOOL_OK; }
 
-__device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader* hdr) {
+template <class P>
+__device__ __forceinline__ void attn_check(const P& p, WorkspaceHeader* hdr) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   for (int b = lane; b <= p.S; b += 32) {
     int k = 0;
-    if (p.table) {
+    if constexpr (kPagedKeys<P>) {
       if (b < p.S) {
         const int n = __ldg(p.lengths + b);
         if (n < 0 || n > attn_page_keys(p)) bad = true;
@@ -200,7 +223,7 @@ __device__ __forceinline__ void attn_check(const AttnParams& p, WorkspaceHeader*
 }
 
 // The page that key j of sequence b lies in; -1 (and *bad) where the table names none of the pool's.
-__device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j, bool* bad) {
+__device__ __forceinline__ int attn_page(const AttnPagedParams& p, int b, int j, bool* bad) {
   const int page = __ldg(p.table + int64_t(b) * p.max_pages + j / p.page_size);
   if (page >= 0 && page < p.num_pages) return page;
   *bad = true;
@@ -265,6 +288,8 @@ bool attn_tc_supported(kpool_dtype dtype, int32_t head_dim);
 bool attn_tc_shared_supported(kpool_dtype dtype, int32_t own, int32_t shared, int32_t value);
 bool attn_gather_supported(int64_t k_ts, int64_t v_ts);
 cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnPagedParams& p, char* ws, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnSharedParams& p, char* ws, cudaStream_t stream);
 
 // Selected tokens by one warp an item, in registers: what attn_tc_supported takes, any strides. Wanted where it
 // beats the other two ways.
@@ -273,5 +298,7 @@ cudaError_t launch_attn_warp(const AttnParams& p, int sms, char* ws, cudaStream_
 
 // CUDA-core kernel: fp32 or bf16, any head_dim <= 256 (of keys and of values).
 cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
+cudaError_t launch_attn_simt(const AttnPagedParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
+cudaError_t launch_attn_simt(const AttnSharedParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream);
 
 }  // namespace kpool

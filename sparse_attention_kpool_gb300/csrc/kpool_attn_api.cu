@@ -70,7 +70,7 @@ void set_shape(AttnParams& p, const kpool_attention_shape& s) {
   p.Hq = s.q_heads;
   p.Hkv = s.kv_heads;
   p.G = s.q_heads / s.kv_heads;
-  p.D = p.Dn = p.Dv = s.head_dim;
+  p.D = s.head_dim;
   p.scale = s.scale;
 }
 
@@ -235,7 +235,7 @@ kpool_status kpool_attention_paged(const kpool_heads* q, const kpool_pages* k, c
       workspace_bytes < kpool_attention_workspace_bytes(q_rows, num_seqs, shape))
     return KPOOL_ERR_WORKSPACE;
 
-  AttnParams p{};
+  AttnPagedParams p{};
   p.mode = kAttnPrompt;
   set_rows(p, q, out, out_lse, num_seqs, q_rows);
   if (some) {
@@ -292,7 +292,7 @@ kpool_status kpool_attention_latent_prompt(const kpool_heads* q, const kpool_hea
       workspace_bytes < kpool_latent_prompt_workspace_bytes(q_rows, num_seqs, shape))
     return KPOOL_ERR_WORKSPACE;
 
-  AttnParams p{};
+  AttnSharedParams p{};
   p.mode = kAttnPrompt;
   set_rows(p, q, out, out_lse, num_seqs, q_rows);
   if (k_tokens > 0) {

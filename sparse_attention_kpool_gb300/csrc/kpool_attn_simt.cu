@@ -47,12 +47,19 @@ __device__ __forceinline__ void group_sync(int group) {
 // Shared memory, in floats: Q, then each group's K and V block; the groups' results overlay the blocks.
 inline __host__ __device__ int group_floats(int D, int Dv) { return kKeys * (D + Dv + 4 + 4 * kPerWarp); }
 
-template <typename E, int kGroups>
+// Channels of v and the result.
+template <class P>
+__host__ __device__ __forceinline__ int value_channels(const P& p) {
+  if constexpr (kSharedKeys<P>) return p.Dv;
+  else return p.D;
+}
+
+template <typename E, int kGroups, class P>
 __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
-    attn_simt_kernel(const __grid_constant__ AttnParams p, int gt, int tt, WorkspaceHeader* hdr) {
+    attn_simt_kernel(const __grid_constant__ P p, int gt, int tt, WorkspaceHeader* hdr) {
   constexpr int kH = kGroups == 4 ? 1 : 2;  // 128-channel parts of a head
   extern __shared__ __align__(16) float smem[];
-  const int D = p.D, Dv = p.Dv, ldk = D + 4;
+  const int D = p.D, Dv = value_channels(p), ldk = D + 4;
   const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
   float* s_q = smem;                                        // [kVRows][D]
   float* s_k = s_q + kVRows * D + group * group_floats(D, Dv);  // [kKeys][D + 4]
@@ -93,7 +100,6 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   const E* q = static_cast<const E*>(p.q);
   const E* kk = static_cast<const E*>(p.k) + int64_t(hk) * p.k_hs;
   const E* vv = static_cast<const E*>(p.v) + int64_t(hk) * p.v_hs;
-  const E* kr = static_cast<const E*>(p.kr);
   const int chunks = D / 4, pieces = max(D, Dv) / 4;
   bool bad_page = false;
   for (int x = threadIdx.x; x < kVRows * chunks; x += kGroupThreads * kGroups) {
@@ -134,24 +140,28 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
         if (at[y] < 0 || j0 + jj >= end) continue;
         const int id = selected ? __ldg(ids + j0 + jj) : j0 + jj;
         if (id < 0 || id >= sq.nk) continue;
-        if (p.table) {  // a page that the pool does not have reads as zeros
+        if constexpr (kPagedKeys<P>) {  // a page that the pool does not have reads as zeros
           const int page = attn_page(p, sq.k0, id, &bad_page), in = id % p.page_size;
           if (page < 0) continue;
           a[y] = load4(kk + int64_t(page) * p.k_ps + in * p.k_ts + c);
           b[y] = load4(vv + int64_t(page) * p.v_ps + in * p.v_ts + c);
-          continue;
+        } else if constexpr (kSharedKeys<P>) {
+          const int64_t t = int64_t(sq.k0) + id;
+          if (c < p.Dn) a[y] = load4(kk + t * p.k_ts + c);
+          else if (c < D) a[y] = load4(static_cast<const E*>(p.kr) + t * p.kr_ts + (c - p.Dn));
+          if (c < Dv) b[y] = load4(vv + t * p.v_ts + c);
+        } else {
+          const int64_t t = int64_t(sq.k0) + id;
+          a[y] = load4(kk + t * p.k_ts + c);
+          b[y] = load4(vv + t * p.v_ts + c);
         }
-        const int64_t t = int64_t(sq.k0) + id;
-        if (c < p.Dn) a[y] = load4(kk + t * p.k_ts + c);
-        else if (c < D) a[y] = load4(kr + t * p.kr_ts + (c - p.Dn));
-        if (c < Dv) b[y] = load4(vv + t * p.v_ts + c);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         if (at[y] < 0) continue;
         const int jj = at[y] >> 10, c = at[y] & 1023;
-        if (c < D) store4(s_k + jj * ldk + c, a[y]);
-        if (c < Dv) store4(s_v + jj * Dv + c, b[y]);
+        if (!kSharedKeys<P> || c < D) store4(s_k + jj * ldk + c, a[y]);
+        if (!kSharedKeys<P> || c < Dv) store4(s_v + jj * Dv + c, b[y]);
       }
     }
     group_sync(group);
@@ -296,33 +306,45 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
   if (checks && threadIdx.x < 32) attn_check(p, hdr);
 }
 
-template <typename E, int kGroups>
-cudaError_t launch(const AttnParams& p, const dim3& grid, int gt, int tt, WorkspaceHeader* hdr, cudaStream_t stream) {
+template <typename E, int kGroups, class P>
+cudaError_t launch(const P& p, const dim3& grid, int gt, int tt, WorkspaceHeader* hdr, cudaStream_t stream) {
   auto bytes = [](int D, int Dv) {
     return sizeof(float) * (size_t(kVRows) * D + size_t(kGroups) * group_floats(D, Dv));
   };
-  auto kernel = attn_simt_kernel<E, kGroups>;
+  auto kernel = attn_simt_kernel<E, kGroups, P>;
   static std::atomic<uint64_t> ready{0};
-  const size_t most = bytes(256, kGroups == 4 ? 128 : 256);
+  const size_t most = bytes(kSharedKeys<P> || kGroups == 2 ? 256 : 128, kGroups == 4 ? 128 : 256);
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), most, &ready);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kGroupThreads * kGroups, bytes(p.D, p.Dv), stream>>>(p, gt, tt, hdr);
+  kernel<<<grid, kGroupThreads * kGroups, bytes(p.D, value_channels(p)), stream>>>(p, gt, tt, hdr);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
+template <class P>
+cudaError_t launch_family(const P& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
   // heads of a group share the CTA's key blocks; what is left of the 16 slots takes more tokens
   const int gt = p.G < kVRows ? p.G : kVRows;
   const int tt = p.mode == kAttnSelected ? 1 : kVRows / gt;
   const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles(p.R, p.S, tt);
   const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
+  const bool narrow = value_channels(p) <= 128;
   if (dtype == KPOOL_BF16)
-    return p.Dv <= 128 ? launch<__nv_bfloat16, 4>(p, grid, gt, tt, hdr, stream)
-                      : launch<__nv_bfloat16, 2>(p, grid, gt, tt, hdr, stream);
-  return p.Dv <= 128 ? launch<float, 4>(p, grid, gt, tt, hdr, stream) : launch<float, 2>(p, grid, gt, tt, hdr, stream);
+    return narrow ? launch<__nv_bfloat16, 4>(p, grid, gt, tt, hdr, stream)
+                  : launch<__nv_bfloat16, 2>(p, grid, gt, tt, hdr, stream);
+  return narrow ? launch<float, 4>(p, grid, gt, tt, hdr, stream) : launch<float, 2>(p, grid, gt, tt, hdr, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
+  return launch_family(p, dtype, ws, stream);
+}
+cudaError_t launch_attn_simt(const AttnPagedParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
+  return launch_family(p, dtype, ws, stream);
+}
+cudaError_t launch_attn_simt(const AttnSharedParams& p, kpool_dtype dtype, char* ws, cudaStream_t stream) {
+  return launch_family(p, dtype, ws, stream);
 }
 
 }  // namespace kpool

@@ -13,7 +13,8 @@
 //            gather of four rows moved 6 bytes a cycle and SM, these copies 27; 2048 rows x
 //            2052 ids of 64 / 1 heads: 1222 against 288 us.)
 //   kDense   kTwo under a mask of bits for all keys (kpool_attn_dense.cu).
-//   kPagedOne, kPagedTwo   kOne and kTwo over a cache in pages.
+//   kPagedOne, kPagedTwo   kOne and kTwo over a cache in pages, a TMA box for what lies in one page;
+//   kPagedRows  decode steps over small pages: as kGather, but for whole caches of any length.
 //
 // Roles (12 warps; kGather 16): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread
 // per row; warp 8 loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns
@@ -77,8 +78,8 @@ constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
 // The forms of the kernel: one or two row tiles of consecutive tokens, one token's heads over gathered keys, or
-// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages.
-enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo };
+// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages, by TMA; a token's heads over pages, by plain copies.
+enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo, kPagedRows };
 
 // Where a tile of the ring lies, and the parity of its use of that slot.
 struct Place {
@@ -90,12 +91,14 @@ struct Place {
 template <int DK, int DV, Form F>
 struct Cfg {
   static constexpr bool TWO = F == kTwo || F == kDense || F == kPagedTwo;
-  static constexpr bool PAGED = F == kPagedOne || F == kPagedTwo;
+  static constexpr bool PAGED = F == kPagedOne || F == kPagedTwo || F == kPagedRows;
   static constexpr bool SHARED = DK != DV;
+  static constexpr bool GATHER = F == kGather || F == kPagedRows;  // keys come by plain copies
+  using Params = std::conditional_t<PAGED, AttnPagedParams, std::conditional_t<SHARED, AttnSharedParams, AttnParams>>;
   // The ring holds K(0) .. K(kAhead - 1), then K(j), V(j - kAhead) in turn: the order in which the MMAs use
   // them, K one tile (one-tile form: one per group) ahead.
   static constexpr int kAhead = TWO ? 1 : 2;
-  static constexpr int kThreads = F == kGather ? 512 : 384;
+  static constexpr int kThreads = GATHER ? 512 : 384;
   static constexpr int kTileBytes = kTileKeys * DK * 2;  // one K tile, one Q tile
   static constexpr int kVBytes = kTileKeys * DV * 2;     // one V tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
@@ -114,7 +117,7 @@ struct Cfg {
   static constexpr int kOffStat = kOffSeg + 64 * kSegRing;         // [2][128] float2 (m, l), one-tile form only
   static constexpr int kOffBits = kOffStat + (TWO ? 0 : 2 * kTileRows * 8);  // [kBitsRing] x 128 bits
   static_assert(kOffBits % 16 == 0 && kOffSeg % 16 == 0 && kOffStat % 16 == 0, "16-byte accesses");
-  static constexpr int kSmem = kOffBits + (F == kGather ? 16 * kBitsRing : 0);
+  static constexpr int kSmem = kOffBits + (GATHER ? 16 * kBitsRing : 0);
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
 
   // Use number u of the ring (of the K or the V ring where they are apart), and a slot's bytes from the ring's start.
@@ -166,7 +169,8 @@ struct Seg {
 };
 static_assert(sizeof(Seg) <= 64, "Seg fits its space");
 
-__device__ __forceinline__ int tile_cost(const AttnParams& p, const AttnSeq& s, int t, int ttb) {
+template <class P>
+__device__ __forceinline__ int tile_cost(const P& p, const AttnSeq& s, int t, int ttb) {
   const int end = attn_keys_end(p, s, min((t + 1) * ttb, s.nq));
   return max(1, (end + kTileKeys - 1) / kTileKeys);
 }
@@ -207,7 +211,8 @@ __device__ __forceinline__ int row_tiles(const AttnSeq& s, int ttb) { return (s.
 
 // Positions of one head's row tiles [0, t), t <= row_tiles: tile u ends at key prefix + (u + 1) ttb
 // (the last at prefix + nq) and counts at least one key tile.
-__device__ __forceinline__ int64_t head_cost(const AttnParams& p, const AttnSeq& s, int t, int ttb) {
+template <class P>
+__device__ __forceinline__ int64_t head_cost(const P& p, const AttnSeq& s, int t, int ttb) {
   if (t == 0) return 0;
   if (!s.ok || s.nk == 0) return int64_t(t) * (kItemCost + 1);
   if (!attn_causal(p)) return int64_t(t) * (kItemCost + (s.nk + kTileKeys - 1) / kTileKeys);
@@ -219,7 +224,8 @@ __device__ __forceinline__ int64_t head_cost(const AttnParams& p, const AttnSeq&
   return c;
 }
 
-__device__ __forceinline__ int64_t seq_cost(const AttnParams& p, const AttnSeq& s, int ttb) {
+template <class P>
+__device__ __forceinline__ int64_t seq_cost(const P& p, const AttnSeq& s, int ttb) {
   return head_cost(p, s, row_tiles(s, ttb), ttb) * p.Hkv;
 }
 
@@ -232,7 +238,8 @@ struct SegIter {
   int b, hk, t, nt, c;     // its sequence, key head and row tile; the head's row tiles, the item's key tiles
   AttnSeq sq;
 
-  __device__ __forceinline__ void start(const AttnParams& p, const Misc* m, int ttb) {
+  template <class P>
+  __device__ __forceinline__ void start(const P& p, const Misc* m, int ttb) {
     pos = m->lo;
     hi = m->hi;
     b = m->b;
@@ -251,7 +258,8 @@ struct SegIter {
     c = tile_cost(p, sq, t, ttb);
   }
   __device__ __forceinline__ int64_t first_tile() const { return item + kItemCost; }
-  __device__ __forceinline__ bool next(const AttnParams& p, int ttb, Seg* s) {
+  template <class P>
+  __device__ __forceinline__ bool next(const P& p, int ttb, Seg* s) {
     if (pos >= hi) return false;
     if (pos == first_tile() + c) {  // the item is done
       item = pos;
@@ -282,11 +290,22 @@ struct SegIter {
 };
 
 // One CTA per row tile: head by head (a head's K and V stay in L2), the deepest row tiles of each first.
-__device__ __forceinline__ bool direct_seg(const AttnParams& p, int ttb, int tiles, Seg* s) {
+template <class P>
+__device__ __forceinline__ bool direct_seg(const P& p, int ttb, int tiles, Seg* s) {
   s->hk = blockIdx.x / tiles;
   const int tile = tiles - 1 - int(blockIdx.x % tiles);
-  const int b = attn_seq_of_tile(p, tile, ttb);
+  int b;
+  if constexpr (kPagedKeys<P>) b = ttb == 1 ? tile : attn_seq_of_tile(p, tile, ttb);  // (a row per sequence)
+  else b = attn_seq_of_tile(p, tile, ttb);
   s->sq = attn_seq(p, b);
+  if constexpr (kPagedKeys<P>)
+    if (ttb == 1) {
+      s->tok0 = s->kt0 = 0;
+      s->n = tile_cost(p, s->sq, 0, 1);
+      s->whole = 1;
+      s->slot = 0;
+      return s->sq.nq > 0;
+    }
   s->tok0 = (tile - (attn_q0(p, b) / ttb + b)) * ttb;
   if (s->tok0 < 0 || s->tok0 >= s->sq.nq) return false;
   s->kt0 = 0;
@@ -333,7 +352,8 @@ __device__ __forceinline__ bool gather_seg(const AttnParams& p, int64_t* pos, in
 }
 
 // The rest of a segment's fields; tt: tokens of a row tile, ttb: of all row tiles of the CTA.
-__device__ __forceinline__ void finish_seg(const AttnParams& p, int tt, int ttb, Seg* s) {
+template <class P>
+__device__ __forceinline__ void finish_seg(const P& p, int tt, int ttb, Seg* s) {
   s->end = attn_keys_end(p, s->sq, min(s->tok0 + ttb, s->sq.nq));
   if (s->end == 0) s->n = 0;
   const int end0 = attn_keys_end(p, s->sq, min(s->tok0 + tt, s->sq.nq));
@@ -360,7 +380,8 @@ struct Cuts {
 
 // Every thread of the CTA: this CTA's run of positions [total * i / n, total * (i + 1) / n)
 // and the sequence it starts in. `scratch` holds S 64-bit words of shared memory.
-__device__ __forceinline__ void find_run(const AttnParams& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas,
+template <class P>
+__device__ __forceinline__ void find_run(const P& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas,
                                          Misc* m) {
   for (int b = threadIdx.x; b < p.S; b += blockDim.x) scratch[b] = seq_cost(p, attn_seq(p, b), ttb);
   __syncthreads();
@@ -444,6 +465,8 @@ __host__ __device__ __forceinline__ int piece_rows(int page_size) {
   return low < kTileKeys ? low : kTileKeys;
 }
 
+constexpr int kPagedBoxRows = 64;  // keys of a TMA box that decode steps want at least
+
 // Bounded wait; also gives up when another role did.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -475,7 +498,8 @@ __device__ __forceinline__ bool group_bar_or(bool flag) {
 // Visibility of 32 keys from key j on to row i of the sequence, as bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-__device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const AttnSeq& s, int i, int j) {
+template <class P>
+__device__ __forceinline__ uint32_t seen_bits(const P& p, const AttnSeq& s, int i, int j) {
   if (p.mask == nullptr) return low_bits(s.prefix + i + 1 - j);
   const int slot = j - s.prefix;  // first of the 32 keys as a node; negative: committed keys come first
   if (slot <= -32) return 0xffffffffu;
@@ -558,10 +582,10 @@ template <int DK, int DV, Form F>
 __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
-                   const __grid_constant__ AttnParams p, int tiles, int direct, float* part, int slot_rows,
+                   const __grid_constant__ typename Cfg<DK, DV, F>::Params p, int tiles, int direct, float* part, int slot_rows,
                    JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<DK, DV, F>;
-  constexpr bool TWO = C::TWO, GATHER = F == kGather, DENSE = F == kDense, PAGED = C::PAGED;
+  constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, LISTED = F == kGather;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     if (threadIdx.x == 0 && !direct) joins[blockIdx.x].runs = 0;
     return;
   }
-  if (GATHER) {
+  if constexpr (LISTED) {
     // (listed rows, mostly none: whole items, so that there is nothing to join)
     const int64_t total = gather_total(p), unit = p.list ? gather_tiles(p) : 1;
     const Cuts cuts(total / unit, gridDim.x);
@@ -650,21 +674,23 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (GATHER && warp == 8) {
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
-        const int64_t hi = misc->hi;
-        int64_t pos = misc->lo;
+        int64_t pos = LISTED ? misc->lo : 0;
+        SegIter it;
+        if (!LISTED && !direct) it.start(p, misc, ttb);
         uint32_t q_loads = 0;
         Seg sg{};
         for (int i = 0;; ++i) {
           const int64_t at = pos;
-          const bool more = gather_seg(p, &pos, hi, &sg);
-          if (i == 0) {
-            const int nt = gather_tiles(p);
-            if (direct || p.list) {
-              // whole items: nothing to join
-            } else if (more) write_join(joins + blockIdx.x, sg, at - sg.kt0, nt, gather_total(p), blockIdx.x,
-                                 gridDim.x);
-            else joins[blockIdx.x].runs = 0;
+          bool more;
+          if constexpr (LISTED) more = gather_seg(p, &pos, misc->hi, &sg);
+          else more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          if (i == 0 && !direct && !p.list) {  // (else whole items: nothing to join)
+            if (!more) joins[blockIdx.x].runs = 0;
+            else if constexpr (LISTED)
+              write_join(joins + blockIdx.x, sg, at - sg.kt0, gather_tiles(p), gather_total(p), blockIdx.x, gridDim.x);
+            else write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
           }
+          if (!LISTED && more) finish_seg(p, tt, ttb, &sg);
           if (!more) sg.n = -1;
           if (i >= kSegRing && !wait_bar(seg_empty + i % kSegRing, (i / kSegRing - 1) & 1, misc)) break;
           ring[i % kSegRing] = sg;
@@ -693,9 +719,13 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       uint32_t fills = 0, tile = 0;
       bool ok = true;
       const Seg* sg;
+      bool bad_page = false;
+      // What the lane reads ahead for its key of a tile: its id, or the page that it lies in.
       auto load_id = [&](int kt) {
         const int j = kt * kTileKeys + w * 32 + lane;
-        return j < p.width ? __ldg(p.ids + int64_t(sg->sq.q0) * p.width + j) : -1;
+        if constexpr (LISTED) return j < p.width ? __ldg(p.ids + int64_t(sg->sq.q0) * p.width + j) : -1;
+        else if constexpr (PAGED) return j < sg->end ? ptx::ldg_ordered(p.table + int64_t(sg->sq.k0) * p.max_pages + j / p.page_size) : -1;
+        else return -1;
       };
       // tok: the lane's key as a token of k and v, -1 where it is not seen
       auto load_kv = [&](const void* src, int64_t hs, uint32_t ts_bytes, int tok, bool is_k) {
@@ -735,7 +765,14 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           tok2 = tok1;
           tok1 = tok;
           if (j < n) {
-            tok = next >= 0 && next < nk ? next + k0 : -1;
+            if constexpr (LISTED) {
+              tok = next >= 0 && next < nk ? next + k0 : -1;
+            } else if constexpr (PAGED) {
+              const int key = (kt0 + j) * kTileKeys + w * 32 + lane;
+              const bool have = next >= 0 && next < p.num_pages;
+              tok = have ? next * p.page_size + key % p.page_size : -1;
+              bad_page |= !have && key < sg->end;
+            }
             if (j + 1 < n) next = load_id(kt0 + j + 1);
             ok = load_kv(p.k, p.k_hs, uint32_t(p.k_ts * 2), tok, true);
           }
@@ -745,6 +782,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
       }
+      if (bad_page) misc->bad_page = 1;
       ptx::cp_async_wait_all();                    // every copy has landed before the CTA exits
     } else if (warp == 8) {  // ------------------------------------------------- TMA producer
       // One lane, or over pages all of them, each with its own pieces of a tile.
@@ -754,6 +792,20 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         uint32_t fills[2] = {0, 0}, q_loads = 0;  // of the ring, or of K's and V's
         bool ok = true, bad_page = false;
         Seg sg{};
+        // Pages of the lane's first piece: of the tile whose K is loaded next, of the tiles before, whose V is; the next one.
+        [[maybe_unused]] int rows = 1, pages[C::kAhead + 1] = {}, next_page = -1;
+        if constexpr (PAGED) rows = piece_rows(p.page_size);
+        auto read_page = [&](int kt) {
+          if constexpr (PAGED) {
+#pragma unroll
+            for (int x = C::kAhead; x > 0; --x) pages[x] = pages[x - 1];
+            pages[0] = next_page;
+            const int j = kt * kTileKeys + lane * rows;
+            next_page = -1;
+            if (lane * rows < kTileKeys && j < sg.end)
+              next_page = ptx::ldg_ordered(p.table + int64_t(sg.sq.k0) * p.max_pages + j / p.page_size);
+          }
+        };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           const bool r = wait_bar(bar, parity, misc);
           return PAGED ? bool(__all_sync(0xffffffffu, r)) : r;
@@ -766,16 +818,21 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           ++f;
           uint8_t* dst = smem + C::kOffRing + C::slot_at(st);
           const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-          if (PAGED) {
+          if constexpr (PAGED) {
             // Pieces of `rows` keys lie in one page each; the keys past the last one that a row sees are not loaded.
-            const int rows = piece_rows(p.page_size), key0 = kt * kTileKeys;
-            const int pieces = min(kTileKeys / rows, (sg.end - key0 + rows - 1) / rows);
+            const int key0 = kt * kTileKeys, pieces = min(kTileKeys / rows, (sg.end - key0 + rows - 1) / rows);
             if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, uint32_t(pieces * rows * 128 * C::kVBlocks));
             __syncwarp();
             for (int x = lane; x < pieces; x += 32) {
-              const int j = key0 + x * rows, page = attn_page(p, sg.sq.k0, j, &bad_page);
+              const int j = key0 + x * rows;
+              int page = is_k ? pages[0] : pages[C::kAhead];  // of the lane's first piece, read ahead
+              if (x >= 32) page = __ldg(p.table + int64_t(sg.sq.k0) * p.max_pages + j / p.page_size);
+              if (page < 0 || page >= p.num_pages) {
+                bad_page = true;
+                page = -1;  // (zeros)
+              }
 #pragma unroll
-              for (int h = 0; h < C::kVBlocks; ++h)  // (page -1: zeros)
+              for (int h = 0; h < C::kVBlocks; ++h)
                 ptx::tma_load_4d(dst + h * C::kHalf + x * rows * 128, tm, full + st, 64 * h, sg.hk, j % p.page_size, page);
             }
           } else {
@@ -817,7 +874,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
                 ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
                                  sg.sq.q0 + sg.tok0 + g * tt);
           }
+          read_page(sg.kt0);
           for (int j = 0; ok && j < sg.n + C::kAhead; ++j) {
+            read_page(sg.kt0 + j + 1);
             if (j < sg.n) ok = load_kv(true, sg.kt0 + j);
             if (ok && j >= C::kAhead) ok = load_kv(false, sg.kt0 + j - C::kAhead);
           }
@@ -1227,7 +1286,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           for (int j = j0; j < j1; ++j) {
             if (!attn_sees(p, sg->sq, i, j)) continue;
             int64_t at = (int64_t(sg->sq.k0) + j) * p.v_ts;
-            if (PAGED) {
+            if constexpr (PAGED) {
               bool none_such = false;
               const int page = attn_page(p, sg->sq.k0, j, &none_such);
               if (none_such) continue;
@@ -1446,9 +1505,9 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int DK, int DV, Form F>
-cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
+cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStream_t stream) {
   using C = Cfg<DK, DV, F>;
-  constexpr bool GATHER = F == kGather;
+  constexpr bool GATHER = C::GATHER, LISTED = F == kGather;
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -1457,7 +1516,7 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), DK, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
     return cudaErrorInvalidValue;
   tk = tv = tr = tq;  // (gathered: not used, keys and values come by plain copies)
-  if (C::PAGED) {
+  if constexpr (C::PAGED && !GATHER) {
     const uint32_t rows = uint32_t(piece_rows(p.page_size));
     if (!make_tmap_bf16_pages(&tk, p.k, uint64_t(p.num_pages), uint64_t(p.page_size), uint64_t(p.Hkv), DK, p.k_ps, p.k_ts,
                               p.k_hs, rows) ||
@@ -1468,8 +1527,9 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
     if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), DV, p.k_ts, p.k_hs, kTileKeys, 1) ||
         !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), DV, p.v_ts, p.v_hs, kTileKeys, 1))
       return cudaErrorInvalidValue;
-    if (C::SHARED && !make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, kTileKeys, 1))
-      return cudaErrorInvalidValue;
+    if constexpr (C::SHARED)
+      if (!make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, kTileKeys, 1))
+        return cudaErrorInvalidValue;
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
   const int64_t items = tiles * p.Hkv;
@@ -1484,14 +1544,14 @@ cudaError_t launch(const AttnParams& p, char* ws, cudaStream_t stream) {
   //    6.5 ms;
   //  - for gathered items, all of the same tiles, where their rounding up to the SMs costs less than the join.
   const int64_t nt = (p.width + kTileKeys - 1) / kTileKeys;
-  const bool even = GATHER && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
-  const bool small = !p.list && (even || ((GATHER ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
+  const bool even = LISTED && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
+  const bool small = !p.list && (even || ((LISTED ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
   const bool like = F == kTwo && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
   const bool deep = C::TWO && items >= int64_t(kAttnDirectItems) * sms && p.T >= int64_t(kAttnDirectKeys) * p.S;
-  const bool direct = !GATHER && (small || like || deep || p.S > kAttnMaxRunSeqs);
+  const bool direct = !LISTED && (small || like || deep || p.S > kAttnMaxRunSeqs);
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
   int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
-  if (GATHER && !small && !p.list) grid = int(run_count(items * nt, grid));
+  if (LISTED && !small && !p.list) grid = int(run_count(items * nt, grid));
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles);
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
   float* part = reinterpret_cast<float*>(joins + kAttnMaxRuns);
@@ -1572,13 +1632,29 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
   //    8,192 316 / 404, of 512 rows 221 / 273; 16 over 8,000 and a prompt of 2,048 129 / 147; 8 trees of 1 to 64
   //    nodes 98 / 97.
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);
-  if (p.kr) return two ? launch<192, 128, kTwo>(p, ws, stream) : launch<192, 128, kOne>(p, ws, stream);
-  if (p.table) {
-    if (p.D == 64) return two ? launch<64, 64, kPagedTwo>(p, ws, stream) : launch<64, 64, kPagedOne>(p, ws, stream);
-    return two ? launch<128, 128, kPagedTwo>(p, ws, stream) : launch<128, 128, kPagedOne>(p, ws, stream);
-  }
   if (p.D == 64) return two ? launch<64, 64, kTwo>(p, ws, stream) : launch<64, 64, kOne>(p, ws, stream);
   return two ? launch<128, 128, kTwo>(p, ws, stream) : launch<128, 128, kOne>(p, ws, stream);
+}
+
+cudaError_t launch_attn_tc(const AttnPagedParams& p, char* ws, cudaStream_t stream) {
+  // Decode steps over small pages by plain copies, where the pages follow one another in memory: a TMA box of 16 keys or
+  // fewer moves what it names no faster than one of 64 (PAGED_TIMES).
+  const bool rows = p.cu_q == nullptr && piece_rows(p.page_size) < kPagedBoxRows &&
+                    p.k_ps == p.page_size * p.k_ts && p.v_ps == p.page_size * p.v_ts &&
+                    int64_t(p.num_pages) * p.page_size <= INT32_MAX && attn_gather_supported(p.k_ts, p.v_ts);
+  const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);  // (as above)
+  if (p.D == 64)
+    return rows  ? launch<64, 64, kPagedRows>(p, ws, stream)
+           : two ? launch<64, 64, kPagedTwo>(p, ws, stream)
+                 : launch<64, 64, kPagedOne>(p, ws, stream);
+  return rows  ? launch<128, 128, kPagedRows>(p, ws, stream)
+         : two ? launch<128, 128, kPagedTwo>(p, ws, stream)
+               : launch<128, 128, kPagedOne>(p, ws, stream);
+}
+
+cudaError_t launch_attn_tc(const AttnSharedParams& p, char* ws, cudaStream_t stream) {
+  const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);  // (as above)
+  return two ? launch<192, 128, kTwo>(p, ws, stream) : launch<192, 128, kOne>(p, ws, stream);
 }
 
 }  // namespace kpool
