@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "kpool_latent.cuh"
 #include "kpool_ptx.cuh"
 
@@ -45,6 +47,12 @@ constexpr int kBlock = kKeys * 128;          // bytes of 64 channels of a tile, 
 constexpr int kBlocks = kDim / 64;
 constexpr int kTileBytes = kBlocks * kBlock;
 constexpr int kStages = 2;
+// A tile's parts, in the order in which they are freed and copied: the rotated block, which nothing reads after the
+// scores, then the 128-channel blocks of the second product. (Scored part by part as they land, a tile's first product
+// takes 2,300 cycles instead of 1,250: 200 a wait and the start of its steps.)
+constexpr int kParts = 1 + kLatent / 128;
+__host__ __device__ constexpr int part_block(int c) { return c == 0 ? kLatent / 64 : 2 * (c - 1); }  // first 64-channel block
+__host__ __device__ constexpr int part_blocks(int c) { return c == 0 ? 1 : 2; }
 constexpr int kSoftWarps = 8, kCopyWarps = 4, kMmaWarp = kSoftWarps + kCopyWarps, kSegWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSegWarp + 1);
 constexpr int kCopyRows = kKeys / kCopyWarps;  // tokens of a tile that a warp copies
@@ -60,10 +68,13 @@ constexpr int kOffTiles = kTileBytes;
 constexpr int kOffP = kOffTiles + kStages * kTileBytes;
 constexpr int kOffMax = kOffP + kBlock;                  // [2][2][64] fp32: maxima of a tile's halves; sums at the end
 constexpr int kOffSeg = kOffMax + 4 * kHeads * 4;
-constexpr int kOffBits = kOffSeg + 48 * kSegRing;        // [kStages] x 64 bits: tokens of a tile that are seen
-constexpr int kOffBar = kOffBits + 8 * kStages;
-// full[2] empty[2] q_full q_empty s_full[2] p_ready p_empty o_final o_free done seg_full[4] seg_empty[4]
-constexpr int kNumBars = 2 * kStages + 9 + 2 * kSegRing;
+// [kBitsRing] x 64 bits, the tokens of a tile that are seen. A tile's are written when the scores of the tile kStages
+// before are done, and read by its softmax; scores are at most one tile ahead of it.
+constexpr int kBitsRing = 4;
+constexpr int kOffBits = kOffSeg + 48 * kSegRing;
+constexpr int kOffBar = kOffBits + 8 * kBitsRing;
+// full[2] empty[2][5] q_full q_empty s_full[2] p_ready p_empty o_final o_free done seg_full[4] seg_empty[4]
+constexpr int kNumBars = kStages * (1 + kParts) + 9 + 2 * kSegRing;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 constexpr int kSmem = kOffMisc + 72;
 static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
@@ -179,7 +190,7 @@ __device__ __forceinline__ void find_run(const LatentParams& p, int64_t* scratch
 // Rows of a partial result of `per` heads: their 16-byte words stay aligned.
 __host__ __device__ __forceinline__ int part_rows(int per) { return (per + 15) & ~15; }
 
-// What the join of the row that the border before a run cuts needs; runs = 0: nothing to join here.
+// What the join of a row that several runs have parts of needs; runs = 0: nothing to join.
 struct JoinItem {
   int64_t item;       // position of the row's first tile
   int64_t each;       // Cuts of the call
@@ -187,8 +198,10 @@ struct JoinItem {
   int32_t tiles;
   int32_t runs;
   int32_t row;
+  int32_t first;      // the run that has the row's first tile
+  int32_t pad[3];
 };
-static_assert(sizeof(JoinItem) == 32, "join items are laid out in the workspace");
+static_assert(sizeof(JoinItem) == 48, "join items are laid out in the workspace");
 
 // The segments of a run: whole rows, `step` apart, or the rows of its positions.
 struct SegIter {
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
-  uint64_t* q_full = empty + kStages;
+  uint64_t* q_full = empty + kStages * kParts;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;   // [2]
   uint64_t* p_ready = q_full + 4;
@@ -272,10 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(full + i, kCopyWarps);
-      ptx::mbar_init(empty + i, 1);
-    }
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(full + i, kCopyWarps);
+    for (int i = 0; i < kStages * kParts; ++i) ptx::mbar_init(empty + i, 1);
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
     ptx::mbar_init(s_full, 1);
@@ -326,22 +337,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           more = it.next(p, &s);
         }
-        if (i == 0 && !direct && group == 0) {
-          // The join of a cut row is left to the first run that begins inside it.
-          JoinItem j{};
-          if (more && s.kt0 > 0) {
+        if (!direct && group == 0) {
+          // The run that begins a row leaves its join: with fewer rows than runs in the row's place, else in the run's
+          // own (only the last row that it begins can be cut).
+          const bool by_row = p.R <= runs;
+          if (more && s.kt0 == 0) {
             const Cuts cuts(misc->total, uint32_t(misc->runs));
+            JoinItem j{};
             j.item = it.item + kRowCost;
-            bool own = true;
-            const int64_t pos = cuts.lo(run);
-            for (int b = run - 1; own && b > 0 && cuts.lo(b) > j.item; --b) own = cuts.lo(b) == pos;
             j.each = cuts.each;
             j.rest = cuts.rest;
             j.tiles = it.c;
-            j.runs = own ? misc->runs : 0;
+            j.runs = s.whole ? 0 : misc->runs;
             j.row = s.row;
+            j.first = run;
+            joins[by_row ? s.row : run] = j;
+          } else if (!by_row && i == 0) {
+            joins[run].runs = 0;
           }
-          joins[run] = j;
         }
         if (more) {
           s.keys = latent_seq(p, s.row, &s.seq);
@@ -389,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && !(ok = wait(q_full, q_uses & 1))) break;
       int scored = 0;  // tiles of the segment whose scores are issued
       auto score = [&](uint32_t v) {
+        ptx::fence_proxy_async_smem();  // the tile may have been written by ordinary copies
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = c_desc + v % kStages * (kTileBytes >> 4);
@@ -399,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_mma_f16(to, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
           }
           ptx::tc_commit(s_full + (v & 1));
+          ptx::tc_commit(empty + v % kStages * kParts);
           if (scored == n - 1) ptx::tc_commit(q_empty);
         }
         __syncwarp();
@@ -410,17 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(full + st, (u / kStages) & 1))) break;
           score(u);
         }
-        // While the weights are made, the next scores if their tile is there by then: the second product frees
-        // the slot of the tile after, so it does not wait for the next one to land.
+        // While the weights are made, the next scores if their tile is there by then: the second product frees the
+        // slot of the tile after, so it does not wait for the next one to land.
         const uint64_t t0 = ptx::globaltimer_ns();
-        while (!__all_sync(0xffffffffu, ptx::mbar_test(p_ready, u & 1))) {
+        while (ok && !__all_sync(0xffffffffu, ptx::mbar_test(p_ready, u & 1))) {
           if (scored == j + 1 && scored < n &&
               __all_sync(0xffffffffu, ptx::mbar_test(full + (u + 1) % kStages, ((u + 1) / kStages) & 1)))
             score(u + 1);
-          if (__any_sync(0xffffffffu, misc->abort || ptx::globaltimer_ns() - t0 > kMaxWaitNs)) {
-            ok = false;
-            break;
-          }
+          if (__any_sync(0xffffffffu, misc->abort || ptx::globaltimer_ns() - t0 > kMaxWaitNs)) ok = false;
         }
         if (!ok) {
           misc->abort = 1;
@@ -431,12 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ptx::elect_one()) {
           const uint64_t a = v_desc + st * (kTileBytes >> 4);
 #pragma unroll
-          for (int c = 0; c < kLatent / 128; ++c)
+          for (int c = 0; c < kLatent / 128; ++c) {
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
               ptx::tc_mma_f16(acc + 64 * c, a + ((2 * c * kBlock + kk * 2048) >> 4), p_desc + (kk * 32 >> 4), idesc_o,
                               (kk > 0 || j > 0) ? 1u : 0u);
-          ptx::tc_commit(empty + st);
+            ptx::tc_commit(empty + st * kParts + c + 1);
+          }
           ptx::tc_commit(p_empty);
           if (j == n - 1) ptx::tc_commit(o_final);
         }
@@ -450,22 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
   } else if (warp >= kSoftWarps) {  // --------------------------------------- copying warps
     // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each. Whole
-    // tiles of a cache in pages of 16 tokens and more come by TMA instead, a box in four from each warp. Where a tile's tokens
-    // lie is looked up while the tile before is on its way: ids two tiles ahead, pages one.
+    // tiles of a cache in pages of 16 tokens and more come by TMA instead, a box in four from each warp. Where a tile's
+    // tokens lie is looked up while the tile before is on its way: ids two tiles ahead, pages one.
     const int w = warp - kSoftWarps, c = lane & 7, sub = lane >> 3;
-    const int box = lane < 9 ? kCopyWarps * lane + w : kCopyWarps * 9;  // of 9 to 36 in a tile
     const char* base = static_cast<const char*>(p.cache) + c * 16;
     const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * kCopyRows + sub) * 128;
     uint32_t u = 0, by_tma_at[kStages] = {};  // 1 + the last tile of a slot where TMA brought it
-    bool ok = true, bad = false, held = false;  // held: the tile before has been copied, but not waited for
+    bool ok = true, bad = false;
     const Seg* s;
-    // Copies are waited for here, where they are also made known to the tensor core: a fence in the issuing warp
-    // would wait for the products in flight.
-    auto land = [&](uint32_t v) {
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full + v % kStages);
-    };
     for (int i = 0;; ++i) {
       s = segment(i);
       if (!__all_sync(0xffffffffu, s != nullptr) || s->n < 0) break;
@@ -473,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = p.table + int64_t(s->seq) * p.max_pages;
       const int32_t* ids = p.ids + int64_t(s->row) * p.width;
       auto by_tma = [&](int j) { return box_rows > 0 && (kt0 + j + 1) * kKeys <= end; };
-      // The token (of the sequence) that the lane looks up for tile j: lanes 0-15 the warp's rows of a copied tile,
-      // lanes 0-8 the first token of the piece of their TMA box; -1: none.
+      // The token (of the sequence) that the lane looks up for tile j: lanes 0-15 the warp's rows of a copied tile, lanes
+      // 0-3 the first of the pieces that TMA takes; -1: none.
       auto id_of = [&](int j) {
         const int first = (kt0 + j) * kKeys;
         if (j >= n) return -1;
-        if (by_tma(j)) return box < pieces * kBlocks ? first + box / kBlocks * box_rows : -1;
+        if (by_tma(j)) return lane < pieces ? first + lane * box_rows : -1;
         const int place = first + w * kCopyRows + lane;
         if (lane >= kCopyRows || place >= end) return -1;
         return latent_listed(p) ? ptx::ldg_ordered(ids + place) : place;
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_up();
         id1 = id_of(1);
       }
-      for (int j = 0; j < n; ++j, ++u) {
+      for (int j = 0; ok && j < n; ++j, ++u) {
         const uint32_t st = u % kStages;
         const bool tma = by_tma(j);
         if (id >= 0 && (page < 0 || page >= p.num_pages)) {
@@ -505,57 +510,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         // everything but the copies themselves comes before the slot is free
         const char* from[kCopyRows / 4];
         uint32_t bytes[kCopyRows / 4];
-        {
-          const int64_t at = page >= 0 ? int64_t(page) * p.c_ps + int64_t(in_page) * p.c_ts : -1;
+        const int64_t at = page >= 0 ? int64_t(page) * p.c_ps + int64_t(in_page) * p.c_ts : -1;
 #pragma unroll
-          for (int q = 0; q < kCopyRows / 4; ++q) {
-            const int64_t t = __shfl_sync(0xffffffffu, at, 4 * q + sub);
-            from[q] = base + (t >= 0 ? t : 0) * 2;
-            bytes[q] = t >= 0 ? 16u : 0u;
-            asm volatile("" : "+l"(from[q]), "+r"(bytes[q]));
-          }
+        for (int q = 0; q < kCopyRows / 4; ++q) {
+          const int64_t t = __shfl_sync(0xffffffffu, at, 4 * q + sub);
+          from[q] = base + (t >= 0 ? t : 0) * 2;
+          bytes[q] = t >= 0 ? 16u : 0u;
         }
-        if (u >= kStages) ok = __all_sync(0xffffffffu, wait_bar(empty + st, (u / kStages - 1) & 1, misc));
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) reinterpret_cast<uint16_t*>(smem + kOffBits)[4 * st + w] = uint16_t(bits);
-        if (tma) {
-          const int boxes = (pieces * kBlocks - w + kCopyWarps - 1) / kCopyWarps;
-          if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, uint32_t(boxes * box_rows * 128));
-          __syncwarp();
-          if (lane < boxes) {
-            const int piece = box / kBlocks, h = box - piece * kBlocks;
-            ptx::tma_load_4d(smem + kOffTiles + st * kTileBytes + h * kBlock + piece * box_rows * 128, &tm_c, full + st, 64 * h,
-                             0, in_page, page);  // (page -1: zeros)
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < kCopyRows / 4; ++q) {
-            // the row's number modulo eight permutes its 16-byte pieces
-            const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ ((q * 4 + sub) & 7)) << 4);
-#pragma unroll
-            for (int h = 0; h < kBlocks; ++h) ptx::cp_async_16(dst + h * kBlock, from[q] + h * 128, bytes[q]);
-          }
-          ptx::cp_async_commit();
-        }
+        const int box_page = page, box_in = in_page;  // (lanes 0-3)
         if (j + 1 < n) {
           look_up();
           id1 = id_of(j + 2);
         }
         by_tma_at[st] = tma ? u + 1 : 0;
-        if (!tma && j + 1 < n && u + 1 < kStages) {  // (the first tiles: the next slot is free)
-          held = true;
-          continue;
+        // TMA: a box is a block of 64 channels of a piece; this warp takes every fourth of a part's
+        int boxes = 0;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) boxes += (pieces * part_blocks(part) - w + kCopyWarps - 1) / kCopyWarps;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          if (u >= kStages)
+            ok = __all_sync(0xffffffffu, wait_bar(empty + st * kParts + part, (u / kStages - 1) & 1, misc));
+          if (!ok) break;
+          __syncwarp();
+          if (part == 0 && lane == 0) {
+            reinterpret_cast<uint16_t*>(smem + kOffBits)[4 * (u % kBitsRing) + w] = uint16_t(bits);
+            // (not before the slot's last tile is scored: its phase has to be over; the arrival follows the last part)
+            if (tma) ptx::mbar_expect_tx(full + st, uint32_t(boxes * box_rows * 128));
+          }
+          if (part == 0) __syncwarp();
+          if (tma) {
+            const int box = kCopyWarps * lane + w, piece = box / part_blocks(part), h = part_block(part) + box % part_blocks(part);
+            const int z = __shfl_sync(0xffffffffu, box_in, piece & 3), y = __shfl_sync(0xffffffffu, box_page, piece & 3);
+            if (box < pieces * part_blocks(part))  // (page -1: zeros)
+              ptx::tma_load_4d(smem + kOffTiles + st * kTileBytes + h * kBlock + piece * box_rows * 128, &tm_c, full + st,
+                               64 * h, 0, z, y);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kCopyRows / 4; ++q) {
+              // the row's number modulo eight permutes its 16-byte pieces
+              const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ ((q * 4 + sub) & 7)) << 4);
+#pragma unroll
+              for (int h = part_block(part); h < part_block(part) + part_blocks(part); ++h)
+                ptx::cp_async_16(dst + h * kBlock, from[q] + h * 128, bytes[q]);
+            }
+          }
         }
-        if (held) {
-          if (tma) ptx::cp_async_wait<0>();
-          else ptx::cp_async_wait<1>();
-          land(u - 1);
-          held = false;
-        }
-        if (tma) continue;
-        ptx::cp_async_wait<0>();
-        land(u);
+        if (!ok) break;
+        if (!tma) ptx::cp_async_arrive_inc(full + st);  // the phase waits for this lane's pieces
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full + st);
       }
       if (!ok) break;
       __syncwarp();
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         uint32_t s[16];
         ptx::tc_ld_16x256b_x4(tmem + 256 + 64 * (u & 1) + lanes + 32 * half, s);
-        const uint32_t bits = *reinterpret_cast<const volatile uint32_t*>(smem + kOffBits + 8 * (u % kStages) + 4 * half);
+        const uint32_t bits = *reinterpret_cast<const volatile uint32_t*>(smem + kOffBits + 8 * (u % kBitsRing) + 4 * half);
         ptx::tc_wait_ld();
         ptx::tc_reg_fence(s);
         if (bits != 0xffffffffu) {
@@ -777,92 +781,80 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------- join
 //
-// CTA x adds up, in the order of the runs, the partial results of the row that the border before run x + 1 cuts
-// (if that run was the first to begin inside it). kShare warps have one head, each every kShare-th run; a lane
-// holds 16 of the 512 channels.
-template <int kShare>
+// CTA x adds up, in the order of the runs, the partial results of the row that item x names. A warp has a quarter
+// of a head's channels, four a lane, and reads eight runs at a time; kShare: the 8 warps of a CTA share one quarter,
+// each taking every eighth run (few rows, each cut into many runs), else each has its own. What is read was just written:
+// 131 KB a run and 64 heads, 38 MB for 16 rows over 152 runs, at most.
+constexpr int kQuarters = kLatent / 128;
+constexpr int kJoinBatch = 8;
+
+template <bool kShare>
 __global__ void __launch_bounds__(256)
-    latent_join_kernel(const __grid_constant__ LatentParams p, int per, int groups, const JoinItem* joins,
+    latent_join_kernel(const __grid_constant__ LatentParams p, int per, int groups, int runs, const JoinItem* joins,
                        const float* part) {
-  constexpr int kPer = kLatent / 32, kHeadsCta = 8 / kShare;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
-  const JoinItem it = joins[blockIdx.x + 1];
-  if (it.runs == 0) return;
+  const JoinItem it = joins[blockIdx.x];
+  // (after a wait that ran out an item may never have been written)
+  if (it.runs <= 0 || it.runs > runs || it.first < 0 || it.first >= runs || it.row < 0 || it.row >= p.R) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int in_cta = warp / kShare, share = warp % kShare;
-  const int head = int(blockIdx.y) * kHeadsCta + in_cta;   // of the call
+  const int unit = kShare ? int(blockIdx.y) : int(blockIdx.y) * 8 + warp;
+  const int head = unit / kQuarters, ch = unit % kQuarters * 128 + 4 * lane;
   const int group = head / per, h = head - group * per;
   const bool live = head < p.H;
   auto run_lo = [&](int r) { return it.each * r + it.rest * uint32_t(r) / uint32_t(it.runs); };
-  int first = blockIdx.x;
-  while (first > 0 && run_lo(first) > it.item) --first;
   const float c2 = p.scale * kLog2e;
   const int64_t end = it.item + it.tiles;
-  float acc[kPer], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int y = 0; y < kPer; ++y) acc[y] = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.0f;
   // adds a part (o, pm, pl); one without any weight adds nothing, with a NaN among its scores its sum passes on
-  auto add = [&](const float (&o)[kPer], float pm, float pl) {
+  auto add = [&](const float4& o, float pm, float pl) {
     const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
     const float f = m == -INFINITY ? 1.0f : exp2f((m - base) * c2);
     const float w = pm == -INFINITY ? 1.0f : exp2f((pm - base) * c2);
     l = l * f + pl * w;
-#pragma unroll
-    for (int y = 0; y < kPer; ++y) acc[y] = acc[y] * f + o[y] * w;
+    acc.x = acc.x * f + o.x * w;
+    acc.y = acc.y * f + o.y * w;
+    acc.z = acc.z * f + o.z * w;
+    acc.w = acc.w * f + o.w * w;
     m = mn;
   };
-  const int slots = part_rows(per);
+  const int slots = part_rows(per), step = kShare ? 8 : 1;
   const size_t stride = size_t(slots) * (kLatent + 2);
-  for (int r = first + share; live && r < it.runs && run_lo(r) < end; r += kShare) {
-    const int64_t lo = run_lo(r), hi = run_lo(r + 1);
-    if (!(hi > it.item && hi > lo)) continue;
-    const float* s = part + ((size_t(r) * groups + group) * 2 + (lo > it.item ? 0 : 1)) * stride;
-    const float2 ml = *reinterpret_cast<const float2*>(s + size_t(slots) * kLatent + 2 * h);
-    float o[kPer];
+  for (int r0 = it.first + (kShare ? warp : 0); live && r0 < it.runs && run_lo(r0) < end; r0 += step * kJoinBatch) {
+    float4 o[kJoinBatch];
+    float2 ml[kJoinBatch];
+    bool has[kJoinBatch];
 #pragma unroll
-    for (int y = 0; y < kPer; y += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(s + size_t(h) * kLatent + 32 * y + 4 * lane);
-      o[y] = f.x;
-      o[y + 1] = f.y;
-      o[y + 2] = f.z;
-      o[y + 3] = f.w;
+    for (int b = 0; b < kJoinBatch; ++b) {
+      const int r = r0 + b * step;
+      const int64_t lo = run_lo(r), hi = run_lo(r + 1);
+      has[b] = r < it.runs && lo < end && hi > it.item && hi > lo;
+      if (!has[b]) continue;
+      const float* s = part + ((size_t(r) * groups + group) * 2 + (r == it.first ? 1 : 0)) * stride;
+      ml[b] = __ldcg(reinterpret_cast<const float2*>(s + size_t(slots) * kLatent + 2 * h));
+      o[b] = __ldcg(reinterpret_cast<const float4*>(s + size_t(h) * kLatent + ch));
     }
-    add(o, ml.x, ml.y);
-  }
-  if (kShare > 1) {  // the first warp adds the others' parts in their order
-    __shared__ float s_o[8][kLatent];
-    __shared__ float2 s_ml[8];
 #pragma unroll
-    for (int y = 0; y < kPer; y += 4)
-      *reinterpret_cast<float4*>(&s_o[warp][32 * y + 4 * lane]) = make_float4(acc[y], acc[y + 1], acc[y + 2], acc[y + 3]);
+    for (int b = 0; b < kJoinBatch; ++b)
+      if (has[b]) add(o[b], ml[b].x, ml[b].y);
+  }
+  if (kShare) {  // the first warp adds the others' parts in their order
+    __shared__ float4 s_o[8][32];
+    __shared__ float2 s_ml[8];
+    s_o[warp][lane] = acc;
     if (lane == 0) s_ml[warp] = make_float2(m, l);
     __syncthreads();
-    if (share != 0) return;
-    for (int x = 1; x < kShare; ++x) {
-      float o[kPer];
-#pragma unroll
-      for (int y = 0; y < kPer; y += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&s_o[warp + x][32 * y + 4 * lane]);
-        o[y] = f.x;
-        o[y + 1] = f.y;
-        o[y + 2] = f.z;
-        o[y + 3] = f.w;
-      }
-      add(o, s_ml[warp + x].x, s_ml[warp + x].y);
-    }
+    if (warp != 0) return;
+    for (int x = 1; x < 8; ++x) add(s_o[x][lane], s_ml[x].x, s_ml[x].y);
   }
   if (!live) return;
   const bool none = m == -INFINITY && l == 0.0f;
   const float inv = none ? 0.0f : 1.0f / l;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(it.row) * p.o_ts + head * p.o_hs;
-#pragma unroll
-  for (int y = 0; y < kPer; y += 4) {
-    uint2 v = make_uint2(0, 0);
-    if (!none)
-      v = make_uint2(ptx::pack_bf16(acc[y] * inv, acc[y + 1] * inv), ptx::pack_bf16(acc[y + 2] * inv, acc[y + 3] * inv));
-    *reinterpret_cast<uint2*>(out + 32 * y + 4 * lane) = v;
-  }
-  if (lane == 0 && p.lse) p.lse[int64_t(it.row) * p.H + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+  uint2 v = make_uint2(0, 0);
+  if (!none) v = make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(it.row) * p.o_ts + head * p.o_hs + ch) = v;
+  if (lane == 0 && ch == 0 && p.lse)
+    p.lse[int64_t(it.row) * p.H + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
 }
 
 // Heads split evenly over CTAs of at most 64, whole sixteens where there are several.
@@ -921,9 +913,10 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || runs < 2) return e;
   cudaLaunchConfig_t cfg{};
-  // many runs to a row: a CTA's warps share its heads; else each has its own
-  const bool share = int64_t(p.R) * 4 <= runs;
-  cfg.gridDim = dim3(uint32_t(runs - 1), uint32_t(share ? p.H : (p.H + 7) / 8));
+  // many runs to a row: a CTA's warps share a quarter of a head; else each has its own
+  const bool share = int64_t(p.R) * 2 * kJoinBatch <= runs;
+  const int units = p.H * kQuarters;
+  cfg.gridDim = dim3(uint32_t(p.R <= runs ? p.R : runs), uint32_t(share ? units : (units + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -931,7 +924,7 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<8> : latent_join_kernel<1>, p, per, groups,
+  e = cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<true> : latent_join_kernel<false>, p, per, groups, runs,
                          static_cast<const JoinItem*>(joins), static_cast<const float*>(part));
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -38,6 +38,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
       : "memory");
 }
 
+// More bytes for the present phase to wait for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
 // One poll; the hardware may suspend the thread for up to ~1 ms (suspend-time
 // hint) while the phase is incomplete and wakes it when the phase completes.
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
@@ -142,11 +147,10 @@ __device__ __forceinline__ void cp_async_16_at(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(dst), "l"(src), "n"(kOffset) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the last kLast groups of copies have landed.
-template <int kLast>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLast) : "memory");
+// The present phase of `bar` does not end before all this thread's earlier cp_async_16 have landed; the arrivals that
+// it expects are not changed. (Another arrival of the thread's warp has to follow.)
+__device__ __forceinline__ void cp_async_arrive_inc(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // This thread's arrival on `bar` once all its earlier cp_async_16 have landed (counts as one arrival).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
