@@ -427,17 +427,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // While the weights are made, the next scores if their tile is there by then: the second product frees the
         // slot of the tile after, so it does not wait for the next one to land.
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (ok && !__all_sync(0xffffffffu, ptx::mbar_test(p_ready, u & 1))) {
-          if (scored == j + 1 && scored < n &&
-              __all_sync(0xffffffffu, ptx::mbar_test(full + (u + 1) % kStages, ((u + 1) / kStages) & 1)))
-            score(u + 1);
-          if (__any_sync(0xffffffffu, misc->abort || ptx::globaltimer_ns() - t0 > kMaxWaitNs)) ok = false;
+        if (scored < n && scored == j + 1) {
+          const uint64_t t0 = ptx::globaltimer_ns();
+          for (int polls = 1; !__all_sync(0xffffffffu, ptx::mbar_test(p_ready, u & 1)); ++polls) {
+            if (__all_sync(0xffffffffu, ptx::mbar_test(full + (u + 1) % kStages, ((u + 1) / kStages) & 1))) {
+              score(u + 1);
+              break;
+            }
+            if ((polls & 255) == 0 && __any_sync(0xffffffffu, misc->abort || ptx::globaltimer_ns() - t0 > kMaxWaitNs)) break;
+          }
         }
-        if (!ok) {
-          misc->abort = 1;
-          break;
-        }
+        if (!(ok = wait(p_ready, u & 1))) break;
         if (j == 0 && q_uses > 0 && !(ok = wait(o_free, (q_uses - 1) & 1))) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -626,8 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
           if (t == 0) mx[half * kHeads + row0 + 8 * h] = mt;
         }
-        // the second product of the tile before is done: O is at rest, and P may be written
-        if (u > 0 && !__all_sync(0xffffffffu, wait_bar(p_empty, (u - 1) & 1, misc))) misc->dead[u & 1] = 1;
         soft_sync();
         if (misc->dead[u & 1]) {
           ok = false;
@@ -640,8 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           top[h] = fmaxf(mx[lane + 32 * h], mx[kHeads + lane + 32 * h]);
           grow[h] = top[h] > m[h] && (top[h] - m[h]) * c2 > kLazy;
         }
-        if (__any_sync(0xffffffffu, grow[0] || grow[1])) {  // (the same in every warp)
-          float f[2];
+        const bool rescale = __any_sync(0xffffffffu, grow[0] || grow[1]);  // (the same in every warp)
+        float f[2];
+        if (rescale) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             f[h] = grow[h] ? ptx::exp2_approx((m[h] - top[h]) * c2) : 1.0f;
@@ -653,37 +652,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mine = own(m, h);
             nb[h] = mine == -INFINITY ? 0.0f : -mine * c2;
           }
-          if (j > 0) {
-            ptx::tc_fence_after();
-            const int per_block = cols / 16;
-#pragma unroll 1
-            for (int x = 0; x < 2 * per_block; ++x) {
-              const int c = 2 * half + x / per_block, col = (x % per_block) * 16;
-              const uint32_t at = tmem + lanes + 64 * c + col;
-              uint32_t o[16];
-              ptx::tc_ld_32x32b_x16(at, o);
-              ptx::tc_wait_ld();
-              ptx::tc_reg_fence(o);
-#pragma unroll
-              for (int y = 0; y < 16; ++y)
-                o[y] = __float_as_uint(__uint_as_float(o[y]) *
-                                       __shfl_sync(0xffffffffu, col < 32 ? f[0] : f[1], (col & 31) + y));
-              ptx::tc_st_32x32b_x16(at, o);
-            }
-            ptx::tc_wait_st();
-          }
         }
+        uint32_t weights[2][4];
         if (live) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const float a = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h]), c2, nb[h]));
               const float b = ptx::exp2_approx(fmaf(__uint_as_float(s[4 * x + 2 * h + 1]), c2, nb[h]));
               l[h] += a + b;
-              *reinterpret_cast<uint32_t*>(p_row + h * 1024 + (((4 * half + x) ^ g) << 4)) = ptx::pack_bf16(a, b);
+              weights[h][x] = ptx::pack_bf16(a, b);
             }
+        }
+        // When the second product of the tile before is done, O is at rest and P may be written. (A warp whose wait runs
+        // out says so at the next barrier; the others' waits then end, too.)
+        if (u > 0 && !__all_sync(0xffffffffu, wait_bar(p_empty, (u - 1) & 1, misc))) misc->dead[(u + 1) & 1] = 1;
+        if (rescale && j > 0) {
+          ptx::tc_fence_after();
+          const int per_block = cols / 16;
+#pragma unroll 1
+          for (int x = 0; x < 2 * per_block; ++x) {
+            const int c = 2 * half + x / per_block, col = (x % per_block) * 16;
+            const uint32_t at = tmem + lanes + 64 * c + col;
+            uint32_t o[16];
+            ptx::tc_ld_32x32b_x16(at, o);
+            ptx::tc_wait_ld();
+            ptx::tc_reg_fence(o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              o[y] = __float_as_uint(__uint_as_float(o[y]) *
+                                     __shfl_sync(0xffffffffu, col < 32 ? f[0] : f[1], (col & 31) + y));
+            ptx::tc_st_32x32b_x16(at, o);
           }
+          ptx::tc_wait_st();
+        }
+        if (live) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint32_t*>(p_row + h * 1024 + (((4 * half + x) ^ g) << 4)) = weights[h][x];
           ptx::fence_proxy_async_smem();
         }
         ptx::tc_fence_before();
