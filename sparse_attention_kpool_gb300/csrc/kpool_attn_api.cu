@@ -243,6 +243,14 @@ kpool_status kpool_attention_paged(const kpool_heads* q, const kpool_pages* k, c
     set_keys(p, &kh, &vh);
     p.k_ps = k->page_stride;
     p.v_ps = v->page_stride;
+    // the strides of a page of one token, or of one page, carry no meaning of their own
+    if (page_size == 1) {
+      p.k_ts = p.k_ps;
+      p.v_ts = p.v_ps;
+    } else if (num_pages == 1) {
+      p.k_ps = page_size * p.k_ts;
+      p.v_ps = page_size * p.v_ts;
+    }
   }
   set_shape(p, *shape);
   p.cu_q = cu_q;

@@ -14,7 +14,7 @@
 //            2052 ids of 64 / 1 heads: 1222 against 288 us.)
 //   kDense   kTwo under a mask of bits for all keys (kpool_attn_dense.cu).
 //   kPagedOne, kPagedTwo   kOne and kTwo over a cache in pages, a TMA box for what lies in one page;
-//   kPagedRows  decode steps over small pages: as kGather, but for whole caches of any length.
+//   kPagedRows  decode steps over pages: as kGather, but for whole caches of any length.
 //
 // Roles (12 warps; kGather 16): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread
 // per row; warp 8 loads by TMA; warps 9 and 10 issue the MMAs of group 0 and 1 (warp 9 owns
@@ -464,8 +464,6 @@ __host__ __device__ __forceinline__ int piece_rows(int page_size) {
   const int low = page_size & -page_size;
   return low < kTileKeys ? low : kTileKeys;
 }
-
-constexpr int kPagedBoxRows = 64;  // keys of a TMA box that decode steps want at least
 
 // Bounded wait; also gives up when another role did.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
@@ -1637,10 +1635,10 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
 }
 
 cudaError_t launch_attn_tc(const AttnPagedParams& p, char* ws, cudaStream_t stream) {
-  // Decode steps over small pages by plain copies, where the pages follow one another in memory: a TMA box of 16 keys or
-  // fewer moves what it names no faster than one of 64 (PAGED_TIMES).
-  const bool rows = p.cu_q == nullptr && piece_rows(p.page_size) < kPagedBoxRows &&
-                    p.k_ps == p.page_size * p.k_ts && p.v_ps == p.page_size * p.v_ts &&
+  // Decode steps by plain copies, where the pages follow one another in memory; chunks by TMA, a box for what lies in one
+  // page (us, 32 / 8 heads of 128, plain copies / TMA): 16 decode tokens over pages of 8 132 / 268, of 16 132 / 187, of
+  // 64 131 / 136; a chunk of 300 rows over 12,000 keys by TMA 480 with pages of 1, 107 of 8, 83 of 16, 70 of 64.
+  const bool rows = p.cu_q == nullptr && p.k_ps == p.page_size * p.k_ts && p.v_ps == p.page_size * p.v_ts &&
                     int64_t(p.num_pages) * p.page_size <= INT32_MAX && attn_gather_supported(p.k_ts, p.v_ts);
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);  // (as above)
   if (p.D == 64)

@@ -706,44 +706,32 @@ def kpool_attention_selected(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
                       cu_k.numel() - 1, scale, out, return_lse, out_lse, workspace, stream, score_kernel)
 
 
-class _ServingArgs(threading.local):
-    """A thread's argument structures of the calls below, filled anew by every call."""
+class _Args(threading.local):
+    """A thread's argument structures of one entry point, side by side in one buffer that every call fills anew with
+    one pack of their fields (building them took most of a short call). `floats` are set by name: they are
+    rounded as C does, out of fp32's range they are infinite."""
 
-    def __init__(self):
-        heads, pages = ctypes.sizeof(kpool_heads), ctypes.sizeof(kpool_pages)
-        parts = [kpool_heads] * 4 + [kpool_pages] * 2 + [kpool_rotary_part] * 2 + [kpool_attention_shape,
-                                                                                    kpool_latent_shape,
-                                                                                    kpool_rotary_shape]
-        at = [0]
-        for t in parts:
-            at.append(at[-1] + ctypes.sizeof(t))
-        self.buffer = bytearray(at[-1])
-        made = [t.from_buffer(self.buffer, a) for t, a in zip(parts, at)]
-        refs = [ctypes.byref(x) for x in made]
-        self.heads, self.pages, self.parts = refs[:4], refs[4:6], refs[6:8]
-        self.attention, self.latent, self.rotary = refs[8:]
-        self.latent_shape, self.attention_shape, self.rotary_shape = made[9], made[8], made[10]
-        self.heads_at = at[:4]
-        self.pages_at, self.part_at = at[4:6], at[6:8]
-        self.attention_at, self.latent_at, self.rotary_at = at[8:11]
-        self.pack_heads = struct.Struct("=Qqq").pack_into
-        self.pack_pages = struct.Struct("=Qqqq").pack_into
-        self.pack_part = struct.Struct("=QqqQqqiiii").pack_into
-        self.pack_shape = struct.Struct("=iiii").pack_into       # kpool_attention_shape without scale
-        self.pack_latent = struct.Struct("=iiiii").pack_into     # kpool_latent_shape without scale
-        self.pack_rotary = struct.Struct("=iii").pack_into       # kpool_rotary_shape without magnitude
-        assert heads == 24 and pages == 32
+    def __init__(self, *parts):
+        sizes = [ctypes.sizeof(t) for t, _ in parts]
+        self.buffer = bytearray(sum(sizes))
+        made = [t.from_buffer(self.buffer, sum(sizes[:i])) for i, (t, _) in enumerate(parts)]
+        self.refs = [ctypes.byref(x) for x in made]
+        self.last = made[-1]
+        self.pack = struct.Struct("=" + "".join(f for _, f in parts)).pack_into
 
 
-_serving_args = _ServingArgs()
+_HEADS, _PAGES = (kpool_heads, "Qqq"), (kpool_pages, "Qqqq")
+_paged_args = _Args(_HEADS, _HEADS, _PAGES, _PAGES, (kpool_attention_shape, "iiii"))
+_latent_args = _Args(_HEADS, _HEADS, _PAGES, (kpool_latent_shape, "iiiii"))
+_latent_prompt_args = _Args(_HEADS, _HEADS, _HEADS, _HEADS, _HEADS, (kpool_latent_shape, "iiiii"))
+_ROTARY_PART = (kpool_rotary_part, "QqqQqqiiii")
+_rotary_args = _Args(_ROTARY_PART, _ROTARY_PART, (kpool_rotary_shape, "iii"))
+_LAST = "the last dimension of a tensor must be contiguous"
 
 
-def _current_device(*tensors) -> int:
-    """The device of all of them, which has to be the current one (the library launches there)."""
-    dev = tensors[0].get_device()  # -1 on the CPU
-    for t in tensors:
-        if t.get_device() != dev:
-            dev = -1
+def _current_device(dev: int) -> int:
+    """dev, the device of a call's tensors (-1: the CPU, or not the same for all): the library launches on the
+    current one."""
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("tensors must be CUDA tensors on the current device")
     return dev
@@ -753,30 +741,26 @@ def _array(t, dev, dtype=torch.int32):
     """Pointer of an index array (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"page tables, lengths, cumulative lengths, token ids, row_seq and positions are {dtype}")
     if t.get_device() != dev or not t.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors on the current device")
     return t.data_ptr()
 
 
-def _strides(t):
-    """(token stride, head stride) of a [tokens, heads, dim] tensor; a dimension of one element has none of its own."""
-    n, h, d = t.shape
+def _strides(t, n, h, d):
+    """(token stride, head stride) of a tensor of shape (n, h, d); a dimension of one element has none of its own."""
     a, b, c = t.stride()
     if c != 1 and d > 1:
-        raise ValueError("the last dimension of a tensor must be contiguous")
-    if h == 1:
-        b = d
-    return (d if n <= 1 else a), b
+        raise ValueError(_LAST)
+    return (d if n <= 1 else a), (d if h == 1 else b)
 
 
-def _page_strides(t):
+def _page_strides(t, n, size, h, d):
     """(page, token, head stride) of a [pages, page_size, heads, dim] tensor."""
-    n, size, h, d = t.shape
     a, b, c, e = t.stride()
     if e != 1 and d > 1:
-        raise ValueError("the last dimension of a tensor must be contiguous")
+        raise ValueError(_LAST)
     return (d if n <= 1 else a), (d if size == 1 else b), (d if h == 1 else c)
 
 
@@ -784,29 +768,23 @@ def _results(q_rows, heads, dim, q, out, return_lse, out_lse, stream):
     """out [rows, heads, dim] and out_lse [rows, heads] or None, made here or the caller's."""
     if out is None:
         out = _empty((q_rows, heads, dim), q.dtype, q.device, stream)
-    elif out.shape != (q_rows, heads, dim) or out.dtype != q.dtype:
+    elif out.shape != (q_rows, heads, dim) or out.dtype is not q.dtype:
         raise TypeError("out must have q's dtype and a row of values for every query row and head")
     if out_lse is None:
         if return_lse:
             out_lse = _empty((q_rows, heads), torch.float32, q.device, stream)
-    elif out_lse.dtype != torch.float32 or out_lse.shape != (q_rows, heads):
+    elif out_lse.dtype is not torch.float32 or out_lse.shape != (q_rows, heads):
         raise TypeError("out_lse must be float32 [rows, q_heads]")
     return out, out_lse
 
 
-def _finish(name, call, args, out, out_lse, workspace, stream, dev, score_kernel):
-    """The arguments that all attention calls end with, and the call's status."""
+def _tail(out_lse, workspace, stream, dev, score_kernel):
+    """The arguments that all attention calls end with."""
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors on the current device")
-    a = _serving_args
-    ot, oh = _strides(out)
-    a.pack_heads(a.buffer, a.heads_at[3], out.data_ptr(), ot, oh)
-    st = call(*args, a.heads[3], _array(out_lse, dev, torch.float32), workspace.data_ptr(), workspace.nbytes,
-              torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream),
-              None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
-    if st != KPOOL_OK:
-        raise KpoolError(st, name)
-    return out, out_lse
+    return (None if out_lse is None else _array(out_lse, dev, torch.float32), workspace.data_ptr(), workspace.nbytes,
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream),
+            None if score_kernel == KPOOL_SCORE_AUTO else kpool_options(score_kernel))
 
 
 def kpool_attention_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -816,33 +794,36 @@ def kpool_attention_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pag
     page, token and head strides), page_table [S, max_pages] and lengths [S] int32. Sequence b's query rows (cu_q
     [S+1] int32; None: row b alone, a decode step) are the last ones of its lengths[b] keys. Returns (out, lse)
     as kpool_attention_prompt does; the workspace is new_attention_workspace's."""
-    if q.dim() != 3 or k.dim() != 4 or v.shape != k.shape or q.shape[2] != k.shape[3]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 4 or v.shape != ks or qs[2] != ks[3]:
         raise ValueError("q is [rows, q_heads, head_dim]; k and v are [pages, page_size, kv_heads, head_dim] alike")
     dtype = q.dtype
-    if k.dtype != dtype or v.dtype != dtype:
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise TypeError("k and v must match q's dtype")
     code = _ATTENTION_DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
-    R, hq, d = q.shape
-    pages, size, hkv, _ = k.shape
-    S = lengths.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != S or (R != S if cu_q is None else cu_q.numel() != S + 1):
+    R, hq, d = qs
+    pages, size, hkv, _ = ks
+    S, ts = lengths.numel(), page_table.shape
+    if len(ts) != 2 or ts[0] != S or (R != S if cu_q is None else cu_q.numel() != S + 1):
         raise ValueError("page_table is [sequences, pages], lengths [sequences], cu_q [sequences + 1] (or a row each)")
     out, out_lse = _results(R, hq, d, q, out, return_lse, out_lse, stream)
     if workspace is None:
         workspace = _new(lambda: new_attention_workspace(R, S, hq, hkv, d, dtype, q.device), stream, returned=False)
-    dev = _current_device(q, k, v, out)
-    a = _serving_args
-    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
-    a.pack_pages(a.buffer, a.pages_at[0], k.data_ptr(), *_page_strides(k))
-    a.pack_pages(a.buffer, a.pages_at[1], v.data_ptr(), *_page_strides(v))
-    a.pack_shape(a.buffer, a.attention_at, hq, hkv, d, code)
-    a.attention_shape.scale = scale  # (rounded as C does: out of fp32's range it is infinite, and refused)
-    return _finish("kpool_attention_paged", (_lib or load()).kpool_attention_paged,
-                   (a.heads[0], *a.pages, _array(page_table, dev), page_table.shape[1], pages, size,
-                    _array(lengths, dev), _array(cu_q, dev), S, R, a.attention), out, out_lse, workspace, stream, dev,
-                   score_kernel)
+    dev = q.get_device()
+    dev = _current_device(dev if dev == k.get_device() == v.get_device() == out.get_device() else -1)
+    a = _paged_args
+    a.pack(a.buffer, 0, q.data_ptr(), *_strides(q, R, hq, d), out.data_ptr(), *_strides(out, R, hq, d), k.data_ptr(),
+           *_page_strides(k, pages, size, hkv, d), v.data_ptr(), *_page_strides(v, pages, size, hkv, d), hq, hkv, d, code)
+    a.last.scale = scale
+    rq, ro, rk, rv, rs = a.refs
+    st = (_lib or load()).kpool_attention_paged(
+        rq, rk, rv, _array(page_table, dev), ts[1], pages, size, _array(lengths, dev),
+        None if cu_q is None else _array(cu_q, dev), S, R, rs, ro, *_tail(out_lse, workspace, stream, dev, score_kernel))
+    if st != KPOOL_OK:
+        raise KpoolError(st, "kpool_attention_paged")
+    return out, out_lse
 
 
 def _latent_shape(heads, key_dim, rotary_dim, value_dim, dtype, scale=1.0):
@@ -900,20 +881,24 @@ def kpool_attention_latent_prompt(q: torch.Tensor, k: torch.Tensor, k_rotary: to
     if workspace is None:
         workspace = _new(lambda: new_latent_prompt_workspace(R, S, h, dn, dr, dv, dtype, q.device), stream,
                          returned=False)
-    dev = _current_device(q, k, k_rotary, v, out)
+    dev = q.get_device()
+    dev = _current_device(dev if dev == k.get_device() == k_rotary.get_device() == v.get_device() == out.get_device()
+                          else -1)
     rt, rd = k_rotary.stride()
     if rd != 1 and dr > 1:
-        raise ValueError("the last dimension of a tensor must be contiguous")
-    a = _serving_args
-    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
-    a.pack_heads(a.buffer, a.heads_at[1], k.data_ptr(), *_strides(k))
-    a.pack_heads(a.buffer, a.heads_at[2], v.data_ptr(), *_strides(v))
-    rotary = kpool_heads(k_rotary.data_ptr(), rt if T > 1 else dr, dr)
-    a.pack_latent(a.buffer, a.latent_at, h, dn, dr, dv, code)
-    a.latent_shape.scale = scale
-    return _finish("kpool_attention_latent_prompt", (_lib or load()).kpool_attention_latent_prompt,
-                   (a.heads[0], a.heads[1], rotary, a.heads[2], _array(cu_q, dev), _array(cu_k, dev), S, R, T,
-                    a.latent), out, out_lse, workspace, stream, dev, score_kernel)
+        raise ValueError(_LAST)
+    a = _latent_prompt_args
+    a.pack(a.buffer, 0, q.data_ptr(), *_strides(q, R, h, dk), k.data_ptr(), *_strides(k, T, h, dn), k_rotary.data_ptr(),
+           rt if T > 1 else dr, dr, v.data_ptr(), *_strides(v, T, h, dv), out.data_ptr(), *_strides(out, R, h, dv), h, dn, dr,
+           dv, code)
+    a.last.scale = scale
+    rq, rk, rr, rv, ro, rs = a.refs
+    st = (_lib or load()).kpool_attention_latent_prompt(
+        rq, rk, rr, rv, _array(cu_q, dev), _array(cu_k, dev), S, R, T, rs, ro,
+        *_tail(out_lse, workspace, stream, dev, score_kernel))
+    if st != KPOOL_OK:
+        raise KpoolError(st, "kpool_attention_latent_prompt")
+    return out, out_lse
 
 
 def kpool_attention_latent(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -924,18 +909,19 @@ def kpool_attention_latent(q: torch.Tensor, cache: torch.Tensor, page_table: tor
     first L = latent_dim channels are the value too, page_table [S, max_pages] and lengths [S] int32. Row r, of
     sequence row_seq[r] ([R] int32; None: sequence r), sees its whole cache, or the tokens that token_ids
     [R, width] int32 names, as kpool_select_rows returns them. Returns (out [R,H,L], lse [R,H] fp32 or None)."""
-    if q.dim() != 3 or cache.dim() != 3 or q.shape[2] != cache.shape[2] or not 0 < latent_dim < q.shape[2]:
+    qs, cs = q.shape, cache.shape
+    if len(qs) != 3 or len(cs) != 3 or qs[2] != cs[2] or not 0 < latent_dim < qs[2]:
         raise ValueError("q is [rows, heads, channels], cache [pages, page_size, channels] with more than latent_dim")
     dtype = q.dtype
-    if cache.dtype != dtype:
+    if cache.dtype is not dtype:
         raise TypeError("cache must match q's dtype")
     code = _ATTENTION_DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"q and cache must be bfloat16 or float32, got {dtype}")
-    R, h, dim = q.shape
-    pages, size, _ = cache.shape
-    S = lengths.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != S or (R != S if row_seq is None else row_seq.numel() != R):
+    R, h, dim = qs
+    pages, size, _ = cs
+    S, ts = lengths.numel(), page_table.shape
+    if len(ts) != 2 or ts[0] != S or (R != S if row_seq is None else row_seq.numel() != R):
         raise ValueError("page_table is [sequences, pages], lengths [sequences], row_seq [rows] (or a row each)")
     width = KPOOL_WHOLE_CACHE
     if token_ids is not None:
@@ -946,19 +932,24 @@ def kpool_attention_latent(q: torch.Tensor, cache: torch.Tensor, page_table: tor
     if workspace is None:
         workspace = _new(lambda: new_latent_workspace(R, S, h, latent_dim, dim - latent_dim, dtype, q.device), stream,
                          returned=False)
-    dev = _current_device(q, cache, out)
-    ps, ts, cd = cache.stride()
+    dev = q.get_device()
+    dev = _current_device(dev if dev == cache.get_device() == out.get_device() else -1)
+    cp, ct, cd = cache.stride()
     if cd != 1 and dim > 1:
-        raise ValueError("the last dimension of a tensor must be contiguous")
-    a = _serving_args
-    a.pack_heads(a.buffer, a.heads_at[0], q.data_ptr(), *_strides(q))
-    a.pack_pages(a.buffer, a.pages_at[0], cache.data_ptr(), ps if pages > 1 else dim, ts if size > 1 else dim, dim)
-    a.pack_latent(a.buffer, a.latent_at, h, latent_dim, dim - latent_dim, latent_dim, code)
-    a.latent_shape.scale = scale
-    return _finish("kpool_attention_latent", (_lib or load()).kpool_attention_latent,
-                   (a.heads[0], a.pages[0], _array(page_table, dev), page_table.shape[1], pages, size,
-                    _array(lengths, dev), _array(token_ids, dev), width, _array(row_seq, dev), S, R, a.latent), out,
-                   out_lse, workspace, stream, dev, score_kernel)
+        raise ValueError(_LAST)
+    a = _latent_args
+    a.pack(a.buffer, 0, q.data_ptr(), *_strides(q, R, h, dim), out.data_ptr(), *_strides(out, R, h, latent_dim),
+           cache.data_ptr(), cp if pages > 1 else dim, ct if size > 1 else dim, dim, h, latent_dim, dim - latent_dim,
+           latent_dim, code)
+    a.last.scale = scale
+    rq, ro, rc, rs = a.refs
+    st = (_lib or load()).kpool_attention_latent(
+        rq, rc, _array(page_table, dev), ts[1], pages, size, _array(lengths, dev),
+        None if token_ids is None else _array(token_ids, dev), width, None if row_seq is None else _array(row_seq, dev), S, R,
+        rs, ro, *_tail(out_lse, workspace, stream, dev, score_kernel))
+    if st != KPOOL_OK:
+        raise KpoolError(st, "kpool_attention_latent")
+    return out, out_lse
 
 
 def new_rotary_table(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: float = 0.0,
@@ -979,38 +970,50 @@ def kpool_rotary(q: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, 
     head are rotated, in halves or in neighbouring pairs, the others copied. out_q and out_k may be q and k
     themselves. With inverse the rotation goes the other way (with the same magnitude: the gradient).
     Returns (out_q, out_k)."""
-    dtype, n = q.dtype, q.shape[0] if q.dim() == 3 else -1
+    qs, dtype = q.shape, q.dtype
     code = _ATTENTION_DTYPES.get(dtype)
-    if code is None or (k is not None and k.dtype != dtype):
+    if code is None or (k is not None and k.dtype is not dtype):
         raise TypeError("q and k must be bfloat16 or float32 alike")
-    if n < 0 or (k is not None and (k.dim() != 3 or k.shape[0] != n)) or positions.numel() != n:
+    if len(qs) != 3 or positions.numel() != qs[0]:
         raise ValueError("q and k are [tokens, heads, channels], positions [tokens]")
-    a = _serving_args
-    found, dev = [], _current_device(q)
-    for i, (x, out, offset) in enumerate(((q, out_q, q_offset), (k, out_k, k_offset))):
-        if x is None:
-            if out is not None:
-                raise ValueError("out_k without k")
-            found.append(None)
-            continue
-        if out is None:
-            out = _empty(x.shape, dtype, x.device, stream)
-        elif out.shape != x.shape or out.dtype != dtype:
+    n, hq, dq = qs
+    if out_q is None:
+        out_q = _empty(qs, dtype, q.device, stream)
+    elif out_q.shape != qs or out_q.dtype is not dtype:
+        raise TypeError("out_q and out_k must have the shape and dtype of q and k")
+    dev = q.get_device()
+    if dev != out_q.get_device():
+        dev = -1
+    flags = (KPOOL_ROTARY_INTERLEAVED if interleaved else 0) | (KPOOL_ROTARY_INVERSE if inverse else 0)
+    a = _rotary_args
+    qt, qh = _strides(q, n, hq, dq)
+    ot, oh = (qt, qh) if out_q is q else _strides(out_q, n, hq, dq)
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k without k")
+        k_part = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    else:
+        ks = k.shape
+        if len(ks) != 3 or ks[0] != n:
+            raise ValueError("q and k are [tokens, heads, channels], positions [tokens]")
+        if out_k is None:
+            out_k = _empty(ks, dtype, k.device, stream)
+        elif out_k.shape != ks or out_k.dtype is not dtype:
             raise TypeError("out_q and out_k must have the shape and dtype of q and k")
-        if x.get_device() != dev or out.get_device() != dev:
-            raise ValueError("tensors must be CUDA tensors on the current device")
-        a.pack_part(a.buffer, a.part_at[i], x.data_ptr(), *_strides(x), out.data_ptr(), *_strides(out), x.shape[1],
-                    x.shape[2], offset, 0)
-        found.append(out)
-    a.pack_rotary(a.buffer, a.rotary_at, 2 * table.numel(), code,
-                  (KPOOL_ROTARY_INTERLEAVED if interleaved else 0) | (KPOOL_ROTARY_INVERSE if inverse else 0))
-    a.rotary_shape.magnitude = magnitude
-    st = (_lib or load()).kpool_rotary(a.parts[0], None if k is None else a.parts[1], _array(positions, dev),
-                                       _array(table, dev, torch.int64), n, a.rotary,
+        if not dev == k.get_device() == out_k.get_device():
+            dev = -1
+        k_part = (k.data_ptr(), *_strides(k, *ks), out_k.data_ptr(), *_strides(out_k, *ks), ks[1], ks[2], k_offset, 0)
+    _current_device(dev)
+    a.pack(a.buffer, 0, q.data_ptr(), qt, qh, out_q.data_ptr(), ot, oh, hq, dq, q_offset, 0, *k_part, 2 * table.numel(),
+           code, flags)
+    a.last.magnitude = magnitude
+    rq, rk, rs = a.refs
+    st = (_lib or load()).kpool_rotary(rq, None if k is None else rk, _array(positions, dev),
+                                       _array(table, dev, torch.int64), n, rs,
                                        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st != KPOOL_OK:
         raise KpoolError(st, "kpool_rotary")
-    return tuple(found)
+    return out_q, out_k
 
 
 def kpool_balanced_row_split(cu_seqlens, kpool: int, parts: int, row_weight: int = 0) -> list:
