@@ -62,9 +62,11 @@
 namespace kpool {
 namespace {
 
-constexpr int kTileKeys = 128;
+// Keys of a tile. 96 with a shared part of the keys: two tiles of K (192 channels) and of V then fit beside Q of two row
+// tiles; with 128 there is room for one V, whose next tile is waited for (5,200 cycles a pair of tiles, half of them).
+template <class P>
+constexpr int kTile = kSharedKeys<P> ? 96 : 128;
 constexpr int kTileRows = kAttnTileRows;
-constexpr int kPCol = 64;      // a tile's weights, bf16 in 64 columns, replace the upper half of its scores
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (in powers of two) that O is not rescaled for
@@ -99,15 +101,20 @@ struct Cfg {
   // them, K one tile (one-tile form: one per group) ahead.
   static constexpr int kAhead = TWO ? 1 : 2;
   static constexpr int kThreads = GATHER ? 512 : 384;
-  static constexpr int kTileBytes = kTileKeys * DK * 2;  // one K tile, one Q tile
+  static constexpr int kTileKeys = kTile<Params>;
+  static constexpr int kScoreCols = kTileKeys / 32;      // 32-column pieces of a row's scores
+  static constexpr int kPCol = kTileKeys / 2;            // a tile's weights, bf16, replace the upper half of its scores
+  static constexpr int kQBytes = kTileRows * DK * 2;     // one Q tile
+  static constexpr int kQBlock = kTileRows * 128;        // a 64-column block of one
+  static constexpr int kTileBytes = kTileKeys * DK * 2;  // one K tile
   static constexpr int kVBytes = kTileKeys * DV * 2;     // one V tile
   static constexpr int kHalf = kTileKeys * 128;          // a 64-column block of a tile
   static constexpr int kBlocks = DK / 64, kVBlocks = DV / 64;
   static constexpr int kQTiles = TWO ? 2 : 1;
   // rings apart: the first kKSlots slots hold K, the others V; as many as fit beside Q at 192 + 128 channels
-  static constexpr int kKSlots = 2, kVSlots = TWO ? 1 : 2;
+  static constexpr int kKSlots = TWO ? 2 : 3, kVSlots = 2;
   static constexpr int kStages = SHARED ? kKSlots + kVSlots : DK == 64 ? 8 : (TWO ? 5 : 6);
-  static constexpr int kOffRing = kQTiles * kTileBytes;
+  static constexpr int kOffRing = kQTiles * kQBytes;
   static constexpr int kOffBar = kOffRing + (SHARED ? kKSlots * kTileBytes + kVSlots * kVBytes : kStages * kTileBytes);
   // full[stages] empty[stages] clean[stages] dirty[stages] q_full q_empty s_full[2] p_ready[2] o_final o_free done
   // seg_full[ring] seg_empty[ring] turn[2]
@@ -172,7 +179,7 @@ static_assert(sizeof(Seg) <= 64, "Seg fits its space");
 template <class P>
 __device__ __forceinline__ int tile_cost(const P& p, const AttnSeq& s, int t, int ttb) {
   const int end = attn_keys_end(p, s, min((t + 1) * ttb, s.nq));
-  return max(1, (end + kTileKeys - 1) / kTileKeys);
+  return max(1, (end + kTile<P> - 1) / kTile<P>);
 }
 
 // Beginning and finishing an item (Q, first product, epilogue) takes about as long as this
@@ -215,12 +222,12 @@ template <class P>
 __device__ __forceinline__ int64_t head_cost(const P& p, const AttnSeq& s, int t, int ttb) {
   if (t == 0) return 0;
   if (!s.ok || s.nk == 0) return int64_t(t) * (kItemCost + 1);
-  if (!attn_causal(p)) return int64_t(t) * (kItemCost + (s.nk + kTileKeys - 1) / kTileKeys);
+  if (!attn_causal(p)) return int64_t(t) * (kItemCost + (s.nk + kTile<P> - 1) / kTile<P>);
   const int nt = row_tiles(s, ttb), m = min(t, nt - 1);
   const int z = s.prefix < 0 ? min(m, -s.prefix / ttb) : 0;  // tiles without any key
   int64_t c = int64_t(t) * kItemCost + z;
-  c += floor_sum(uint32_t(m - z), kTileKeys, uint32_t(ttb), uint32_t(s.prefix + (z + 1) * ttb + kTileKeys - 1));
-  if (t == nt) c += max(1, (s.prefix + s.nq + kTileKeys - 1) / kTileKeys);
+  c += floor_sum(uint32_t(m - z), kTile<P>, uint32_t(ttb), uint32_t(s.prefix + (z + 1) * ttb + kTile<P> - 1));
+  if (t == nt) c += max(1, (s.prefix + s.nq + kTile<P> - 1) / kTile<P>);
   return c;
 }
 
@@ -318,7 +325,7 @@ __device__ __forceinline__ bool direct_seg(const P& p, int ttb, int tiles, Seg* 
 // Gathered form: every row and key head has the same number of tiles, and positions run over
 // rows, then key heads (the heads of a token lie together in memory).
 __device__ __forceinline__ int gather_tiles(const AttnParams& p) {
-  return max(1, (p.width + kTileKeys - 1) / kTileKeys);
+  return max(1, (p.width + kTile<AttnParams> - 1) / kTile<AttnParams>);
 }
 
 __device__ __forceinline__ int64_t gather_total(const AttnParams& p) {
@@ -357,7 +364,7 @@ __device__ __forceinline__ void finish_seg(const P& p, int tt, int ttb, Seg* s) 
   s->end = attn_keys_end(p, s->sq, min(s->tok0 + ttb, s->sq.nq));
   if (s->end == 0) s->n = 0;
   const int end0 = attn_keys_end(p, s->sq, min(s->tok0 + tt, s->sq.nq));
-  s->n0 = max(0, min(s->n, (end0 + kTileKeys - 1) / kTileKeys - s->kt0));
+  s->n0 = max(0, min(s->n, (end0 + kTile<P> - 1) / kTile<P> - s->kt0));
   s->all = p.mask ? s->sq.prefix : s->sq.prefix + s->tok0 + 1;
 }
 
@@ -462,7 +469,7 @@ __device__ __forceinline__ void write_join(JoinItem* out, const Seg& s, int64_t 
 // the page size.
 __host__ __device__ __forceinline__ int piece_rows(int page_size) {
   const int low = page_size & -page_size;
-  return low < kTileKeys ? low : kTileKeys;
+  return low < kTile<AttnPagedParams> ? low : kTile<AttnPagedParams>;
 }
 
 // Bounded wait; also gives up when another role did.
@@ -515,7 +522,7 @@ __device__ __forceinline__ uint32_t seen_bits(const P& p, const AttnSeq& s, int 
 }
 
 // K/V tile kt holds keys that some row of the segment does not see.
-__device__ __forceinline__ bool tile_masked(const Seg* s, int kt) { return (kt + 1) * kTileKeys > s->all; }
+__device__ __forceinline__ bool tile_masked(const Seg* s, int kt, int keys) { return (kt + 1) * keys > s->all; }
 
 // Rows rsub + kRowsPer * I of a warp's 32, all present: the token a lane wants comes from the lane that
 // holds its id; the destination differs by constants but for two address bits.
@@ -540,16 +547,18 @@ __device__ __forceinline__ void load_scores(uint32_t col, uint32_t (&s)[N][32]) 
 
 template <int N>
 __device__ __forceinline__ float max_score(const uint32_t (&s)[N][32]) {
-  float mx[4];  // four chains
+  constexpr int kChains = N == 3 ? 3 : 4;
+  float mx[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int first = c * N / 4, from = N == 4 ? 0 : 16 * (c & 1), n = N * 8;
+  for (int c = 0; c < kChains; ++c) {
+    const int first = c * N / kChains, from = N == 2 ? 16 * (c & 1) : 0, n = N * 32 / kChains;
     mx[c] = __uint_as_float(s[first][from]);
 #pragma unroll
     for (int x = 1; x < n - 1; x += 2)
       mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[first][from + x])), __uint_as_float(s[first][from + x + 1]));
     mx[c] = fmaxf(mx[c], __uint_as_float(s[first][from + n - 1]));
   }
+  if (kChains == 3) mx[3] = mx[2];
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
@@ -583,6 +592,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
                    const __grid_constant__ typename Cfg<DK, DV, F>::Params p, int tiles, int direct, float* part, int slot_rows,
                    JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<DK, DV, F>;
+  constexpr int kTileKeys = C::kTileKeys, kPCol = C::kPCol;
   constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, LISTED = F == kGather;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           ++q_loads;
 #pragma unroll
           for (int h = 0; h < C::kBlocks; ++h)
-            ptx::tma_load_3d(smem + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G, sg.sq.q0);
+            ptx::tma_load_3d(smem + h * C::kQBlock, &tm_q, q_full, 64 * h, sg.hk * p.G, sg.sq.q0);
         }
         if (q_loads) ptx::mbar_wait_bounded(q_full, (q_loads - 1) & 1, int64_t(1) << 40, kMaxWaitNs);
       }
@@ -845,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
                                  sg.sq.k0 + kt * kTileKeys);
             }
           }
-          if (!is_k && !no_cleaning && tile_masked(&sg, kt) && lane == 0) ptx::mbar_arrive(dirty + st);
+          if (!is_k && !no_cleaning && tile_masked(&sg, kt, kTileKeys) && lane == 0) ptx::mbar_arrive(dirty + st);
           return true;
         };
         for (int i = 0;; ++i) {
@@ -869,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
             for (int g = 0; g < C::kQTiles; ++g)
 #pragma unroll
               for (int h = 0; h < C::kBlocks; ++h)
-                ptx::tma_load_3d(smem + g * C::kTileBytes + h * C::kHalf, &tm_q, q_full, 64 * h, sg.hk * p.G,
+                ptx::tma_load_3d(smem + g * C::kQBytes + h * C::kQBlock, &tm_q, q_full, 64 * h, sg.hk * p.G,
                                  sg.sq.q0 + sg.tok0 + g * tt);
           }
           read_page(sg.kt0);
@@ -896,12 +906,12 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         // Descriptors of the Q tile and of the first ring slot; the others differ in the address field
         // (bytes / 16) only, so a step is one addition.
         const uint64_t q_desc =
-            ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + (TWO ? g * C::kTileBytes : 0)));
+            ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + (TWO ? g * C::kQBytes : 0)));
         const uint64_t k_desc = ptx::smem_desc_kmajor_sw128(ptx::smem_addr(smem + C::kOffRing));
         const uint64_t v_desc = ptx::smem_desc_mnmajor_sw128(ptx::smem_addr(smem + C::kOffRing), C::kHalf);
         constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(kTileRows, kTileKeys);
         constexpr uint32_t idesc_o = ptx::idesc_bf16_f32_bn(kTileRows, DV);
-        const uint32_t s_acc = tmem + g * kTileKeys, o_acc = tmem + 256 + g * DV;
+        const uint32_t s_acc = tmem + g * 128, o_acc = tmem + 256 + g * DV;
         uint32_t use = 0, q_uses = 0, p_uses = 0, turns = 0;  // ring uses before this segment, Q tiles, P tiles
         uint32_t clean_par = 0;                    // bit per ring slot
         bool ok = true;
@@ -926,8 +936,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           for (int kk = 0; kk < DK / 16; ++kk) {
             // handed on a little early: the other's first product follows without a gap
             if (kk == DK / 32 && pass) ptx::mbar_arrive(turn + (g ^ 1));
+            const uint32_t q_step = ((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4;
             const uint32_t step = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
-            ptx::tc_mma_f16(s_acc, q_desc + step, b + step, idesc_s, kk > 0 ? 1u : 0u);
+            ptx::tc_mma_f16(s_acc, q_desc + q_step, b + step, idesc_s, kk > 0 ? 1u : 0u);
           }
           ptx::tc_commit(s_full + g);
         };
@@ -973,7 +984,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
               if (jk < n && !(ok = landed(uk))) break;
               if (!(ok = landed(uv))) break;
               const uint32_t slot = uv.slot;
-              const bool masked = !no_cleaning && tile_masked(sg, kt0 + j);
+              const bool masked = !no_cleaning && tile_masked(sg, kt0 + j, kTileKeys);
               if (mine(j)) {
                 if (masked && !(ok = wait_bar(clean + slot, (clean_par >> slot) & 1, misc))) break;
                 if (!(ok = wait_bar(p_ready + g, p_uses & 1, misc))) break;
@@ -1081,7 +1092,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     const int g = warp >> 2;                 // group
     const int row = threadIdx.x & 127;       // row of the tile
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + g * kTileKeys;
+    const uint32_t s_col = tmem + lane_base + g * 128;
     const uint32_t o_col = tmem + lane_base + 256 + g * DV;
     const int tok_in = row / p.G, head_in = row - tok_in * p.G;
     const float c2 = p.scale * kLog2e;
@@ -1119,10 +1130,10 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         // where a row of the warp needs it. (As straight code on the 128 registers below it took three
         // times as long: it runs once or twice per row tile and is fetched anew each time.)
         const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + C::kOffBits) + 4 * ((tile + j) % kBitsRing);
-        if (GATHER ? (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu : !DENSE && tile_masked(sg, kt)) {
+        if (GATHER ? (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu : !DENSE && tile_masked(sg, kt, kTileKeys)) {
           const int im = min(i, sg->sq.nq - 1);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < C::kScoreCols; ++c) {
             const uint32_t bits = GATHER ? w[c] : seen_bits(p, sg->sq, im, kt * kTileKeys + 32 * c);
             if (!__any_sync(0xffffffffu, bits != 0xffffffffu)) continue;
             uint32_t x32[32];
@@ -1140,12 +1151,12 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         // and the lower ones are read again for their weights; half the code and registers, which is what
         // counts beside the gathering warps (350 -> 319 us for 2048 rows x 2052 ids of 64 heads; with two
         // row tiles the second read costs 5 % at 32,768 tokens).
-        constexpr int kHeld = TWO ? 4 : 2;
+        constexpr int kHeld = TWO || C::kScoreCols == 3 ? C::kScoreCols : 2, kReads = C::kScoreCols / kHeld;
         uint32_t s[kHeld][32];
         float mt = -INFINITY;
 #pragma unroll 1
-        for (int h = 0; h < 4 / kHeld; ++h) {
-          load_scores<kHeld>(s_col + 64 * h, s);
+        for (int h = 0; h < kReads; ++h) {
+          load_scores<kHeld>(s_col + 32 * kHeld * h, s);
           if (DENSE) {
 #pragma unroll
             for (int c = 0; c < kHeld; ++c) {
@@ -1181,8 +1192,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         const float nb = m == -INFINITY ? 0.0f : -m * c2;
         const uint64_t c22 = ptx::pack_f32x2(c2, c2), nb2 = ptx::pack_f32x2(nb, nb);
 #pragma unroll 1
-        for (int h = 4 / kHeld - 1; h >= 0; --h) {
-          if (!TWO && h == 0) load_scores<kHeld>(s_col, s);
+        for (int h = kReads - 1; h >= 0; --h) {
+          if (kReads > 1 && h == 0) load_scores<kHeld>(s_col, s);
 #pragma unroll
           for (int c = 0; c < kHeld; ++c) {
             uint32_t pk[16];
@@ -1197,7 +1208,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
               l2[x & 1] = ptx::add_f32x2(l2[x & 1], ptx::pack_f32x2(a, b));
               pk[x] = ptx::pack_bf16(a, b);
             }
-            ptx::tc_st_32x32b_x16(s_col + kPCol + 32 * h + 16 * c, pk);
+            ptx::tc_st_32x32b_x16(s_col + kPCol + 16 * (kHeld * h + c), pk);
           }
         }
         ptx::tc_wait_st();
@@ -1522,11 +1533,11 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
                               p.v_hs, rows))
       return cudaErrorInvalidValue;
   } else if (!GATHER) {
-    if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), DV, p.k_ts, p.k_hs, kTileKeys, 1) ||
-        !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), DV, p.v_ts, p.v_hs, kTileKeys, 1))
+    if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), DV, p.k_ts, p.k_hs, C::kTileKeys, 1) ||
+        !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), DV, p.v_ts, p.v_hs, C::kTileKeys, 1))
       return cudaErrorInvalidValue;
     if constexpr (C::SHARED)
-      if (!make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, kTileKeys, 1))
+      if (!make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, C::kTileKeys, 1))
         return cudaErrorInvalidValue;
   }
   const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
@@ -1541,7 +1552,7 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
   //  - for long sequences with many items (deepest first, a head's K and V in L2): 32,768 tokens 6.1 against
   //    6.5 ms;
   //  - for gathered items, all of the same tiles, where their rounding up to the SMs costs less than the join.
-  const int64_t nt = (p.width + kTileKeys - 1) / kTileKeys;
+  const int64_t nt = (p.width + C::kTileKeys - 1) / C::kTileKeys;
   const bool even = LISTED && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
   const bool small = !p.list && (even || ((LISTED ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
   const bool like = F == kTwo && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
