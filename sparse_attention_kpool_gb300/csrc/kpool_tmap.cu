@@ -28,6 +28,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// The encoder wants the device's context on the calling thread, which a thread that has made no runtime call of its own
+// that needs one does not have yet: a failed call is made once more behind cudaSetDevice, which puts it there.
+template <typename... Args>
+bool encode(EncodeTiledFn fn, Args... args) {
+  if (fn(args...) == CUDA_SUCCESS) return true;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+  return fn(args...) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
@@ -37,9 +47,9 @@ bool make_tmap_bf16_k128(CUtensorMap* map, const void* base, uint64_t rows, uint
   const cuuint64_t strides[1] = {cuuint64_t(128) * 2};
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return encode(fn, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t dim,
@@ -50,9 +60,9 @@ bool make_tmap_bf16_heads(CUtensorMap* map, const void* base, uint64_t tokens, u
   const cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2};
   const cuuint32_t box[3] = {64, box_heads, box_tokens};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+  return encode(fn, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool make_tmap_bf16_pages(CUtensorMap* map, const void* base, uint64_t pages, uint64_t page_size, uint64_t heads,
@@ -64,9 +74,9 @@ bool make_tmap_bf16_pages(CUtensorMap* map, const void* base, uint64_t pages, ui
   const cuuint64_t strides[3] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2, cuuint64_t(page_stride) * 2};
   const cuuint32_t box[4] = {64, 1, box_tokens, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+  return encode(fn, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace kpool
