@@ -1555,7 +1555,7 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
   const int64_t nt = (p.width + C::kTileKeys - 1) / C::kTileKeys;
   const bool even = LISTED && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
   const bool small = !p.list && (even || ((LISTED ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
-  const bool like = F == kTwo && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
+  const bool like = F == kTwo && (!C::SHARED || p.T == p.R) && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
   const bool deep = C::TWO && items >= int64_t(kAttnDirectItems) * sms && p.T >= int64_t(kAttnDirectKeys) * p.S;
   const bool direct = !LISTED && (small || like || deep || p.S > kAttnMaxRunSeqs);
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;

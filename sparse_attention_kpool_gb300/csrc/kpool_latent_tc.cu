@@ -790,78 +790,101 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------- join
 //
-// CTA x adds up, in the order of the runs, the partial results of the row that item x names. A warp has a quarter
-// of a head's channels, four a lane, and reads eight runs at a time; kShare: the 8 warps of a CTA share one quarter,
-// each taking every eighth run (few rows, each cut into many runs), else each has its own. What is read was just written:
-// 131 KB a run and 64 heads, 38 MB for 16 rows over 152 runs, at most.
-constexpr int kQuarters = kLatent / 128;
-constexpr int kJoinBatch = 8;
+// CTA x adds up, in the order of the runs, the partial results of the row that item x names, a head or a quarter of one
+// to a warp (Join):
+//   kFewParts   more rows than runs, so that a row is cut into two or three: a head a warp, 16 channels a lane, two parts
+//               at a time;
+//   kSomeParts  a quarter of a head a warp, four channels a lane, eight parts at a time;
+//   kManyParts  few rows, each cut into very many: the 8 warps of a CTA share a quarter, each taking every eighth part.
+// What is read was just written: 131 KB a part of 64 heads, 38 MB for 16 rows over 152 runs, at most.
+enum Join { kFewParts, kSomeParts, kManyParts };
+constexpr int kSomeBatch = 8;
 
-template <bool kShare>
+template <Join J>
 __global__ void __launch_bounds__(256)
     latent_join_kernel(const __grid_constant__ LatentParams p, int per, int groups, int runs, const JoinItem* joins,
                        const float* part) {
+  constexpr int kWords = J == kFewParts ? 4 : 1;               // float4 of a lane
+  constexpr int kPieces = kLatent / (128 * kWords);            // warps' pieces of a head
+  constexpr int kBatch = J == kFewParts ? 2 : kSomeBatch, kStep = J == kManyParts ? 8 : 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // in every CTA: the call ends after both kernels have
   const JoinItem it = joins[blockIdx.x];
   // (after a wait that ran out an item may never have been written)
   if (it.runs <= 0 || it.runs > runs || it.first < 0 || it.first >= runs || it.row < 0 || it.row >= p.R) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = kShare ? int(blockIdx.y) : int(blockIdx.y) * 8 + warp;
-  const int head = unit / kQuarters, ch = unit % kQuarters * 128 + 4 * lane;
+  const int unit = J == kManyParts ? int(blockIdx.y) : int(blockIdx.y) * 8 + warp;
+  const int head = unit / kPieces, ch = unit % kPieces * 128 * kWords + 4 * lane;
   const int group = head / per, h = head - group * per;
   const bool live = head < p.H;
   auto run_lo = [&](int r) { return it.each * r + it.rest * uint32_t(r) / uint32_t(it.runs); };
   const float c2 = p.scale * kLog2e;
   const int64_t end = it.item + it.tiles;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kWords];
+#pragma unroll
+  for (int x = 0; x < kWords; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.0f;
   // adds a part (o, pm, pl); one without any weight adds nothing, with a NaN among its scores its sum passes on
-  auto add = [&](const float4& o, float pm, float pl) {
+  auto add = [&](const float4 (&o)[kWords], float pm, float pl) {
     const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
     const float f = m == -INFINITY ? 1.0f : exp2f((m - base) * c2);
     const float w = pm == -INFINITY ? 1.0f : exp2f((pm - base) * c2);
     l = l * f + pl * w;
-    acc.x = acc.x * f + o.x * w;
-    acc.y = acc.y * f + o.y * w;
-    acc.z = acc.z * f + o.z * w;
-    acc.w = acc.w * f + o.w * w;
+#pragma unroll
+    for (int x = 0; x < kWords; ++x) {
+      acc[x].x = acc[x].x * f + o[x].x * w;
+      acc[x].y = acc[x].y * f + o[x].y * w;
+      acc[x].z = acc[x].z * f + o[x].z * w;
+      acc[x].w = acc[x].w * f + o[x].w * w;
+    }
     m = mn;
   };
-  const int slots = part_rows(per), step = kShare ? 8 : 1;
+  const int slots = part_rows(per);
   const size_t stride = size_t(slots) * (kLatent + 2);
-  for (int r0 = it.first + (kShare ? warp : 0); live && r0 < it.runs && run_lo(r0) < end; r0 += step * kJoinBatch) {
-    float4 o[kJoinBatch];
-    float2 ml[kJoinBatch];
-    bool has[kJoinBatch];
+  // the runs that have tiles of the row: they begin before its end, and end behind its first tile
+  for (int r0 = it.first + (J == kManyParts ? warp : 0); live && r0 < it.runs && run_lo(r0) < end; r0 += kStep * kBatch) {
+    float4 o[kBatch][kWords];
+    float2 ml[kBatch];
+    bool has[kBatch];
 #pragma unroll
-    for (int b = 0; b < kJoinBatch; ++b) {
-      const int r = r0 + b * step;
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kStep;
       const int64_t lo = run_lo(r), hi = run_lo(r + 1);
       has[b] = r < it.runs && lo < end && hi > it.item && hi > lo;
       if (!has[b]) continue;
       const float* s = part + ((size_t(r) * groups + group) * 2 + (r == it.first ? 1 : 0)) * stride;
       ml[b] = __ldcg(reinterpret_cast<const float2*>(s + size_t(slots) * kLatent + 2 * h));
-      o[b] = __ldcg(reinterpret_cast<const float4*>(s + size_t(h) * kLatent + ch));
+#pragma unroll
+      for (int x = 0; x < kWords; ++x)
+        o[b][x] = __ldcg(reinterpret_cast<const float4*>(s + size_t(h) * kLatent + ch + 128 * x));
     }
 #pragma unroll
-    for (int b = 0; b < kJoinBatch; ++b)
+    for (int b = 0; b < kBatch; ++b)
       if (has[b]) add(o[b], ml[b].x, ml[b].y);
   }
-  if (kShare) {  // the first warp adds the others' parts in their order
+  if (J == kManyParts) {  // the first warp adds the others' parts in their order
     __shared__ float4 s_o[8][32];
     __shared__ float2 s_ml[8];
-    s_o[warp][lane] = acc;
+    s_o[warp][lane] = acc[0];
     if (lane == 0) s_ml[warp] = make_float2(m, l);
     __syncthreads();
     if (warp != 0) return;
-    for (int x = 1; x < 8; ++x) add(s_o[x][lane], s_ml[x].x, s_ml[x].y);
+    for (int x = 1; x < 8; ++x) {
+      float4 o[kWords];
+      o[0] = s_o[x][lane];
+      add(o, s_ml[x].x, s_ml[x].y);
+    }
   }
   if (!live) return;
   const bool none = m == -INFINITY && l == 0.0f;
   const float inv = none ? 0.0f : 1.0f / l;
-  uint2 v = make_uint2(0, 0);
-  if (!none) v = make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(it.row) * p.o_ts + head * p.o_hs + ch) = v;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(it.row) * p.o_ts + head * p.o_hs + ch;
+#pragma unroll
+  for (int x = 0; x < kWords; ++x) {
+    uint2 v = make_uint2(0, 0);
+    if (!none)
+      v = make_uint2(ptx::pack_bf16(acc[x].x * inv, acc[x].y * inv), ptx::pack_bf16(acc[x].z * inv, acc[x].w * inv));
+    *reinterpret_cast<uint2*>(out + 128 * x) = v;
+  }
   if (lane == 0 && ch == 0 && p.lse)
     p.lse[int64_t(it.row) * p.H + head] = none ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
 }
@@ -922,10 +945,9 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || runs < 2) return e;
   cudaLaunchConfig_t cfg{};
-  // many runs to a row: a CTA's warps share a quarter of a head; else each has its own
-  const bool share = int64_t(p.R) * 2 * kJoinBatch <= runs;
-  const int units = p.H * kQuarters;
-  cfg.gridDim = dim3(uint32_t(p.R <= runs ? p.R : runs), uint32_t(share ? units : (units + 7) / 8));
+  const Join join = p.R > runs ? kFewParts : int64_t(p.R) * 2 * kSomeBatch <= runs ? kManyParts : kSomeParts;
+  const int units = join == kFewParts ? p.H : p.H * (kLatent / 128);
+  cfg.gridDim = dim3(uint32_t(p.R <= runs ? p.R : runs), uint32_t(join == kManyParts ? units : (units + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -933,8 +955,11 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<true> : latent_join_kernel<false>, p, per, groups, runs,
-                         static_cast<const JoinItem*>(joins), static_cast<const float*>(part));
+  auto kernel = join == kFewParts    ? latent_join_kernel<kFewParts>
+                : join == kSomeParts ? latent_join_kernel<kSomeParts>
+                                     : latent_join_kernel<kManyParts>;
+  e = cudaLaunchKernelEx(&cfg, kernel, p, per, groups, runs, static_cast<const JoinItem*>(joins),
+                         static_cast<const float*>(part));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
