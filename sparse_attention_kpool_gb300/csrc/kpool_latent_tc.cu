@@ -10,15 +10,20 @@
 // buffers of scores. More than 64 heads are split evenly over CTAs side by side that walk
 // the same tokens at the same time, so that the second reads what the first brought into L2.
 //
-// Roles (18 warps): warps 0-7 softmax, eight threads to a head's 64 scores (the layout in which a 16-row
-// accumulator is read); warps 8-15 copy tokens, by TMA where a whole tile lies in few pages, else 16 bytes a lane
-// (cp.async), rows of 1,152 bytes wherever the ids and the page table put them; warp 16 issues the MMAs and owns
-// tensor memory; warp 17 hands out segments and loads Q. The scores of tile j + 1 are issued while the softmax of
-// tile j runs if that tile has landed by then, else behind the second product of tile j.
+// Roles (14 warps): warps 0-7 softmax, eight threads to a head's 64 scores (the layout in which a 16-row
+// accumulator is read); warps 8-11 copy tokens, 16 bytes a lane (cp.async), rows of 1,152 bytes wherever the ids
+// and the page table put them (TMA of whole pages: 108.1 against 106.5 us for the first case below); warp 12 issues the MMAs and owns
+// tensor memory; warp 13 hands out segments and loads Q. The scores of tile j + 1 are issued while the softmax of
+// tile j runs if that tile has landed by then, else behind the second product of tile j. A slot's parts (rotated block,
+// four blocks of channels) are freed one by one, the first as soon as the tile is scored.
 //
-// What bounds it. A tile is 74 KB, at the measured copy rate and 152 SMs 3,100 cycles. The tensor core
-// reads operands from shared memory at about 90 bytes a cycle: 36 x 4 KB and 16 x 6 KB are 2,700 cycles at 64 heads
-// (1,600 + 800 at 16). Two tiles in shared memory are what fits beside 64 heads of Q.
+// What bounds it. Of a tile (74 KB; 3,100 cycles of an SM's share of the measured copy rate at 1.9 GHz) the products
+// take 2,470 cycles at 64 heads: operands from shared memory come at about 90 bytes a cycle, 36 x 4 KB in 1,390 and 16 x
+// 6 KB in 1,080. The softmax between them (860, of which exponentials and stores are 550) and the handing over (150 +
+// 200) are hidden only where the next tile has landed in time: two tiles are what fits beside 64 heads of Q.
+//   - 32 sequences of 64 heads, 389,566 tokens (449 MB): 104 us, of it 88 the tiles (5.1 TB/s, 3,900 cycles each: a tile
+//     takes 2,800 from HBM, so its scores wait for it) and 10 the join;
+//   - 512 rows x 2,052 ids of 128 heads (2.3 GB out of L2): 390 us, 2,850 cycles a tile, the tensor core 87 % of them.
 //
 // Masked places: tokens that are not seen are written as zeros (no infinity meets a weight of zero) and
 // score -inf. P is rounded to bf16 (half a step is 2^-8 of a weight) because the second product takes
@@ -31,8 +36,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
-
-#include <type_traits>
 
 #include "kpool_latent.cuh"
 #include "kpool_ptx.cuh"
@@ -56,7 +59,6 @@ __host__ __device__ constexpr int part_blocks(int c) { return c == 0 ? 1 : 2; }
 constexpr int kSoftWarps = 8, kCopyWarps = 4, kMmaWarp = kSoftWarps + kCopyWarps, kSegWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSegWarp + 1);
 constexpr int kCopyRows = kKeys / kCopyWarps;  // tokens of a tile that a warp copies
-constexpr int kBoxRows = 16;                 // smallest boxes that TMA is taken for
 constexpr int kSegRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -105,8 +107,6 @@ static_assert(sizeof(Seg) <= 48, "Seg fits its space");
 // Beginning and finishing a row (Q, first product, epilogue) takes about as long as this many tiles; it is counted
 // when runs are cut, as positions before the row's first tile.
 constexpr int kRowCost = 2;
-// A run has at least this many positions.
-constexpr int kMinRun = 3;
 constexpr int kMaxRuns = 152;
 constexpr int kMaxRunRows = 8192;   // rows whose lengths a CTA adds up itself (whole rows above)
 
@@ -115,12 +115,12 @@ __device__ __forceinline__ int row_tiles(const LatentParams& p, int r) {
   return max(1, (latent_places(p, latent_seq(p, r, &b)) + kKeys - 1) / kKeys);
 }
 // Over ids every row has the tiles of the list, whatever its sequence holds.
-__device__ __forceinline__ int id_tiles(const LatentParams& p) { return max(1, (p.width + kKeys - 1) / kKeys); }
-
-__host__ __device__ __forceinline__ int64_t run_count(int64_t total, int64_t runs) {
-  const int64_t n = total / kMinRun < runs ? total / kMinRun : runs;
-  return n < 1 ? 1 : n;
+__host__ __device__ __forceinline__ int id_tiles(const LatentParams& p) {
+  return p.width <= kKeys ? 1 : (p.width + kKeys - 1) / kKeys;
 }
+
+// (Runs of three positions and more would spare joins: one row of 2,052 ids and 64 heads 22.6 us, of one 16.5.)
+__host__ __device__ __forceinline__ int64_t run_count(int64_t total, int64_t runs) { return total < runs ? total : runs; }
 
 // The positions of the runs: run r of n begins at floor(total r / n).
 struct Cuts {
@@ -251,11 +251,10 @@ __device__ __forceinline__ void soft_sync() {
   asm volatile("barrier.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
 }
 
-// box_rows: tokens of a TMA copy of the cache, 0 for none; per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
+// per: heads of a CTA (a multiple of 16 when there are several); groups: CTAs that share a run's tokens.
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                     const __grid_constant__ LatentParams p, int box_rows, int per, int groups, int direct, float* part,
-                     JoinItem* joins, WorkspaceHeader* hdr) {
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ LatentParams p, int per,
+                     int groups, int direct, float* part, JoinItem* joins, WorkspaceHeader* hdr) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
@@ -276,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int run = blockIdx.x / groups, group = blockIdx.x - run * groups, runs = gridDim.x / groups;
   const int head0 = group * per, heads = min(per, p.H - head0), cols = (heads + 15) & ~15;
   const int slots = part_rows(per);
-  const int pieces = box_rows > 0 ? kKeys / box_rows : 0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this kernel's end itself
   if (blockIdx.x == 0 && threadIdx.x == 0) hdr->error = KPOOL_OK;
@@ -402,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && !(ok = wait(q_full, q_uses & 1))) break;
       int scored = 0;  // tiles of the segment whose scores are issued
       auto score = [&](uint32_t v) {
-        ptx::fence_proxy_async_smem();  // the tile may have been written by ordinary copies
+        ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = c_desc + v % kStages * (kTileBytes >> 4);
@@ -462,13 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ptx::elect_one()) ptx::tc_commit(done);  // every MMA issued above completes before TMEM is freed
     ptx::mbar_wait_bounded(done, 0, int64_t(1) << 40, kMaxWaitNs);
   } else if (warp >= kSoftWarps) {  // --------------------------------------- copying warps
-    // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each. Whole
-    // tiles of a cache in pages of 16 tokens and more come by TMA instead, a box in four from each warp. Where a tile's
-    // tokens lie is looked up while the tile before is on its way: ids two tiles ahead, pages one.
+    // Warp w copies the tokens [16 w, 16 w + 16) of a tile, four at a time: eight lanes take 128 bytes of each. Where a
+    // tile's tokens lie is looked up while the tile before is on its way: ids two tiles ahead, pages one.
     const int w = warp - kSoftWarps, c = lane & 7, sub = lane >> 3;
     const char* base = static_cast<const char*>(p.cache) + c * 16;
     const uint32_t dst0 = ptx::smem_addr(smem + kOffTiles) + uint32_t(w * kCopyRows + sub) * 128;
-    uint32_t u = 0, by_tma_at[kStages] = {};  // 1 + the last tile of a slot where TMA brought it
+    uint32_t u = 0;
     bool ok = true, bad = false;
     const Seg* s;
     for (int i = 0;; ++i) {
@@ -477,19 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = s->n, keys = s->keys, end = s->end, kt0 = s->kt0;
       const int32_t* table = p.table + int64_t(s->seq) * p.max_pages;
       const int32_t* ids = p.ids + int64_t(s->row) * p.width;
-      auto by_tma = [&](int j) { return box_rows > 0 && (kt0 + j + 1) * kKeys <= end; };
-      // The token (of the sequence) that the lane looks up for tile j: lanes 0-15 the warp's rows of a copied tile, lanes
-      // 0-3 the first of the pieces that TMA takes; -1: none.
+      // The id at the lane's place of tile j, lanes 0-15 for the warp's tokens; -1: none.
       auto id_of = [&](int j) {
-        const int first = (kt0 + j) * kKeys;
-        if (j >= n) return -1;
-        if (by_tma(j)) return lane < pieces ? first + lane * box_rows : -1;
-        const int place = first + w * kCopyRows + lane;
-        if (lane >= kCopyRows || place >= end) return -1;
+        const int place = (kt0 + j) * kKeys + w * kCopyRows + lane;
+        if (j >= n || lane >= kCopyRows || place >= end) return -1;
         return latent_listed(p) ? ptx::ldg_ordered(ids + place) : place;
       };
       int id1 = id_of(0), page = -1, in_page = 0, id = -1;
-      auto look_up = [&]() {  // the page of the id that was read before; the next id
+      auto look_up = [&]() {  // the page of the id that was read before
         id = id1 >= 0 && id1 < keys ? id1 : -1;
         const int at = id / p.page_size;
         in_page = id - at * p.page_size;
@@ -499,14 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_up();
         id1 = id_of(1);
       }
-      for (int j = 0; ok && j < n; ++j, ++u) {
+      for (int j = 0; j < n; ++j, ++u) {
         const uint32_t st = u % kStages;
-        const bool tma = by_tma(j);
         if (id >= 0 && (page < 0 || page >= p.num_pages)) {
           bad = true;
           page = -1;
         }
-        const uint32_t bits = tma ? 0xffffu : __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t bits = __ballot_sync(0xffffffffu, page >= 0);
         // everything but the copies themselves comes before the slot is free
         const char* from[kCopyRows / 4];
         uint32_t bytes[kCopyRows / 4];
@@ -517,47 +508,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           from[q] = base + (t >= 0 ? t : 0) * 2;
           bytes[q] = t >= 0 ? 16u : 0u;
         }
-        const int box_page = page, box_in = in_page;  // (lanes 0-3)
         if (j + 1 < n) {
           look_up();
           id1 = id_of(j + 2);
         }
-        by_tma_at[st] = tma ? u + 1 : 0;
-        // TMA: a box is a block of 64 channels of a piece; this warp takes every fourth of a part's
-        int boxes = 0;
-#pragma unroll
-        for (int part = 0; part < kParts; ++part) boxes += (pieces * part_blocks(part) - w + kCopyWarps - 1) / kCopyWarps;
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
           if (u >= kStages)
             ok = __all_sync(0xffffffffu, wait_bar(empty + st * kParts + part, (u / kStages - 1) & 1, misc));
           if (!ok) break;
           __syncwarp();
-          if (part == 0 && lane == 0) {
+          if (part == 0 && lane == 0)
             reinterpret_cast<uint16_t*>(smem + kOffBits)[4 * (u % kBitsRing) + w] = uint16_t(bits);
-            // (not before the slot's last tile is scored: its phase has to be over; the arrival follows the last part)
-            if (tma) ptx::mbar_expect_tx(full + st, uint32_t(boxes * box_rows * 128));
-          }
-          if (part == 0) __syncwarp();
-          if (tma) {
-            const int box = kCopyWarps * lane + w, piece = box / part_blocks(part), h = part_block(part) + box % part_blocks(part);
-            const int z = __shfl_sync(0xffffffffu, box_in, piece & 3), y = __shfl_sync(0xffffffffu, box_page, piece & 3);
-            if (box < pieces * part_blocks(part))  // (page -1: zeros)
-              ptx::tma_load_4d(smem + kOffTiles + st * kTileBytes + h * kBlock + piece * box_rows * 128, &tm_c, full + st,
-                               64 * h, 0, z, y);
-          } else {
 #pragma unroll
-            for (int q = 0; q < kCopyRows / 4; ++q) {
-              // the row's number modulo eight permutes its 16-byte pieces
-              const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ ((q * 4 + sub) & 7)) << 4);
+          for (int q = 0; q < kCopyRows / 4; ++q) {
+            // the row's number modulo eight permutes its 16-byte pieces
+            const uint32_t dst = dst0 + st * kTileBytes + q * 512 + ((c ^ ((q * 4 + sub) & 7)) << 4);
 #pragma unroll
-              for (int h = part_block(part); h < part_block(part) + part_blocks(part); ++h)
-                ptx::cp_async_16(dst + h * kBlock, from[q] + h * 128, bytes[q]);
-            }
+            for (int h = part_block(part); h < part_block(part) + part_blocks(part); ++h)
+              ptx::cp_async_16(dst + h * kBlock, from[q] + h * 128, bytes[q]);
           }
         }
         if (!ok) break;
-        if (!tma) ptx::cp_async_arrive_inc(full + st);  // the phase waits for this lane's pieces
+        ptx::cp_async_arrive_inc(full + st);  // the phase waits for this lane's pieces
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(full + st);
       }
@@ -566,12 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(seg_empty + i % kSegRing);
     }
     if (bad) misc->bad_page = 1;
-    // every copy has landed before the CTA exits
-    ptx::cp_async_wait_all();
-#pragma unroll
-    for (int st = 0; st < kStages; ++st)
-      if (by_tma_at[st])
-        ptx::mbar_wait_bounded(full + st, ((by_tma_at[st] - 1) / kStages) & 1, int64_t(1) << 40, kMaxWaitNs);
+    ptx::cp_async_wait_all();  // every copy has landed before the CTA exits
   } else {  // ---------------------------------------------------------------- softmax
     // Warps w and w + 4 share the heads [16 w, 16 w + 16), a half of a tile's tokens each: lane 4 g + t has the heads
     // 16 w + g and 8 further, tokens 8 x + 2 t and the next of every eight. Every warp keeps the maxima of all 64 heads
@@ -917,31 +885,19 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   CUtensorMap tq;
   if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.H), kDim, p.q_ts, p.q_hs, 1, kHeads))
     return cudaErrorInvalidValue;
-  // Whole caches by TMA where the pieces that lie in one page wherever they begin, the largest power of two that divides
-  // the page size, have at least 16 tokens.
-  const int low = p.page_size & -p.page_size, box = low < kKeys ? low : kKeys;
-  const int box_rows = latent_listed(p) || box < kBoxRows ? 0 : box;
-  CUtensorMap tc = tq;
-  if (box_rows > 0 && !make_tmap_bf16_pages(&tc, p.cache, uint64_t(p.num_pages), uint64_t(p.page_size), 1, kDim, p.c_ps, p.c_ts,
-                                            kDim, uint32_t(box_rows)))
-    return cudaErrorInvalidValue;
   if (sms > kMaxRuns) sms = kMaxRuns;
   int runs = groups > sms ? 1 : sms / groups;
-  // Equal runs of tiles fill the SMs and cost a join (about four tiles' time). Lists of ids are all alike: whole
-  // rows are taken where their rounding up to the runs costs less than that.
-  const bool listed = latent_listed(p);
-  const int64_t nt = listed ? (p.width + kKeys - 1) / kKeys : 0;
-  const bool even = listed && (nt + kRowCost) * ((p.R + runs - 1) / runs) <= p.R * (nt + kRowCost) / runs + 4;
-  const bool direct = even || (!listed && p.R > kMaxRunRows);
-  if (direct && runs > p.R) runs = p.R;
-  if (!direct && listed) runs = int(run_count(int64_t(p.R) * (nt + kRowCost), runs));
+  // Equal runs of tiles fill the SMs and cost a join (whole rows where lists fill the SMs evenly: 160 rows x 2,052 ids 79.9
+  // against 79.3 us); whole rows only where there are more lengths than a CTA adds up.
+  const bool direct = !latent_listed(p) && p.R > kMaxRunRows;
+  if (!direct && latent_listed(p)) runs = int(run_count(int64_t(p.R) * (id_tiles(p) + kRowCost), runs));
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader));
   float* part = reinterpret_cast<float*>(ws + sizeof(WorkspaceHeader) + align256(sizeof(JoinItem) * kMaxRuns));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   static std::atomic<uint64_t> ready{0};
   e = allow_dynamic_smem(reinterpret_cast<const void*>(latent_tc_kernel), kSmem, &ready);
   if (e != cudaSuccess) return e;
-  latent_tc_kernel<<<runs * groups, kThreads, kSmem, stream>>>(tq, tc, p, box_rows, per, groups, direct ? 1 : 0, part, joins, hdr);
+  latent_tc_kernel<<<runs * groups, kThreads, kSmem, stream>>>(tq, p, per, groups, direct ? 1 : 0, part, joins, hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || runs < 2) return e;
   cudaLaunchConfig_t cfg{};
