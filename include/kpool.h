@@ -489,7 +489,8 @@ kpool_status kpool_attention_latent_prompt(const kpool_heads* q, const kpool_hea
  *              that are named (ids outside [0, lengths[b]) are not seen, an id that appears twice counts twice)
  *   row_seq    [q_rows] int32 (device): the row's sequence; NULL: row r is of sequence r (q_rows = num_seqs)
  * A row whose sequence does not exist gets 0 and -INFINITY (and KPOOL_ERR_INVALID_ARG is recorded). Each part is a
- * multiple of 16 bytes, key_dim + rotary_dim at most 1,024. options: KPOOL_SCORE_TC takes bf16, 512 + 64 channels.
+ * multiple of 16 bytes, key_dim + rotary_dim at most 1,024. options: KPOOL_SCORE_TC takes bf16, 512 + 64 channels (its
+ * workspace holds partial results of up to 40 MB). out and out_lse overlap no input, here and in the calls above.
  */
 #define KPOOL_WHOLE_CACHE (-1)
 size_t kpool_latent_workspace_bytes(int64_t q_rows, int32_t num_seqs, const kpool_latent_shape* shape);

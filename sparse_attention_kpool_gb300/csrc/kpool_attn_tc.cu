@@ -84,7 +84,8 @@ constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
 // The forms of the kernel: one or two row tiles of consecutive tokens, one token's heads over gathered keys, or
-// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages, by TMA; a token's heads over pages, by plain copies.
+// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages, by TMA; a
+// token's heads over pages, by plain copies.
 enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo, kPagedRows };
 
 // Where a tile of the ring lies, and the parity of its use of that slot.

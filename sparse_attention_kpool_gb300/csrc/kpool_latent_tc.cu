@@ -203,7 +203,7 @@ struct JoinItem {
 };
 static_assert(sizeof(JoinItem) == 48, "join items are laid out in the workspace");
 
-// The segments of a run: whole rows, `step` apart, or the rows of its positions.
+// The segments of a run of positions.
 struct SegIter {
   int64_t pos, hi, item;   // item: first position of the present row
   int row, c;              // c: its tiles

@@ -82,6 +82,27 @@ def test_long_caches(heads, lengths, page):
     assert torch.equal(out, again) and torch.equal(lse, alse)
 
 
+@pytest.mark.parametrize("heads", [(128, 1, 64), (80, 2, 128), (20, 1, 64), (24, 2, 128), (7, 7, 128)], ids=str)
+@pytest.mark.parametrize("page", [16, 64])
+def test_group_sizes(page, heads):
+    lengths = [300, 1, 129, 0, 2000]
+    verify(*run(lengths, page, heads, BF, "auto", seed=page), lengths, page)
+
+
+@pytest.mark.parametrize("page", [1, 16, 128])
+def test_decode_as_chunks_of_one_row(page):
+    """cu_q that gives every sequence one row: another form of the kernel, the same rows."""
+    lengths, heads = [700, 3, 0, 4000], (8, 2, 128)
+    verify(*run(lengths, page, heads, BF, "auto", q_lens=[1] * 4, seed=page), lengths, page, [1] * 4)
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (16, 1, 64)], ids=str)
+def test_drafted_rows(heads):
+    """A few rows a sequence, as drafts are verified, over long and short caches."""
+    q_lens, lengths = [4, 5, 1, 8, 3], [9000, 64, 1, 130, 3]
+    verify(*run(lengths, 16, heads, BF, "auto", q_lens=q_lens, seed=31), lengths, 16, q_lens)
+
+
 def test_more_sequences_than_the_runs_take():
     lengths = [(i * 7) % 40 for i in range(9000)]
     (q, k, v, table, scale), out, lse = run(lengths, 16, (2, 1, 64), BF, "auto", seed=6)
