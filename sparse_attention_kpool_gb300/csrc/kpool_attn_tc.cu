@@ -14,6 +14,7 @@
 //            2052 ids of 64 / 1 heads: 1222 against 288 us.)
 //   kDense   kTwo under a mask of bits for all keys (kpool_attn_dense.cu).
 //   kPagedOne, kPagedTwo   kOne and kTwo over a cache in pages, a TMA box for what lies in one page;
+//   kPagedTokens  kPagedTwo, the tokens of small pages by plain copies;
 //   kPagedRows  decode steps over pages: as kGather, but for whole caches of any length.
 //
 // Roles (12 warps; kGather 16): warps 0-3 and 4-7 are the softmax groups 0 and 1, a thread
@@ -84,9 +85,9 @@ constexpr int kBitsRing = 8;
 constexpr int kSegRing = 4;    // segments handed from the producer to the other roles
 
 // The forms of the kernel: one or two row tiles of consecutive tokens, one token's heads over gathered keys, or
-// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages, by TMA; a
-// token's heads over pages, by plain copies.
-enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo, kPagedRows };
+// two row tiles under a mask of bits for all keys (the dense form of a selection); one or two over pages, by TMA, or
+// two by plain copies; a token's heads over pages, by plain copies.
+enum Form { kOne, kTwo, kGather, kDense, kPagedOne, kPagedTwo, kPagedTokens, kPagedRows };
 
 // Where a tile of the ring lies, and the parity of its use of that slot.
 struct Place {
@@ -97,8 +98,9 @@ struct Place {
 // of their own without heads, and K and V have rings of their own.
 template <int DK, int DV, Form F>
 struct Cfg {
-  static constexpr bool TWO = F == kTwo || F == kDense || F == kPagedTwo;
-  static constexpr bool PAGED = F == kPagedOne || F == kPagedTwo || F == kPagedRows;
+  static constexpr bool TOKENS = F == kPagedTokens;
+  static constexpr bool TWO = F == kTwo || F == kDense || F == kPagedTwo || TOKENS;
+  static constexpr bool PAGED = F == kPagedOne || F == kPagedTwo || F == kPagedRows || TOKENS;
   static constexpr bool SHARED = DK != DV;
   static constexpr bool GATHER = F == kGather || F == kPagedRows;  // keys come by plain copies
   using Params = std::conditional_t<PAGED, AttnPagedParams, std::conditional_t<SHARED, AttnSharedParams, AttnParams>>;
@@ -477,6 +479,12 @@ __host__ __device__ __forceinline__ int piece_rows(int page_size) {
   return low < kTile<AttnPagedParams> ? low : kTile<AttnPagedParams>;
 }
 
+// Pages follow one another in memory, so that a token of the pool has a number.
+bool pages_adjoin(const AttnPagedParams& p) {
+  return p.k_ps == p.page_size * p.k_ts && p.v_ps == p.page_size * p.v_ts &&
+         int64_t(p.num_pages) * p.page_size <= INT32_MAX && attn_gather_supported(p.k_ts, p.v_ts);
+}
+
 // Bounded wait; also gives up when another role did.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -540,6 +548,21 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const char* base, int t
    ...);
 }
 
+// The same, for rows of which some may be absent (token -1): zeros.
+template <int kRowsPer>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const char* base, int tok, uint32_t ts_bytes, int rsub) {
+  if (__all_sync(0xffffffffu, tok >= 0)) {
+    fetch_rows<kRowsPer>(dst, base, tok, ts_bytes, rsub, std::make_integer_sequence<int, 32 / kRowsPer>{});
+    return;
+  }
+#pragma unroll 4
+  for (int i = 0; i < 32 / kRowsPer; ++i) {
+    const int t = __shfl_sync(0xffffffffu, tok, rsub + kRowsPer * i);
+    const char* from = base + uint64_t(uint32_t(max(t, 0))) * ts_bytes;
+    ptx::cp_async_16((dst ^ (((kRowsPer * i) & 7) << 4)) + kRowsPer * i * 128, from, t >= 0 ? 16u : 0u);
+  }
+}
+
 // 32 N columns of scores from TMEM column `col` on.
 template <int N>
 __device__ __forceinline__ void load_scores(uint32_t col, uint32_t (&s)[N][32]) {
@@ -598,7 +621,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
                    JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<DK, DV, F>;
   constexpr int kTileKeys = C::kTileKeys, kPCol = C::kPCol;
-  constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, LISTED = F == kGather;
+  constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, TOKENS = C::TOKENS,
+                 LISTED = F == kGather;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -754,17 +778,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           ++tile;
         }
         const char* base = static_cast<const char*>(src) + (int64_t(sg->hk) * hs + c * 8) * 2;
-        const uint32_t dst = dst0 + st * C::kTileBytes;
-        if (__all_sync(0xffffffffu, tok >= 0)) {
-          fetch_rows<kRowsPer>(dst, base, tok, ts_bytes, rsub, std::make_integer_sequence<int, 32 / kRowsPer>{});
-        } else {
-#pragma unroll 4
-          for (int i = 0; i < 32 / kRowsPer; ++i) {
-            const int t = __shfl_sync(0xffffffffu, tok, rsub + kRowsPer * i);
-            const char* from = base + uint64_t(uint32_t(max(t, 0))) * ts_bytes;
-            ptx::cp_async_16((dst ^ (((kRowsPer * i) & 7) << 4)) + kRowsPer * i * 128, from, t >= 0 ? 16u : 0u);
-          }
-        }
+        copy_rows<kRowsPer>(dst0 + st * C::kTileBytes, base, tok, ts_bytes, rsub);
         ptx::cp_async_arrive(full + st);                     // when this lane's pieces have landed
         if (lane == 0) ptx::mbar_arrive(full + st);          // and the warp's word of bits is written
         return true;
@@ -807,9 +821,25 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         Seg sg{};
         // Pages of the lane's first piece: of the tile whose K is loaded next, of the tiles before, whose V is; the next one.
         [[maybe_unused]] int rows = 1, pages[C::kAhead + 1] = {}, next_page = -1;
+        // Or, token by token: the lane's keys lane, lane + 32, ... of those tiles as tokens of the pool (-1: none).
+        constexpr int kOwn = kTileKeys / 32, kChunks = DK / 8, kRowsPer = 32 / kChunks;
+        [[maybe_unused]] int toks[C::kAhead + 1][kOwn] = {}, next_pages[kOwn] = {};
         if constexpr (PAGED) rows = piece_rows(p.page_size);
         auto read_page = [&](int kt) {
-          if constexpr (PAGED) {
+          if constexpr (TOKENS) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+              const int j = kt * kTileKeys + lane + 32 * i, before = j - kTileKeys;
+              const bool have = kt > sg.kt0 && next_pages[i] >= 0 && next_pages[i] < p.num_pages;
+#pragma unroll
+              for (int x = C::kAhead; x > 0; --x) toks[x][i] = toks[x - 1][i];
+              toks[0][i] = have ? next_pages[i] * p.page_size + before % p.page_size : -1;
+              bad_page |= !have && kt > sg.kt0 && before < sg.end;
+              next_pages[i] = -1;
+              if (j < sg.end)
+                next_pages[i] = ptx::ldg_ordered(p.table + int64_t(sg.sq.k0) * p.max_pages + j / p.page_size);
+            }
+          } else if constexpr (PAGED) {
 #pragma unroll
             for (int x = C::kAhead; x > 0; --x) pages[x] = pages[x - 1];
             pages[0] = next_page;
@@ -831,7 +861,24 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           ++f;
           uint8_t* dst = smem + C::kOffRing + C::slot_at(st);
           const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-          if constexpr (PAGED) {
+          if constexpr (TOKENS) {
+            const char* base = static_cast<const char*>(is_k ? p.k : p.v) +
+                               (int64_t(sg.hk) * (is_k ? p.k_hs : p.v_hs) + (lane % kChunks) * 8) * 2;
+            const uint32_t ts_bytes = uint32_t((is_k ? p.k_ts : p.v_ts) * 2);
+            const int rsub = lane / kChunks;
+            // (as the gathering warps place their pieces)
+            const uint32_t to = ptx::smem_addr(dst) + uint32_t(lane % kChunks >> 3) * C::kHalf + uint32_t(rsub) * 128 +
+                                (((lane & 7) ^ rsub) << 4);
+#pragma unroll
+            for (int x = 0; x < kOwn; ++x) {
+              const int tok = is_k ? toks[0][x] : toks[C::kAhead][x];
+              if (!__any_sync(0xffffffffu, tok >= 0)) continue;  // keys past the last one that a row sees
+              copy_rows<kRowsPer>(to + x * 32 * 128, base, tok, ts_bytes, rsub);
+            }
+            ptx::cp_async_arrive_inc(full + st);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full + st);
+          } else if constexpr (PAGED) {
             // Pieces of `rows` keys lie in one page each; the keys past the last one that a row sees are not loaded.
             const int key0 = kt * kTileKeys, pieces = min(kTileKeys / rows, (sg.end - key0 + rows - 1) / rows);
             if (lane == 0) ptx::mbar_arrive_expect_tx(full + st, uint32_t(pieces * rows * 128 * C::kVBlocks));
@@ -896,6 +943,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           if (!ok) break;
         }
         if (PAGED && bad_page) misc->bad_page = 1;
+        if (TOKENS) ptx::cp_async_wait_all();
         // every copy armed above lands before the CTA exits
         auto land = [&](uint32_t first, uint32_t depth, uint32_t f) {
           for (uint32_t s2 = 0; s2 < depth && s2 < f; ++s2)
@@ -923,7 +971,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
         const Seg* sg;
         auto landed = [&](Place u) {
           const bool r = wait_bar(full + u.slot, u.par, misc);
-          if (GATHER) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
+          if (GATHER || TOKENS) ptx::fence_proxy_async_smem();  // the tile was written by ordinary copies
           return r;
         };
         // The issuers take turns, a tile's P V and the next tile's Q K^T at a time. Left to themselves
@@ -1530,14 +1578,14 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
   if (!make_tmap_bf16_heads(&tq, p.q, uint64_t(p.R), uint64_t(p.Hq), DK, p.q_ts, p.q_hs, uint32_t(tt), uint32_t(p.G)))
     return cudaErrorInvalidValue;
   tk = tv = tr = tq;  // (gathered: not used, keys and values come by plain copies)
-  if constexpr (C::PAGED && !GATHER) {
+  if constexpr (C::PAGED && !GATHER && !C::TOKENS) {
     const uint32_t rows = uint32_t(piece_rows(p.page_size));
     if (!make_tmap_bf16_pages(&tk, p.k, uint64_t(p.num_pages), uint64_t(p.page_size), uint64_t(p.Hkv), DK, p.k_ps, p.k_ts,
                               p.k_hs, rows) ||
         !make_tmap_bf16_pages(&tv, p.v, uint64_t(p.num_pages), uint64_t(p.page_size), uint64_t(p.Hkv), DV, p.v_ps, p.v_ts,
                               p.v_hs, rows))
       return cudaErrorInvalidValue;
-  } else if (!GATHER) {
+  } else if (!GATHER && !C::TOKENS) {
     if (!make_tmap_bf16_heads(&tk, p.k, uint64_t(p.T), uint64_t(p.Hkv), DV, p.k_ts, p.k_hs, C::kTileKeys, 1) ||
         !make_tmap_bf16_heads(&tv, p.v, uint64_t(p.T), uint64_t(p.Hkv), DV, p.v_ts, p.v_hs, C::kTileKeys, 1))
       return cudaErrorInvalidValue;
@@ -1653,17 +1701,22 @@ cudaError_t launch_attn_tc(const AttnParams& p, char* ws, cudaStream_t stream) {
 cudaError_t launch_attn_tc(const AttnPagedParams& p, char* ws, cudaStream_t stream) {
   // Decode steps by plain copies, where the pages follow one another in memory; chunks by TMA, a box for what lies in one
   // page (us, 32 / 8 heads of 128, plain copies / TMA): 16 decode tokens over pages of 8 132 / 268, of 16 132 / 187, of
-  // 64 131 / 136; a chunk of 300 rows over 12,000 keys by TMA 480 with pages of 1, 107 of 8, 83 of 16, 70 of 64.
-  const bool rows = p.cu_q == nullptr && p.k_ps == p.page_size * p.k_ts && p.v_ps == p.page_size * p.v_ts &&
-                    int64_t(p.num_pages) * p.page_size <= INT32_MAX && attn_gather_supported(p.k_ts, p.v_ts);
+  // 64 131 / 136. Chunks copy the tokens of pages whose boxes are one or two keys high, with one warp, as fast for any
+  // pages: 300 rows over 12,000 keys 169 / 481 with pages of 1, 169 / 264 of 2 and 6, against 154 of 4, 107 of 8, 83 of 16, 70
+  // of 64 by TMA; eight chunks of 20 over 700 43 / 86 and 43 / 53. (By both ways in one kernel the loading warp's registers
+  // do not suffice: 5 to 10 % more with pages of 64.)
+  const bool adjoin = pages_adjoin(p), rows = p.cu_q == nullptr && adjoin;
+  const bool tokens = adjoin && piece_rows(p.page_size) <= 2;
   const bool two = int64_t(p.R) > int64_t(p.S) * (kTileRows / p.G);  // (as above)
   if (p.D == 64)
-    return rows  ? launch<64, 64, kPagedRows>(p, ws, stream)
-           : two ? launch<64, 64, kPagedTwo>(p, ws, stream)
-                 : launch<64, 64, kPagedOne>(p, ws, stream);
-  return rows  ? launch<128, 128, kPagedRows>(p, ws, stream)
-         : two ? launch<128, 128, kPagedTwo>(p, ws, stream)
-               : launch<128, 128, kPagedOne>(p, ws, stream);
+    return rows     ? launch<64, 64, kPagedRows>(p, ws, stream)
+           : tokens ? launch<64, 64, kPagedTokens>(p, ws, stream)
+           : two    ? launch<64, 64, kPagedTwo>(p, ws, stream)
+                    : launch<64, 64, kPagedOne>(p, ws, stream);
+  return rows     ? launch<128, 128, kPagedRows>(p, ws, stream)
+         : tokens ? launch<128, 128, kPagedTokens>(p, ws, stream)
+         : two    ? launch<128, 128, kPagedTwo>(p, ws, stream)
+                  : launch<128, 128, kPagedOne>(p, ws, stream);
 }
 
 cudaError_t launch_attn_tc(const AttnSharedParams& p, char* ws, cudaStream_t stream) {

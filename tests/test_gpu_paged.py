@@ -103,6 +103,70 @@ def test_drafted_rows(heads):
     verify(*run(lengths, 16, heads, BF, "auto", q_lens=q_lens, seed=31), lengths, 16, q_lens)
 
 
+SMALL_PAGES = [1, 2, 3, 6, 130]  # pieces of one or two tokens
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (16, 1, 64), (6, 2, 128), (128, 1, 128)], ids=str)
+@pytest.mark.parametrize("page", SMALL_PAGES)
+def test_chunks_over_small_pages(page, heads):
+    """Many tiles a run, sequences of one to all of their rows; the same call twice, bit for bit."""
+    q_lens, lengths = [300, 1, 0, 7, 129, 64], [3001, 127, 50, 129, 129, 2048]
+    made, out, lse = run(lengths, page, heads, BF, "auto", q_lens=q_lens, seed=page)
+    verify(made, out, lse, lengths, page, q_lens)
+    _, again, alse = run(lengths, page, heads, BF, "auto", q_lens=q_lens, tensors=made[:3], pool=(None, made[3]))
+    assert torch.equal(out, again) and torch.equal(lse, alse)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("page", SMALL_PAGES)
+def test_behind_the_last_key_of_small_pages(page, bad):
+    lengths, heads, q_lens = [150, 20, 700, 0, 128], (8, 2, 128), [3, 1, 40, 1, 128]
+    total, table = S.pool(lengths, page, random.Random(40))
+    q, k, v = make(40, sum(q_lens), total, page, heads, BF)
+    free = torch.ones(total * page, dtype=torch.bool, device="cuda")
+    free[torch.cat(S.slots(table, lengths, page)).cuda()] = False
+    kb, vb = k.clone(), v.clone()
+    for t in (kb, vb):
+        t.flatten(0, 1)[free] = bad
+    made, out, lse = run(lengths, page, heads, BF, "auto", q_lens=q_lens, tensors=(q, kb, vb), pool=(total, table))
+    verify((q, k, v, table, made[4]), out, lse, lengths, page, q_lens)
+
+
+def test_seen_nan_and_infinite_values_in_small_pages():
+    page, lengths, q_lens = 2, [200], [150]
+    total, table = S.pool(lengths, page, random.Random(41))
+    q, k, v = make(41, 150, total, page, (4, 2, 128), BF)
+    at = S.slots(table, lengths, page)[0]
+    v.flatten(0, 1)[at[130], 0, 5] = math.nan
+    v.flatten(0, 1)[at[140], 1, 7] = math.inf
+    _, out, _ = run(lengths, page, (4, 2, 128), BF, "auto", q_lens=q_lens, tensors=(q, k, v), pool=(total, table))
+    nan, inf = torch.isnan(out), torch.isinf(out)
+    assert nan[80:, :2, 5].all() and not nan[:80].any() and nan.sum() == 70 * 2
+    assert (out[90:, 2:, 7] == math.inf).all() and inf.sum() == 60 * 2
+
+
+def test_small_pages_apart_and_not_there():
+    """Pages with a gap between them (another form), and one that the pool does not have, reported."""
+    lengths, heads, q_lens, page = [300, 40], (8, 2, 128), [90, 40], 2
+    total, table = S.pool(lengths, page, random.Random(42))
+    q, k, v = make(42, 130, total, page, heads, BF)
+    apart = [torch.full((total, 3, 2, 128), math.nan, dtype=BF, device="cuda")[:, :2] for _ in range(2)]
+    for t, x in zip(apart, (k, v)):
+        t.copy_(x)
+    made, out, lse = run(lengths, page, heads, BF, "auto", q_lens=q_lens, tensors=(q, *apart), pool=(total, table))
+    verify((q, k, v, table, made[4]), out, lse, lengths, page, q_lens)
+    ws = K.new_attention_workspace(130, 2, *heads, BF)
+    for bad in (total, -1, 2 ** 31 - 1):
+        t = table.clone()
+        t[0, 70] = bad
+        got, glse = K.kpool_attention_paged(q, k, v, t.cuda(), i32(lengths), made[4], cu_q=i32([0, 90, 130]),
+                                            return_lse=True, workspace=ws)
+        assert K.kpool_last_device_error(ws) == K.KPOOL_ERR_INVALID_ARG
+        see = S.see_paged(table, lengths, page, q_lens)
+        ref = S.attend(q, k.flatten(0, 1), v.flatten(0, 1), see, made[4])
+        A.check(got[90:], glse[90:], [x[90:] for x in ref])
+
+
 def test_more_sequences_than_the_runs_take():
     lengths = [(i * 7) % 40 for i in range(9000)]
     (q, k, v, table, scale), out, lse = run(lengths, 16, (2, 1, 64), BF, "auto", seed=6)
