@@ -84,10 +84,14 @@ struct AttnSeq {
 
 // First query row of sequence b (b <= S).
 template <class P>
-__device__ __forceinline__ int attn_q0(const P& p, int b) {
+__host__ __device__ __forceinline__ int attn_q0(const P& p, int b) {
   if constexpr (kPagedKeys<P>)
     if (p.cu_q == nullptr) return b;
+#ifdef __CUDA_ARCH__
   return __ldg(p.cu_q + b);
+#else
+  return p.cu_q[b];
+#endif
 }
 
 // Keys that a sequence's pages can hold.
@@ -168,16 +172,31 @@ __device__ __forceinline__ int attn_keys_end(const AttnParams& p, const AttnSeq&
 // ceil(n / tt) of them, at most floor(cu[b+1]/tt) - floor(cu[b]/tt) + 1, so the ranges
 // do not overlap, R / tt + S numbers cover all, and a binary search finds a number's
 // sequence without any scan or planning kernel; numbers without a tile are skipped.
-inline int64_t attn_tiles(int64_t R, int64_t S, int64_t tt) { return R / tt + S; }
+// A form that takes one row of every sequence (kRows) numbers its tiles by the sequences themselves, R = S of them.
+// (Not every tile of one token is such a form's: groups of 65 to 128 heads leave row tiles of one token in any call.)
+template <bool kRows>
+inline int64_t attn_tiles(int64_t R, int64_t S, int64_t tt) { return kRows ? R : R / tt + S; }
 
 template <class P>
-__device__ __forceinline__ int attn_seq_of_tile(const P& p, int tile, int tt) {
+__host__ __device__ __forceinline__ int attn_seq_of_tile(const P& p, int tile, int tt) {
   int lo = 0, hi = p.S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (attn_q0(p, mid) / tt + mid <= tile) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// Sequence and first token of tile number `tile` < attn_tiles; the number has no tile where the token is negative or
+// not one of the sequence's.
+struct TilePlace {
+  int b, tok0;
+};
+template <bool kRows, class P>
+__host__ __device__ __forceinline__ TilePlace attn_tile_place(const P& p, int tile, int tt) {
+  if (kRows) return {tile, 0};
+  const int b = attn_seq_of_tile(p, tile, tt);
+  return {b, (tile - (attn_q0(p, b) / tt + b)) * tt};
 }
 
 // The header's error word, first and last: one thread clears it at the start of the call, and one warp

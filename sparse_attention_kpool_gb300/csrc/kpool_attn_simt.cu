@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
     ids = p.ids + int64_t(r) * p.width;
     end = sq.nk > 0 ? p.width : 0;
   } else {
-    const int b = attn_seq_of_tile(p, blockIdx.x, tt);
-    sq = attn_seq(p, b);
-    i0 = (int(blockIdx.x) - (attn_q0(p, b) / tt + b)) * tt;
+    const TilePlace at = attn_tile_place<false>(p, blockIdx.x, tt);
+    sq = attn_seq(p, at.b);
+    i0 = at.tok0;
     if (i0 < 0 || i0 >= sq.nq) {
       __syncwarp();
       if (checks && threadIdx.x < 32) attn_check(p, hdr);
@@ -325,7 +325,7 @@ cudaError_t launch_family(const P& p, kpool_dtype dtype, char* ws, cudaStream_t 
   // heads of a group share the CTA's key blocks; what is left of the 16 slots takes more tokens
   const int gt = p.G < kVRows ? p.G : kVRows;
   const int tt = p.mode == kAttnSelected ? 1 : kVRows / gt;
-  const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles(p.R, p.S, tt);
+  const int64_t tiles = p.mode == kAttnSelected ? p.R : attn_tiles<false>(p.R, p.S, tt);
   const dim3 grid(uint32_t(tiles), uint32_t(p.Hkv * ((p.G + gt - 1) / gt)));
   WorkspaceHeader* hdr = reinterpret_cast<WorkspaceHeader*>(ws);
   const bool narrow = value_channels(p) <= 128;

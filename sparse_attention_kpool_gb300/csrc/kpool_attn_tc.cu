@@ -304,23 +304,12 @@ struct SegIter {
 };
 
 // One CTA per row tile: head by head (a head's K and V stay in L2), the deepest row tiles of each first.
-template <class P>
+template <bool kRows, class P>
 __device__ __forceinline__ bool direct_seg(const P& p, int ttb, int tiles, Seg* s) {
   s->hk = blockIdx.x / tiles;
-  const int tile = tiles - 1 - int(blockIdx.x % tiles);
-  int b;
-  if constexpr (kPagedKeys<P>) b = ttb == 1 ? tile : attn_seq_of_tile(p, tile, ttb);  // (a row per sequence)
-  else b = attn_seq_of_tile(p, tile, ttb);
-  s->sq = attn_seq(p, b);
-  if constexpr (kPagedKeys<P>)
-    if (ttb == 1) {
-      s->tok0 = s->kt0 = 0;
-      s->n = tile_cost(p, s->sq, 0, 1);
-      s->whole = 1;
-      s->slot = 0;
-      return s->sq.nq > 0;
-    }
-  s->tok0 = (tile - (attn_q0(p, b) / ttb + b)) * ttb;
+  const TilePlace at = attn_tile_place<kRows>(p, tiles - 1 - int(blockIdx.x % tiles), ttb);
+  s->sq = attn_seq(p, at.b);
+  s->tok0 = at.tok0;
   if (s->tok0 < 0 || s->tok0 >= s->sq.nq) return false;
   s->kt0 = 0;
   s->n = tile_cost(p, s->sq, s->tok0 / ttb, ttb);
@@ -622,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
   using C = Cfg<DK, DV, F>;
   constexpr int kTileKeys = C::kTileKeys, kPCol = C::kPCol;
   constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, TOKENS = C::TOKENS,
-                 LISTED = F == kGather;
+                 LISTED = F == kGather, ROWS = F == kPagedRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -720,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           const int64_t at = pos;
           bool more;
           if constexpr (LISTED) more = gather_seg(p, &pos, misc->hi, &sg);
-          else more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          else more = direct ? i == 0 && direct_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
           if (i == 0 && !direct && !p.list) {  // (else whole items: nothing to join)
             if (!more) joins[blockIdx.x].runs = 0;
             else if constexpr (LISTED)
@@ -911,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           return true;
         };
         for (int i = 0;; ++i) {
-          const bool more = direct ? i == 0 && direct_seg(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          const bool more = direct ? i == 0 && direct_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
           if (i == 0 && !direct && lane == 0) {
             if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
             else joins[blockIdx.x].runs = 0;
@@ -1593,7 +1582,7 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
       if (!make_tmap_bf16_heads(&tr, p.kr, uint64_t(p.T), 1, DK - DV, p.kr_ts, DK - DV, C::kTileKeys, 1))
         return cudaErrorInvalidValue;
   }
-  const int64_t tiles = GATHER ? p.R : attn_tiles(p.R, p.S, ttb);
+  const int64_t tiles = attn_tiles<GATHER>(p.R, p.S, ttb);  // (gathered: a row each)
   const int64_t items = tiles * p.Hkv;
   // Equal runs of all K/V tiles fill the SMs whatever the lengths are, and cost a join (about five tiles' time)
   // and the starts of the items they cut. Whole items, one to a CTA, are taken instead (us, 32 / 8 heads of 128
