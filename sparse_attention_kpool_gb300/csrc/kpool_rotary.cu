@@ -5,9 +5,9 @@
 //
 // Angles. Only x modulo a turn matters, and t is a whole number: the table holds f[i] / 2 pi as a
 // 64-bit fraction of a turn, and the low 64 bits of t times that are the fraction of a turn at t,
-// exact but for the table's own rounding (t 2^-65 turns) however far t is. In fp32 t f[i] at a million
-// tokens would be off by 0.06, and in fp64 the reduction would cost what the rest does. The top 32 bits go to
-// fp32 (half a step of pi is 1e-7), then through sincospif.
+// exact but for the table's own error, which kpool_rotary_table keeps to a few units of 2^-64 turns (t of them at t: 2^-30
+// of a half turn at 2^31). In fp32 t f[i] at a million tokens would be off by 0.06, and in fp64 the reduction would cost
+// what the rest does. The top 32 bits go to fp32 (half a step is 2^-25 of a half turn at most), then through sincospif.
 //
 // What bounds it. Every channel is read and written once and a pair takes six operations: HBM. A thread has
 // eight bf16 (four fp32) pairs of a token, takes their cosines and sines once and applies them to several
@@ -188,16 +188,21 @@ kpool_status kpool_rotary_table(int32_t rotary_dim, double base, double factor, 
   if (!(isfinite(original_length) && original_length >= 0.0)) return KPOOL_ERR_INVALID_ARG;
   if (original_length > 0.0 && !(isfinite(low) && isfinite(high) && low >= 0.0 && high > low))
     return KPOOL_ERR_INVALID_ARG;
-  const double turn = 6.283185307179586476925;
+  // In long double, whose 64 bits or more are the table's: in double the fast pairs would be off by 2^-56 of a turn and
+  // more, at a position of 2^31 by more than fp32 leaves. (2 pi as two doubles.)
+  const long double turn = static_cast<long double>(6.283185307179586476925) + 2.449293598294706414e-16;
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    const double f = pow(base, -2.0 * i / rotary_dim);
-    double keep = 0.0;
-    if (original_length > 0.0) keep = fmin(1.0, fmax(0.0, (original_length * f / turn - low) / (high - low)));
-    const double g = f * (keep + (1.0 - keep) / factor) / turn;
-    // a fraction of a turn, in units of 2^-64 (a double has 53 bits of it; whole turns do not matter)
-    const double frac = fmod(g, 1.0);
-    if (!isfinite(frac)) return KPOOL_ERR_INVALID_ARG;
-    out[i] = int64_t(uint64_t(frac * 0x1p64 + 0.5));
+    const long double f = powl(base, -2.0L * i / rotary_dim);
+    long double keep = 0.0L;
+    if (original_length > 0.0) {
+      const long double at = (original_length * f / turn - low) / (static_cast<long double>(high) - low);
+      keep = fminl(1.0L, fmaxl(0.0L, at));
+    }
+    const long double g = f * (keep + (1.0L - keep) / factor) / turn;
+    if (!isfinite(static_cast<double>(g))) return KPOOL_ERR_INVALID_ARG;
+    // a fraction of a turn, in units of 2^-64 (whole turns do not matter, one that it rounds up to included)
+    const long double units = floorl(ldexpl(fmodl(g, 1.0L), 64) + 0.5L);
+    out[i] = units < ldexpl(1.0L, 64) ? int64_t(uint64_t(units)) : 0;
   }
   return KPOOL_OK;
 }
