@@ -95,7 +95,7 @@ __host__ __device__ __forceinline__ int attn_q0(const P& p, int b) {
 }
 
 // Keys that a sequence's pages can hold.
-__device__ __forceinline__ int64_t attn_page_keys(const AttnPagedParams& p) {
+__host__ __device__ __forceinline__ int64_t attn_page_keys(const AttnPagedParams& p) {
   return int64_t(p.max_pages) * p.page_size;
 }
 
@@ -262,7 +262,8 @@ __device__ __forceinline__ void attn_selected_seq(const AttnParams& p, int r, in
 
 // The persistent tensor-core form: its runs (CTAs) and the sequences it takes. Beside it, whole row tiles per CTA
 // (kpool_attn_tc.cu, launch): up to kAttnWholeKeys keys; kAttnLikeKeys keys a sequence at one or two row tiles
-// per SM; from kAttnDirectItems row tiles per SM and kAttnDirectKeys keys a sequence on.
+// per SM; from kAttnDirectItems row tiles per SM and kAttnDirectKeys keys a sequence on. (Over pages the host knows no
+// lengths: the first by what a table can hold, the last by the device.)
 constexpr int kAttnMaxRuns = 152;
 constexpr int kAttnMaxRunSeqs = 8192;
 constexpr int kAttnWholeKeys = 1024;

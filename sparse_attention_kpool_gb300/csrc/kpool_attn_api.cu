@@ -260,8 +260,6 @@ kpool_status kpool_attention_paged(const kpool_heads* q, const kpool_pages* k, c
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.num_pages = num_pages;
-  const int64_t named = int64_t(num_seqs) * max_pages;
-  p.T = (named < num_pages ? named : num_pages) * page_size;  // keys that the call may see
   char* ws = static_cast<char*>(workspace);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   const bool tc = tc_ok && some && kernel != KPOOL_SCORE_SIMT;

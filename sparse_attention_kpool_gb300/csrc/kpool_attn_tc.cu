@@ -162,6 +162,7 @@ struct Misc {
   int64_t total;
   int32_t runs;       // runs that have tiles
   int32_t b;
+  int32_t whole;      // pages: row tiles of a head where the lengths want whole items, else 0
   uint32_t tmem;
   volatile int32_t abort;
   volatile int32_t bad_page;           // a page of the table that the pool does not have
@@ -301,11 +302,49 @@ struct SegIter {
     pos = tile0 + s->kt0 + s->n;
     return true;
   }
+
+  // The same for whole items, every grid-th to a CTA in the order of whole_seg, without gaps in their numbers (which would
+  // leave some CTAs an item more than others). pos and item count a head's row tiles here.
+  __device__ __forceinline__ void start_whole(int head_tiles) {
+    hi = head_tiles;
+    pos = hi + blockIdx.x;  // (the first head begins like the others)
+    hk = -1;
+  }
+  template <class P>
+  __device__ __forceinline__ bool next_whole(const P& p, int ttb, Seg* s) {
+    while (pos >= hi) {
+      pos -= hi;
+      if (++hk == p.Hkv) return false;
+      b = p.S;
+      item = 0;
+      nt = 0;
+    }
+    while (pos >= item + nt) {
+      if (--b < 0) return false;
+      item += nt;
+      sq = attn_seq(p, b);
+      nt = row_tiles(sq, ttb);
+    }
+    t = nt - 1 - int(pos - item);
+    s->sq = sq;
+    s->hk = hk;
+    s->tok0 = t * ttb;
+    s->kt0 = 0;
+    s->n = tile_cost(p, sq, t, ttb);
+    s->whole = 1;
+    s->slot = 0;
+    pos += gridDim.x;
+    return true;
+  }
 };
+
+// How the work is cut: into runs; into whole items, one to a CTA; or into runs or whole items as the lengths say, which
+// over pages the device alone knows.
+enum Cut { kRuns, kWhole, kByLengths };
 
 // One CTA per row tile: head by head (a head's K and V stay in L2), the deepest row tiles of each first.
 template <bool kRows, class P>
-__device__ __forceinline__ bool direct_seg(const P& p, int ttb, int tiles, Seg* s) {
+__device__ __forceinline__ bool whole_seg(const P& p, int ttb, int tiles, Seg* s) {
   s->hk = blockIdx.x / tiles;
   const TilePlace at = attn_tile_place<kRows>(p, tiles - 1 - int(blockIdx.x % tiles), ttb);
   s->sq = attn_seq(p, at.b);
@@ -384,7 +423,7 @@ struct Cuts {
 // Every thread of the CTA: this CTA's run of positions [total * i / n, total * (i + 1) / n)
 // and the sequence it starts in. `scratch` holds S 64-bit words of shared memory.
 template <class P>
-__device__ __forceinline__ void find_run(const P& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas,
+__device__ __forceinline__ void find_run(const P& p, int ttb, int64_t* scratch, int64_t i, int64_t ctas, int cut,
                                          Misc* m) {
   for (int b = threadIdx.x; b < p.S; b += blockDim.x) scratch[b] = seq_cost(p, attn_seq(p, b), ttb);
   __syncthreads();
@@ -394,6 +433,24 @@ __device__ __forceinline__ void find_run(const P& p, int ttb, int64_t* scratch, 
     for (int b = lane; b < p.S; b += 32) sum += scratch[b];
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (kPagedKeys<P> && cut == kByLengths) {
+      int64_t keys = 0;
+      int tiles = 0, most = 0;
+      for (int b = lane; b < p.S; b += 32) {
+        const AttnSeq s = attn_seq(p, b);
+        keys += s.nk;
+        most = max(most, s.nk);
+        tiles += row_tiles(s, ttb);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        keys += __shfl_xor_sync(0xffffffffu, keys, d);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+      }
+      if (lane == 0)
+        m->whole = keys >= int64_t(kAttnDirectKeys) * p.S && int64_t(most) * p.S <= 2 * keys ? tiles : 0;
+    }
     const int64_t n = run_count(sum, ctas);
     const Cuts cuts(sum, uint32_t(n));
     const int64_t lo = i < n ? cuts.lo(uint32_t(i)) : sum, hi = i < n ? cuts.lo(uint32_t(i) + 1) : sum;
@@ -606,7 +663,7 @@ template <int DK, int DV, Form F>
 __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
-                   const __grid_constant__ typename Cfg<DK, DV, F>::Params p, int tiles, int direct, float* part, int slot_rows,
+                   const __grid_constant__ typename Cfg<DK, DV, F>::Params p, int tiles, int cut, float* part, int slot_rows,
                    JoinItem* joins, WorkspaceHeader* hdr) {
   using C = Cfg<DK, DV, F>;
   constexpr int kTileKeys = C::kTileKeys, kPCol = C::kPCol;
@@ -638,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
   // dense form: with nothing but finite values there is nothing to clean
   const bool no_cleaning = GATHER || (DENSE && p.dense->finite);
   if (DENSE && !p.dense->enabled) {  // the gathering kernel does all rows
-    if (threadIdx.x == 0 && !direct) joins[blockIdx.x].runs = 0;
+    if (threadIdx.x == 0 && cut != kWhole) joins[blockIdx.x].runs = 0;
     return;
   }
   if constexpr (LISTED) {
@@ -651,8 +708,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       misc->lo = lo;
       misc->hi = hi;
     }
-  } else if (!direct) {
-    find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, misc);
+  } else if (cut != kWhole) {
+    find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, cut, misc);
     ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
   }
   if (threadIdx.x == 0) {
@@ -689,6 +746,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc->tmem;
+  const int whole = F == kPagedTwo && cut == kByLengths ? misc->whole : 0;  // (row tiles of a head)
 
   // the segment with number i, once the producer has written it (null: give up)
   auto segment = [&](int i) -> const Seg* {
@@ -702,15 +760,15 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
         int64_t pos = LISTED ? misc->lo : 0;
         SegIter it;
-        if (!LISTED && !direct) it.start(p, misc, ttb);
+        if (!LISTED && cut == kRuns) it.start(p, misc, ttb);
         uint32_t q_loads = 0;
         Seg sg{};
         for (int i = 0;; ++i) {
           const int64_t at = pos;
           bool more;
           if constexpr (LISTED) more = gather_seg(p, &pos, misc->hi, &sg);
-          else more = direct ? i == 0 && direct_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
-          if (i == 0 && !direct && !p.list) {  // (else whole items: nothing to join)
+          else more = cut == kWhole ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          if (i == 0 && cut != kWhole && !p.list) {  // (else whole items: nothing to join)
             if (!more) joins[blockIdx.x].runs = 0;
             else if constexpr (LISTED)
               write_join(joins + blockIdx.x, sg, at - sg.kt0, gather_tiles(p), gather_total(p), blockIdx.x, gridDim.x);
@@ -804,7 +862,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       // One lane, or over pages all of them, each with its own pieces of a tile.
       if (PAGED || lane == 0) {
         SegIter it;
-        if (!direct) it.start(p, misc, ttb);
+        if (whole) it.start_whole(whole);
+        else if (cut != kWhole) it.start(p, misc, ttb);
         uint32_t fills[2] = {0, 0}, q_loads = 0;  // of the ring, or of K's and V's
         bool ok = true, bad_page = false;
         Seg sg{};
@@ -900,9 +959,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           return true;
         };
         for (int i = 0;; ++i) {
-          const bool more = direct ? i == 0 && direct_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
-          if (i == 0 && !direct && lane == 0) {
-            if (more) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
+          const bool more = cut == kWhole ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg)
+                            : whole       ? it.next_whole(p, ttb, &sg)
+                                          : it.next(p, ttb, &sg);
+          if (i == 0 && cut != kWhole && lane == 0) {
+            if (more && !whole) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
             else joins[blockIdx.x].runs = 0;
           }
           if (more) finish_seg(p, tt, ttb, &sg); else sg.n = -1;
@@ -1594,14 +1655,35 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
   //  - for long sequences with many items (deepest first, a head's K and V in L2): 32,768 tokens 6.1 against
   //    6.5 ms;
   //  - for gathered items, all of the same tiles, where their rounding up to the SMs costs less than the join.
+  // The second rule goes by the mean of the keys. Where they have a shared part it is kept to prompts as a whole: chunks
+  // can be as unlike as the caches before them (16 heads: prompts 2 x 1,024 33 against 47, of 100, 2,000 and 700 62 / 61;
+  // chunks of 4 x 512 over 2,000 keys each 51 / 65, but 8 x 256 over a cache of 5,000 and seven of 300 101 / 49).
+  // Over pages only the device knows the lengths; what the table holds bounds a sequence's (whole items / runs):
+  //  - few tiles at most, up to one item per SM: pages of 16, 16 decode steps of 900 keys 18.5 / 26.6, 4 of 100 10.3 /
+  //    14.4 (two items per SM, of 1,000 keys and, the others, 50: 31 / 24.5);
+  //  - perhaps long: kByLengths, pages of 64. 8 chunks of 1,024 rows over 30,000 keys 2,740 / 3,080 to 3,510, over 8,192
+  //    749 / 782, 2 x 4,096 over 60,000 5,320 / 5,870; but prompts 64 x 256 184 / 136, 128 x 100 176 / 92, 16 x 2,048 686
+  //    / 598, and lengths of 1,000 to 30,000 side by side (the longest more than twice their mean) 1,597 / 1,393;
+  //  - token by token (kPagedTokens) never: 8 x 1,024 over 20,000 keys 5,750 / 5,600, 128 x 100 238 / 158.
   const int64_t nt = (p.width + C::kTileKeys - 1) / C::kTileKeys;
   const bool even = LISTED && (nt + 2) * ((items + sms - 1) / sms) <= items * nt / sms + 5;
-  const bool small = !p.list && (even || ((LISTED ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
-  const bool like = F == kTwo && (!C::SHARED || p.T == p.R) && items >= sms && 2 * items <= 5 * sms && p.T <= int64_t(kAttnLikeKeys) * p.S;
-  const bool deep = C::TWO && items >= int64_t(kAttnDirectItems) * sms && p.T >= int64_t(kAttnDirectKeys) * p.S;
-  const bool direct = !LISTED && (small || like || deep || p.S > kAttnMaxRunSeqs);
+  const int ctas = sms < kAttnMaxRuns ? sms : kAttnMaxRuns;
+  const bool many = C::TWO && items >= int64_t(kAttnDirectItems) * sms;
+  bool small, direct = p.S > kAttnMaxRunSeqs;
+  int cut = kRuns;
+  if constexpr (C::PAGED) {
+    small = items <= sms && attn_page_keys(p) <= kAttnWholeKeys;
+    if (F == kPagedTwo && many && attn_page_keys(p) >= kAttnDirectKeys) cut = kByLengths;
+  } else {
+    small = !p.list && (even || ((LISTED ? p.width : p.T) <= kAttnWholeKeys && items <= 4 * sms));
+    const bool like = F == kTwo && (!C::SHARED || p.T == p.R) && items >= sms && 2 * items <= 5 * sms &&
+                      p.T <= int64_t(kAttnLikeKeys) * p.S;
+    direct = direct || like || (many && p.T >= int64_t(kAttnDirectKeys) * p.S);
+  }
+  direct = !LISTED && (direct || small);
   if (direct && items > INT32_MAX) return cudaErrorInvalidValue;
-  int grid = direct || small ? int(items) : (sms < kAttnMaxRuns ? sms : kAttnMaxRuns);
+  if (direct || small) cut = kWhole;
+  int grid = cut == kWhole ? int(items) : ctas;
   if (LISTED && !small && !p.list) grid = int(run_count(items * nt, grid));
   const int slot_rows = attn_slot_rows(GATHER ? 1 : p.R, p.G, C::kQTiles);
   JoinItem* joins = reinterpret_cast<JoinItem*>(ws + sizeof(WorkspaceHeader) + 256);
@@ -1611,10 +1693,9 @@ cudaError_t launch(const typename Cfg<DK, DV, F>::Params& p, char* ws, cudaStrea
   static std::atomic<uint64_t> ready{0};
   e = allow_dynamic_smem(reinterpret_cast<const void*>(kernel), C::kSmem, &ready);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, tr, p, int(tiles), direct || small ? 1 : 0, part, slot_rows,
-                                                  joins, hdr);
+  kernel<<<grid, C::kThreads, C::kSmem, stream>>>(tq, tk, tv, tr, p, int(tiles), cut, part, slot_rows, joins, hdr);
   e = cudaGetLastError();
-  if (e != cudaSuccess || direct || small || p.list || grid < 2) return e;
+  if (e != cudaSuccess || cut == kWhole || p.list || grid < 2) return e;
   cudaLaunchConfig_t cfg{};
   // many runs to an item: a CTA's warps share its rows; else each has its own
   const bool split = items * (slot_rows <= 64 ? 4 : 16) <= grid;
