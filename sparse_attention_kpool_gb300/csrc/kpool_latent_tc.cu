@@ -760,13 +760,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // CTA x adds up, in the order of the runs, the partial results of the row that item x names, a head or a quarter of one
 // to a warp (Join):
-//   kFewParts   more rows than runs, so that a row is cut into two or three: a head a warp, 16 channels a lane, two parts
-//               at a time;
+//   kFewParts   a head a warp, 16 channels a lane, two parts at a time: enough heads to fill the card, few parts of each;
 //   kSomeParts  a quarter of a head a warp, four channels a lane, eight parts at a time;
-//   kManyParts  few rows, each cut into very many: the 8 warps of a CTA share a quarter, each taking every eighth part.
-// What is read was just written: 131 KB a part of 64 heads, 38 MB for 16 rows over 152 runs, at most.
+//   kManyParts  the 8 warps of a CTA share a quarter, each taking every eighth part: few heads in all, each cut into very many.
+// What is read was just written: 132 KB a part of 64 heads. A row cut by n borders has n + 1 parts, so 152 runs over 16 rows
+// leave 167 of them at most, 22 MB.
 enum Join { kFewParts, kSomeParts, kManyParts };
 constexpr int kSomeBatch = 8;
+
+// By the heads of all rows, which are the warps there are, and a row's parts (us of the whole call, whole caches of 300,000
+// tokens in all, or 30,000 a row):
+//   many / some   4 rows of 16 heads 41 / 51, of 32 45 / 52; 8 of 16 64 / 66, of 32 71 / 68, of 64 82 / 70; 4 of 128 74 / 64;
+//                 more than nine rows, less than 16 parts each: 10 of 16 76 / 75, 20 of 16 81 / 73;
+//   some / few    9 rows of 64 heads 77 / 82, 20 of 32 79 / 79, 32 of 16 73 / 75; 16 of 64 83 / 82, 48 of 32 80 / 77, 76 of 64 92
+//                 / 79, 48 of 128 142 / 126; 200 of 16 78 / 73, of 4 70 / 71.
+inline Join join_form(int64_t rows, int32_t heads, int runs) {
+  if (rows * heads >= 768) return kFewParts;
+  return rows * heads <= 192 && rows * 2 * kSomeBatch <= runs ? kManyParts : kSomeParts;
+}
 
 template <Join J>
 __global__ void __launch_bounds__(256)
@@ -901,7 +912,7 @@ cudaError_t launch_latent_tc(const LatentParams& p, char* ws, cudaStream_t strea
   e = cudaGetLastError();
   if (e != cudaSuccess || direct || runs < 2) return e;
   cudaLaunchConfig_t cfg{};
-  const Join join = p.R > runs ? kFewParts : int64_t(p.R) * 2 * kSomeBatch <= runs ? kManyParts : kSomeParts;
+  const Join join = join_form(p.R, p.H, runs);
   const int units = join == kFewParts ? p.H : p.H * (kLatent / 128);
   cfg.gridDim = dim3(uint32_t(p.R <= runs ? p.R : runs), uint32_t(join == kManyParts ? units : (units + 7) / 8));
   cfg.blockDim = dim3(256);
