@@ -727,6 +727,7 @@ _latent_prompt_args = _Args(_HEADS, _HEADS, _HEADS, _HEADS, _HEADS, (kpool_laten
 _ROTARY_PART = (kpool_rotary_part, "QqqQqqiiii")
 _rotary_args = _Args(_ROTARY_PART, _ROTARY_PART, (kpool_rotary_shape, "iii"))
 _LAST = "the last dimension of a tensor must be contiguous"
+_MANY = "pages, tokens of a page, entries of a table or list and sequences are below 2^31"  # (ctypes would drop the bits)
 
 
 def _current_device(dev: int) -> int:
@@ -808,6 +809,8 @@ def kpool_attention_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pag
     S, ts = lengths.numel(), page_table.shape
     if len(ts) != 2 or ts[0] != S or (R != S if cu_q is None else cu_q.numel() != S + 1):
         raise ValueError("page_table is [sequences, pages], lengths [sequences], cu_q [sequences + 1] (or a row each)")
+    if (pages | size | S | ts[1]) >> 31:
+        raise ValueError(_MANY)
     out, out_lse = _results(R, hq, d, q, out, return_lse, out_lse, stream)
     if workspace is None:
         workspace = _new(lambda: new_attention_workspace(R, S, hq, hkv, d, dtype, q.device), stream, returned=False)
@@ -877,6 +880,8 @@ def kpool_attention_latent_prompt(q: torch.Tensor, k: torch.Tensor, k_rotary: to
     if code is None:
         raise TypeError(f"q, k, v must be bfloat16 or float32, got {dtype}")
     S = cu_k.numel() - 1
+    if S >= 1 << 31:
+        raise ValueError(_MANY)
     out, out_lse = _results(R, h, dv, q, out, return_lse, out_lse, stream)
     if workspace is None:
         workspace = _new(lambda: new_latent_prompt_workspace(R, S, h, dn, dr, dv, dtype, q.device), stream,
@@ -928,6 +933,8 @@ def kpool_attention_latent(q: torch.Tensor, cache: torch.Tensor, page_table: tor
         if token_ids.dim() != 2 or token_ids.shape[0] != R:
             raise ValueError("token_ids is [rows, width]")
         width = token_ids.shape[1]
+    if (pages | size | S | ts[1] | max(width, 0)) >> 31:
+        raise ValueError(_MANY)
     out, out_lse = _results(R, h, latent_dim, q, out, return_lse, out_lse, stream)
     if workspace is None:
         workspace = _new(lambda: new_latent_workspace(R, S, h, latent_dim, dim - latent_dim, dtype, q.device), stream,
