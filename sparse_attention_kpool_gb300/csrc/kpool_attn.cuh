@@ -187,16 +187,15 @@ __host__ __device__ __forceinline__ int attn_seq_of_tile(const P& p, int tile, i
   return lo;
 }
 
-// Sequence and first token of tile number `tile` < attn_tiles; the number has no tile where the token is negative or
+// Sequence of tile number `tile` < attn_tiles, and its first token there; the number has no tile where that is negative or
 // not one of the sequence's.
-struct TilePlace {
-  int b, tok0;
-};
 template <bool kRows, class P>
-__host__ __device__ __forceinline__ TilePlace attn_tile_place(const P& p, int tile, int tt) {
-  if (kRows) return {tile, 0};
-  const int b = attn_seq_of_tile(p, tile, tt);
-  return {b, (tile - (attn_q0(p, b) / tt + b)) * tt};
+__host__ __device__ __forceinline__ int attn_tile_seq(const P& p, int tile, int tt) {
+  return kRows ? tile : attn_seq_of_tile(p, tile, tt);
+}
+template <bool kRows, class P>
+__host__ __device__ __forceinline__ int attn_tile_token(const P& p, int b, int tile, int tt) {
+  return kRows ? 0 : (tile - (attn_q0(p, b) / tt + b)) * tt;
 }
 
 // The header's error word, first and last: one thread clears it at the start of the call, and one warp

@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(kGroupThreads* kGroups, kGroups == 4 ? 2 : 1)
     ids = p.ids + int64_t(r) * p.width;
     end = sq.nk > 0 ? p.width : 0;
   } else {
-    const TilePlace at = attn_tile_place<false>(p, blockIdx.x, tt);
-    sq = attn_seq(p, at.b);
-    i0 = at.tok0;
+    const int b = attn_tile_seq<false>(p, blockIdx.x, tt);
+    sq = attn_seq(p, b);
+    i0 = attn_tile_token<false>(p, b, blockIdx.x, tt);
     if (i0 < 0 || i0 >= sq.nq) {
       __syncwarp();
       if (checks && threadIdx.x < 32) attn_check(p, hdr);

@@ -346,9 +346,9 @@ enum Cut { kRuns, kWhole, kByLengths };
 template <bool kRows, class P>
 __device__ __forceinline__ bool whole_seg(const P& p, int ttb, int tiles, Seg* s) {
   s->hk = blockIdx.x / tiles;
-  const TilePlace at = attn_tile_place<kRows>(p, tiles - 1 - int(blockIdx.x % tiles), ttb);
-  s->sq = attn_seq(p, at.b);
-  s->tok0 = at.tok0;
+  const int tile = tiles - 1 - int(blockIdx.x % tiles), b = attn_tile_seq<kRows>(p, tile, ttb);
+  s->sq = attn_seq(p, b);
+  s->tok0 = attn_tile_token<kRows>(p, b, tile, ttb);
   if (s->tok0 < 0 || s->tok0 >= s->sq.nq) return false;
   s->kt0 = 0;
   s->n = tile_cost(p, s->sq, s->tok0 / ttb, ttb);
@@ -669,6 +669,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
   constexpr int kTileKeys = C::kTileKeys, kPCol = C::kPCol;
   constexpr bool TWO = C::TWO, GATHER = C::GATHER, DENSE = F == kDense, PAGED = C::PAGED, TOKENS = C::TOKENS,
                  LISTED = F == kGather, ROWS = F == kPagedRows;
+  // runs, or by the lengths (which only kPagedTwo goes by)
+  const bool in_runs = F == kPagedTwo ? cut != kWhole : cut == kRuns;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;
@@ -695,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
   // dense form: with nothing but finite values there is nothing to clean
   const bool no_cleaning = GATHER || (DENSE && p.dense->finite);
   if (DENSE && !p.dense->enabled) {  // the gathering kernel does all rows
-    if (threadIdx.x == 0 && cut != kWhole) joins[blockIdx.x].runs = 0;
+    if (threadIdx.x == 0 && in_runs) joins[blockIdx.x].runs = 0;
     return;
   }
   if constexpr (LISTED) {
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       misc->lo = lo;
       misc->hi = hi;
     }
-  } else if (cut != kWhole) {
+  } else if (in_runs) {
     find_run(p, ttb, reinterpret_cast<int64_t*>(smem), blockIdx.x, gridDim.x, cut, misc);
     ptx::fence_proxy_async_smem();  // the scratch lies where TMA writes next
   }
@@ -760,15 +762,15 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       if (lane == 0) {  // ---------------------------------------------- segments and Q tiles
         int64_t pos = LISTED ? misc->lo : 0;
         SegIter it;
-        if (!LISTED && cut == kRuns) it.start(p, misc, ttb);
+        if (!LISTED && in_runs) it.start(p, misc, ttb);
         uint32_t q_loads = 0;
         Seg sg{};
         for (int i = 0;; ++i) {
           const int64_t at = pos;
           bool more;
           if constexpr (LISTED) more = gather_seg(p, &pos, misc->hi, &sg);
-          else more = cut == kWhole ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
-          if (i == 0 && cut != kWhole && !p.list) {  // (else whole items: nothing to join)
+          else more = !in_runs ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg) : it.next(p, ttb, &sg);
+          if (i == 0 && in_runs && !p.list) {  // (else whole items: nothing to join)
             if (!more) joins[blockIdx.x].runs = 0;
             else if constexpr (LISTED)
               write_join(joins + blockIdx.x, sg, at - sg.kt0, gather_tiles(p), gather_total(p), blockIdx.x, gridDim.x);
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
       if (PAGED || lane == 0) {
         SegIter it;
         if (whole) it.start_whole(whole);
-        else if (cut != kWhole) it.start(p, misc, ttb);
+        else if (in_runs) it.start(p, misc, ttb);
         uint32_t fills[2] = {0, 0}, q_loads = 0;  // of the ring, or of K's and V's
         bool ok = true, bad_page = false;
         Seg sg{};
@@ -959,10 +961,10 @@ __global__ void __launch_bounds__(Cfg<DK, DV, F>::kThreads, 1)
           return true;
         };
         for (int i = 0;; ++i) {
-          const bool more = cut == kWhole ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg)
-                            : whole       ? it.next_whole(p, ttb, &sg)
-                                          : it.next(p, ttb, &sg);
-          if (i == 0 && cut != kWhole && lane == 0) {
+          const bool more = !in_runs ? i == 0 && whole_seg<ROWS>(p, ttb, tiles, &sg)
+                            : whole  ? it.next_whole(p, ttb, &sg)
+                                     : it.next(p, ttb, &sg);
+          if (i == 0 && in_runs && lane == 0) {
             if (more && !whole) write_join(joins + blockIdx.x, sg, it.first_tile(), it.c, misc->total, blockIdx.x, misc->runs);
             else joins[blockIdx.x].runs = 0;
           }

@@ -14,8 +14,8 @@ void print(const P& p, int tt) {
   const int tiles = int(attn_tiles<kRows>(p.R, p.S, tt));
   std::printf("%d", tiles);
   for (int t = 0; t < tiles; ++t) {
-    const TilePlace at = attn_tile_place<kRows>(p, t, tt);
-    std::printf(" %d %d", at.b, at.tok0);
+    const int b = attn_tile_seq<kRows>(p, t, tt);
+    std::printf(" %d %d", b, attn_tile_token<kRows>(p, b, t, tt));
   }
   std::printf("\n");
 }
