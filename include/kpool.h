@@ -507,9 +507,11 @@ kpool_status kpool_attention_latent(const kpool_heads* q, const kpool_pages* cac
  * with KPOOL_ROTARY_INVERSE x = -t f[i] (which, with the same magnitude, is the gradient's way back, too). The
  * rotated channels are [offset, offset + rotary_dim) of each head; pair i is channels i and i + rotary_dim / 2 of
  * them, or with KPOOL_ROTARY_INTERLEAVED channels 2 i and 2 i + 1. The other channels are copied. Products
- * and sums are in fp32, rounded once; angles are exact to 2^-24 of a half turn at any position.
- *   in, out    [tokens, heads, head_dim], any token and head strides (multiples of the element; 16-byte aligned
- *              ones are faster); out is in itself (same strides), or overlaps no input
+ * and sums are in fp32, rounded once; angles are exact to 2^-24 of a half turn at any position (by a table of
+ * kpool_rotary_table, whose entries are right to a few units).
+ *   in, out    [tokens, heads, head_dim], any token and head strides (multiples of the element; faster where those of
+ *              q and k, their bases, head_dim and offset are all multiples of 16 bytes); out is in itself (same
+ *              strides), or overlaps no input
  *   positions  [tokens] int32 (device), any value
  *   table      [rotary_dim / 2] int64 (device): f[i] in turns a token, a fraction in units of 2^-64
  * q and k (NULL: none) are two tensors of the same tokens, each with sizes of its own.

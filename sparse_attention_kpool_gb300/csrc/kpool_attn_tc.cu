@@ -36,13 +36,13 @@
 // Over pages, decode steps of the same sizes: 132 us, 6.0 TB/s in the kernel (kPagedRows).
 // Keys with a shared part (192 channels, values of 128): a turn's products are 18 instructions in 1,470
 // cycles (P V 75 each, Q K^T at N = 96 80: operands from shared memory), two groups 2,915 a pair of tiles of
-// 96 keys; 16,384 tokens of 32 heads: 2.03 ms = 1.35 PFLOP/s.
+// 96 keys; 16,384 tokens of 32 heads: 2.03 ms = 1.35 PFLOP/s (2.10 with new inputs in every call).
 //
 // Running maximum. O is rescaled only when a row's maximum has grown by more than 8 in the
 // exponent: weights then reach at most 2^8, which costs neither bf16 nor fp32 any precision,
 // and the rescale (a pass over O in TMEM) becomes rare. P is rounded to bf16 (half a step is
 // 2^-8 of a weight) because the second product takes bf16; the row sum adds the weights before
-// that rounding, in fp32.
+// that rounding, in fp32. Exponentials are the hardware's (2 ulp).
 //
 // Masked places. A key that a row does not see gets s = -inf, so what K holds there does not
 // matter. A weight of zero does not silence V, though (0 * NaN): in the tiles that some row

@@ -20,15 +20,16 @@
 // What bounds it. Of a tile (74 KB; 3,100 cycles of an SM's share of the measured copy rate at 1.9 GHz) the products
 // take 2,470 cycles at 64 heads: operands from shared memory come at about 90 bytes a cycle, 36 x 4 KB in 1,390 and 16 x
 // 6 KB in 1,080. The softmax between them (860, of which exponentials and stores are 550) and the handing over (150 +
-// 200) are hidden only where the next tile has landed in time: two tiles are what fits beside 64 heads of Q.
-//   - 32 sequences of 64 heads, 389,566 tokens (449 MB): 104 us, of it 88 the tiles (5.1 TB/s, 3,900 cycles each: a tile
-//     takes 2,800 from HBM, so its scores wait for it) and 10 the join;
+// 200) are hidden only where the next tile has landed in time: two tiles are what fits beside 64 heads of Q (whose space is
+// that of 64 heads in every call; beside 32 a third tile would fit).
+//   - 32 sequences of 64 heads, 389,566 tokens (449 MB): 101 us, of it 88 the tiles (5.1 TB/s, 3,900 cycles each: a tile
+//     takes 2,800 from HBM, so its scores wait for it), the rest the join;
 //   - 512 rows x 2,052 ids of 128 heads (2.3 GB out of L2): 390 us, 2,850 cycles a tile, the tensor core 87 % of them.
 //
 // Masked places: tokens that are not seen are written as zeros (no infinity meets a weight of zero) and
 // score -inf. P is rounded to bf16 (half a step is 2^-8 of a weight) because the second product takes
-// bf16; the row sum adds the weights before that rounding, in fp32. O is rescaled only when a maximum has
-// grown by more than 8 in the exponent, as in kpool_attn_tc.cu.
+// bf16; the row sum adds the weights before that rounding, in fp32. Exponentials are the hardware's (2 ulp). O is rescaled
+// only when a maximum has grown by more than 8 in the exponent, as in kpool_attn_tc.cu.
 //
 // Work. A run per CTA (per group of CTAs, above 64 heads) of about equally many tiles, found by every CTA itself
 // from the lengths on the device; unfinished rows go to the workspace as (m, l, O) and a second kernel joins
