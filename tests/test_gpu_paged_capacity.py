@@ -50,23 +50,25 @@ def test_long_sequences(q_lens, lengths, heads):
 
 
 def test_long_sequences_with_bad_lengths_and_pages():
-    heads, page, q_lens, lengths = (32, 8, 128), 64, [1024, 1024, 1024], [9000, 9000, 9000]
+    """Long enough without the bad one that the call still takes whole row tiles by its lengths."""
+    heads, page, n, lengths = (128, 1, 64), 64, 1030, [14000, 14000, 14000]
+    q_lens, rows = [n] * 3, 3 * n
     total, table = S.pool(lengths, page, random.Random(5))
-    q, k, v = make(5, 3072, total, page, heads, BF)
-    ws = K.new_attention_workspace(3072, 3, *heads, BF)
+    q, k, v = make(5, rows, total, page, heads, BF)
+    ws = K.new_attention_workspace(rows, 3, *heads, BF)
     see = S.see_paged(table, lengths, page, q_lens)
-    pick = list(range(0, 1024, 97)) + list(range(2048, 3072, 97))
+    pick = list(range(0, n, 97)) + list(range(2 * n, rows, 97))
     ref = S.attend(q[pick], k.flatten(0, 1), v.flatten(0, 1), [see[r] for r in pick], 0.09)
     for what in ("length", "page"):
-        n, t = list(lengths), table.clone()
+        held, t = list(lengths), table.clone()
         if what == "length":
-            n[1] = 2 ** 31 - 1
+            held[1] = 2 ** 31 - 1
         else:
             t[1, 3] = total
         out = torch.full_like(q, math.nan)
-        out, lse = K.kpool_attention_paged(q, k, v, t.cuda(), i32(n), 0.09, cu_q=i32(A.cu(q_lens)), out=out, return_lse=True,
+        out, lse = K.kpool_attention_paged(q, k, v, t.cuda(), i32(held), 0.09, cu_q=i32(A.cu(q_lens)), out=out, return_lse=True,
                                            workspace=ws)
         assert K.kpool_last_device_error(ws) == K.KPOOL_ERR_INVALID_ARG
         A.check(out[pick], lse[pick], ref, what)
         if what == "length":
-            assert (out[1024:2048] == 0).all() and (lse[1024:2048] == -math.inf).all()
+            assert (out[n:2 * n] == 0).all() and (lse[n:2 * n] == -math.inf).all()
